@@ -17,4 +17,8 @@ from .binding import (  # noqa: F401
     CONV_SILU, CONV_NONE, GdnConvParams, GdnConvTensors, gdn_conv_forward, gdn_conv_replay,
     GdnSlots, gdn_forward_pooled, gdn_replay_pooled, gdn_conv_forward_pooled, gdn_conv_replay_pooled,
     gdn_publish_slots, gdn_forward_no_alloc, NO_ALLOC_SCRATCH_BYTES, GdnConvFused, gdn_conv_decode_forward,
+    ROPE_HALF, ROPE_INTERLEAVED, ROPE_SCALING_NONE, ROPE_SCALING_LINEAR, ROPE_SCALING_NTK, ROPE_SCALING_YARN,
+    CACHE_IO, CACHE_E4M3, GdnKvCache, GdnRopeParams, GdnRopeTensors, GdnKvParams, GdnKvTensors, GdnAttnParams,
+    GdnAttnTensors, KVCache, gdn_rope_frequencies, gdn_rope_forward, gdn_kv_write, gdn_kv_read,
+    gdn_attn_workspace_bytes, gdn_attn_forward,
 )

@@ -1,5 +1,5 @@
-"""ctypes binding of the C ABI in include/gdn.h, include/gdn_conv.h and
-include/gdn_pool.h (same entry-point names).
+"""ctypes binding of the C ABI in include/gdn.h, include/gdn_conv.h,
+include/gdn_pool.h and include/gdn_attn.h (same entry-point names).
 
 Tensors are torch tensors on the current HIP device; torch only provides the
 device memory and the stream. Shapes are read from the tensors, checked for
@@ -25,6 +25,9 @@ GATE_RAW, GATE_NONE = 0, 1
 STATE_V_MAJOR, STATE_K_MAJOR = 0, 1
 ABI_VERSION = 7          # the struct layouts below match this version of include/gdn.h
 CONV_SILU, CONV_NONE = 0, 1
+ROPE_HALF, ROPE_INTERLEAVED = 0, 1
+ROPE_SCALING_NONE, ROPE_SCALING_LINEAR, ROPE_SCALING_NTK, ROPE_SCALING_YARN = 0, 1, 2, 3
+CACHE_IO, CACHE_E4M3 = 0, 1
 
 
 class LibraryNotBuilt(RuntimeError):
@@ -76,6 +79,45 @@ class GdnSlots(ctypes.Structure):
     _fields_ = [("num_slots", ctypes.c_int32), ("read_slots", ctypes.c_void_p),
                 ("write_slots", ctypes.c_void_p), ("read_slots_host", ctypes.c_void_p),
                 ("write_slots_host", ctypes.c_void_p)]
+
+
+class GdnKvCache(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k_pages", "v_pages", "k_scales", "v_scales", "page_table",
+                                               "page_table_host")] + \
+               [(n, ctypes.c_int32) for n in ("num_pages", "page_size", "max_pages", "num_kv_heads", "head_dim",
+                                              "io_dtype", "format")]
+
+
+class GdnRopeParams(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("num_tokens", "num_q_heads", "num_k_heads", "head_dim", "io_dtype",
+                                              "rotary_dim", "layout")] + \
+               [("factor", ctypes.c_float), ("q_stride", ctypes.c_int32), ("k_stride", ctypes.c_int32)]
+
+
+class GdnRopeTensors(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("q", "k", "positions", "inv_freq", "q_out", "k_out")]
+
+
+class GdnKvParams(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("num_tokens", "num_reqs", "num_q_heads", "rotary_dim",
+                                              "rope_layout")] + \
+               [("rope_factor", ctypes.c_float)] + \
+               [(n, ctypes.c_int32) for n in ("q_stride", "k_stride", "v_stride")]
+
+
+class GdnKvTensors(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k", "v", "cu_seqlens", "cu_seqlens_host", "seq_lens",
+                                               "seq_lens_host", "q", "q_out", "positions", "inv_freq")]
+
+
+class GdnAttnParams(ctypes.Structure):
+    _fields_ = [("num_tokens", ctypes.c_int32), ("num_reqs", ctypes.c_int32), ("num_q_heads", ctypes.c_int32),
+                ("scale", ctypes.c_float), ("window", ctypes.c_int32), ("q_stride", ctypes.c_int32)]
+
+
+class GdnAttnTensors(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("q", "cu_seqlens", "cu_seqlens_host", "seq_lens", "seq_lens_host",
+                                               "output")]
 
 
 _lib = None
@@ -135,6 +177,17 @@ def lib() -> ctypes.CDLL:
         L.gdn_conv_decode_forward.restype = ctypes.c_int
         L.gdn_publish_slots.argtypes = [i32, vp, vp, vp]
         L.gdn_publish_slots.restype = ctypes.c_int
+        dbl, cp = ctypes.c_double, ctypes.POINTER(GdnKvCache)
+        L.gdn_rope_frequencies.argtypes = [i32, dbl, i32, dbl, dbl, dbl, dbl, vp, ctypes.POINTER(ctypes.c_float)]
+        L.gdn_rope_forward.argtypes = [ctypes.POINTER(GdnRopeParams), ctypes.POINTER(GdnRopeTensors), vp]
+        for fn in (L.gdn_kv_write, L.gdn_kv_read):
+            fn.argtypes = [ctypes.POINTER(GdnKvParams), ctypes.POINTER(GdnKvTensors), cp, vp]
+        L.gdn_attn_forward.argtypes = [ctypes.POINTER(GdnAttnParams), ctypes.POINTER(GdnAttnTensors), cp, vp,
+                                       ctypes.c_size_t, vp]
+        L.gdn_attn_workspace_bytes.argtypes = [ctypes.POINTER(GdnAttnParams), cp, ctypes.POINTER(ctypes.c_size_t)]
+        for fn in (L.gdn_rope_frequencies, L.gdn_rope_forward, L.gdn_kv_write, L.gdn_kv_read, L.gdn_attn_forward,
+                   L.gdn_attn_workspace_bytes):
+            fn.restype = ctypes.c_int
         L.gdn_strerror.argtypes = [ctypes.c_int]
         L.gdn_strerror.restype = ctypes.c_char_p
         L.gdn_abi_version.argtypes = []
@@ -675,4 +728,267 @@ def gdn_publish_slots(committed_slots, inactive_slots, *, stream=None, check: bo
     st = lib().gdn_publish_slots(R, _ptr(committed_slots), _ptr(inactive_slots), _stream_handle(stream))
     if check and st != GDN_OK:
         raise GDNError(st, "gdn_publish_slots")
+    return st
+
+
+# ------------------------------------------------- the attention layer (gdn_attn.h)
+class KVCache:
+    """The paged key-value cache of one layer (gdn_kv_cache of include/gdn_attn.h): a
+    description of tensors that the caller owns, made once and passed to every call.
+
+    k_pages, v_pages [num_pages, Hk, page_size, D] float16 or float32; for the 8-bit
+    format float8_e4m3fn or uint8, with k_scales, v_scales [num_pages, Hk, page_size]
+    uint8 (the exponent bytes; I/O is then float16). page_table [R, max_pages] int32;
+    page_table_host an optional host mirror, checked on every call.
+    """
+
+    def __init__(self, k_pages, v_pages, page_table, *, k_scales=None, v_scales=None, page_table_host=None):
+        torch = _torch()
+        if k_pages.dim() != 4 or page_table.dim() != 2:
+            raise ValueError("k_pages must be [num_pages, Hk, page_size, D] and page_table [R, max_pages]")
+        P, Hk, page_size, D = k_pages.shape
+        self.e4m3 = k_scales is not None or v_scales is not None
+        if self.e4m3:
+            if k_scales is None or v_scales is None:
+                raise ValueError("the 8-bit format needs k_scales and v_scales")
+            if k_pages.dtype not in (torch.uint8, torch.float8_e4m3fn):
+                raise ValueError(f"k_pages: dtype {k_pages.dtype} is not an 8-bit cache")
+            _need(k_scales, "k_scales", (P, Hk, page_size), torch.uint8)
+            _need(v_scales, "v_scales", (P, Hk, page_size), torch.uint8)
+            self.io_dtype = torch.float16
+        else:
+            self.io_dtype = k_pages.dtype
+        _need(k_pages, "k_pages", (P, Hk, page_size, D))
+        _need(v_pages, "v_pages", (P, Hk, page_size, D), k_pages.dtype)
+        _need(page_table, "page_table", tuple(page_table.shape), torch.int32)
+        for x, name in ((v_pages, "v_pages"), (page_table, "page_table"), (k_scales, "k_scales"),
+                        (v_scales, "v_scales")):
+            if x is not None and x.device != k_pages.device:
+                raise ValueError(f"{name} is on {x.device}, k_pages on {k_pages.device}")
+        host, host_ptr = _host_i32(page_table_host)
+        if host is not None and host.shape != tuple(page_table.shape):
+            raise ValueError("page_table_host must have page_table's shape")
+        self.num_reqs, max_pages = page_table.shape
+        self.num_kv_heads, self.head_dim, self.device = Hk, D, k_pages.device
+        self._keep = (k_pages, v_pages, k_scales, v_scales, page_table, host)
+        self.struct = GdnKvCache(_ptr(k_pages), _ptr(v_pages), _ptr(k_scales), _ptr(v_scales), _ptr(page_table),
+                                 host_ptr, P, page_size, max_pages, Hk, D, _io_code(self.io_dtype),
+                                 CACHE_E4M3 if self.e4m3 else CACHE_IO)
+        self._ref = ctypes.byref(self.struct)
+
+
+def _token_rows(x, name, heads, D, dtype, device):
+    """Token stride of x [N, heads, D] whose tokens may lie apart (0: dense): a slice of a
+    wider projection's output is taken as it is."""
+    if x.dim() != 3 or x.shape[1] != heads or x.shape[2] != D:
+        raise ValueError(f"{name}: shape {tuple(x.shape)} != expected (N, {heads}, {D})")
+    if x.dtype != dtype:
+        raise ValueError(f"{name}: dtype {x.dtype} != expected {dtype}")
+    if x.device != device:
+        raise ValueError(f"{name} is on {x.device}, expected {device}")
+    if x.is_contiguous():
+        return 0
+    if x.shape[0] > 1 and x.stride(2) == 1 and (heads <= 1 or x.stride(1) == D) and x.stride(0) >= heads * D:
+        return x.stride(0)
+    if x.shape[0] <= 1 and x.stride(2) == 1 and (heads <= 1 or x.stride(1) == D):
+        return 0
+    raise ValueError(f"{name}: only the token dimension may be strided")
+
+
+def _out_rows(out, of, name, heads, D):
+    """An output of the rotation: dense, or `of` itself."""
+    if out is None or out.shape != of.shape or out.dtype != of.dtype or out.device != of.device:
+        raise ValueError(f"{name} must have its input's shape, type and device")
+    if not out.is_contiguous() and not (out.data_ptr() == of.data_ptr() and out.stride() == of.stride()):
+        raise ValueError(f"{name} must be contiguous, or its input itself")
+
+
+def _on_current_device(device):
+    torch = _torch()
+    if device.type != "cuda":
+        raise ValueError("tensors must be GPU tensors")
+    if device.index != torch.cuda.current_device():
+        raise ValueError(f"tensors are on {device}, the current device is cuda:{torch.cuda.current_device()}")
+
+
+def _int_vector(x, name, n, device):
+    torch = _torch()
+    if x is None:
+        return
+    if x.dim() != 1 or x.shape[0] != n or x.dtype != torch.int32 or not x.is_contiguous() or x.device != device:
+        raise ValueError(f"{name} must be a contiguous int32 [{n}] on {device}")
+
+
+def _check_inv_freq(x, device):
+    torch = _torch()
+    if x is None or x.dim() != 1 or x.dtype != torch.float64 or not x.is_contiguous() or x.device != device:
+        raise ValueError(f"inv_freq must be a contiguous float64 [rotary_dim / 2] on {device}")
+
+
+def _cache_rows(cache, seq_lens, cu_seqlens, num_reqs, cu_seqlens_host, seq_lens_host):
+    """(R, host arrays to keep alive, their addresses) of a call over a cache."""
+    R = int(num_reqs) if num_reqs is not None else \
+        cu_seqlens.shape[0] - 1 if cu_seqlens is not None else seq_lens.shape[0]
+    dev = cache.device
+    if R > cache.num_reqs:
+        raise ValueError(f"{R} requests, but page_table has {cache.num_reqs} rows")
+    _int_vector(seq_lens, "seq_lens", R, dev)
+    _int_vector(cu_seqlens, "cu_seqlens", R + 1, dev)
+    cu_h, cu_ptr = _host_i32(cu_seqlens_host)
+    len_h, len_ptr = _host_i32(seq_lens_host)
+    if cu_h is not None and cu_h.shape != (R + 1,):
+        raise ValueError("cu_seqlens_host must have R + 1 entries")
+    if len_h is not None and len_h.shape != (R,):
+        raise ValueError("seq_lens_host must have R entries")
+    _on_current_device(dev)
+    return R, (cu_h, len_h), cu_ptr, len_ptr
+
+
+def gdn_rope_frequencies(rotary_dim: int, *, base: float = 10000.0, scaling: int = ROPE_SCALING_NONE,
+                         scale: float = 1.0, trained_length: float = 0.0, beta_fast: float = 0.0,
+                         beta_slow: float = 0.0):
+    """gdn_rope_frequencies of include/gdn_attn.h: (inv_freq, a float64 numpy array
+    [rotary_dim / 2], the factor of cos and sin)."""
+    import numpy as np
+    out = np.empty(max(int(rotary_dim) // 2, 1), np.float64)
+    factor = ctypes.c_float(0.0)
+    st = lib().gdn_rope_frequencies(int(rotary_dim), float(base), int(scaling), float(scale), float(trained_length),
+                                    float(beta_fast), float(beta_slow), out.ctypes.data, ctypes.byref(factor))
+    if st != GDN_OK:
+        raise GDNError(st, "gdn_rope_frequencies")
+    return out, float(factor.value)
+
+
+def gdn_rope_forward(q, k, positions, inv_freq, q_out, k_out, *, rope_layout: int = ROPE_HALF,
+                     rope_factor: float = 1.0, stream=None, check: bool = True) -> int:
+    """gdn_rope_forward of include/gdn_attn.h on torch tensors; returns the status.
+
+    q [N, Hq, D] and k [N, Hk, D] float16 or float32 (either may be None; the token
+    dimension may be strided), positions [N] int32, inv_freq [rotary_dim / 2] float64;
+    q_out, k_out dense, or q, k themselves.
+    """
+    x = q if q is not None else k
+    if x is None:
+        raise ValueError("q or k is needed")
+    N, _, D = x.shape
+    dev, io = x.device, x.dtype
+    Hq, Hk = (0 if y is None else y.shape[1] for y in (q, k))
+    strides = [0, 0]
+    for i, (y, out, name) in enumerate(((q, q_out, "q"), (k, k_out, "k"))):
+        if y is not None:
+            if y.shape[0] != N:
+                raise ValueError("q and k must have the same tokens")
+            strides[i] = _token_rows(y, name, y.shape[1], D, io, dev)
+            _out_rows(out, y, name + "_out", y.shape[1], D)
+    _int_vector(positions, "positions", N, dev)
+    _check_inv_freq(inv_freq, dev)
+    _on_current_device(dev)
+    params = GdnRopeParams(N, Hq, Hk, D, _io_code(io), 2 * inv_freq.shape[0], int(rope_layout), float(rope_factor),
+                           strides[0], strides[1])
+    tens = GdnRopeTensors(_ptr(q), _ptr(k), _ptr(positions), _ptr(inv_freq), _ptr(q_out) if q is not None else None,
+                          _ptr(k_out) if k is not None else None)
+    st = lib().gdn_rope_forward(ctypes.byref(params), ctypes.byref(tens), _stream_handle(stream))
+    if check and st != GDN_OK:
+        raise GDNError(st, "gdn_rope_forward")
+    return st
+
+
+def gdn_kv_write(k, v, cache: KVCache, seq_lens, cu_seqlens=None, *, q=None, q_out=None, inv_freq=None,
+                 positions=None, rope_layout: int = ROPE_HALF, rope_factor: float = 1.0,
+                 num_reqs: Optional[int] = None, cu_seqlens_host=None, seq_lens_host=None, stream=None,
+                 check: bool = True) -> int:
+    """gdn_kv_write of include/gdn_attn.h on torch tensors; returns the status.
+
+    k, v [N, Hk, D] in the cache's I/O type (the token dimension may be strided);
+    seq_lens [R] int32, the cached tokens with these included; cu_seqlens [R + 1] int32
+    or None for N / R tokens each. With inv_freq [rotary_dim / 2] float64 k is rotated
+    as it is written, and q [N, Hq, D], when given, into q_out; positions [N] int32
+    default to the positions in the cache.
+    """
+    Hk, D, dev, io = cache.num_kv_heads, cache.head_dim, cache.device, cache.io_dtype
+    N = k.shape[0]
+    ks, vs = _token_rows(k, "k", Hk, D, io, dev), _token_rows(v, "v", Hk, D, io, dev)
+    if v.shape[0] != N:
+        raise ValueError("k and v must have the same tokens")
+    Hq = qs = rot = 0
+    if inv_freq is not None:
+        _check_inv_freq(inv_freq, dev)
+        rot = 2 * inv_freq.shape[0]
+        _int_vector(positions, "positions", N, dev)
+        if q is not None:
+            Hq = q.shape[1]
+            qs = _token_rows(q, "q", Hq, D, io, dev)
+            if q.shape[0] != N:
+                raise ValueError("q and k must have the same tokens")
+            _out_rows(q_out, q, "q_out", Hq, D)
+    elif q is not None or positions is not None:
+        raise ValueError("q and positions go with a rotation (inv_freq)")
+    R, keep, cu_ptr, len_ptr = _cache_rows(cache, seq_lens, cu_seqlens, num_reqs, cu_seqlens_host, seq_lens_host)
+    params = GdnKvParams(N, R, Hq, rot, int(rope_layout), float(rope_factor), qs, ks, vs)
+    tens = GdnKvTensors(_ptr(k), _ptr(v), _ptr(cu_seqlens), cu_ptr, _ptr(seq_lens), len_ptr, _ptr(q),
+                        _ptr(q_out) if q is not None else None, _ptr(positions), _ptr(inv_freq))
+    st = lib().gdn_kv_write(ctypes.byref(params), ctypes.byref(tens), cache._ref, _stream_handle(stream))
+    del keep
+    if check and st != GDN_OK:
+        raise GDNError(st, "gdn_kv_write")
+    return st
+
+
+def gdn_kv_read(k, v, cache: KVCache, seq_lens, cu_seqlens=None, *, num_reqs: Optional[int] = None,
+                cu_seqlens_host=None, seq_lens_host=None, stream=None, check: bool = True) -> int:
+    """gdn_kv_read of include/gdn_attn.h: the newest T_r of every request's seq_lens[r]
+    cached tokens into k, v [N, Hk, D] (dense, the cache's I/O type); returns the status."""
+    Hk, D, dev, io = cache.num_kv_heads, cache.head_dim, cache.device, cache.io_dtype
+    N = k.shape[0]
+    if v.shape[0] != N or not k.is_contiguous() or not v.is_contiguous():
+        raise ValueError("k and v must be contiguous and have the same tokens")
+    _token_rows(k, "k", Hk, D, io, dev)
+    _token_rows(v, "v", Hk, D, io, dev)
+    R, keep, cu_ptr, len_ptr = _cache_rows(cache, seq_lens, cu_seqlens, num_reqs, cu_seqlens_host, seq_lens_host)
+    params = GdnKvParams(N, R, 0, 0, 0, 0.0, 0, 0, 0)
+    tens = GdnKvTensors(_ptr(k), _ptr(v), _ptr(cu_seqlens), cu_ptr, _ptr(seq_lens), len_ptr, None, None, None, None)
+    st = lib().gdn_kv_read(ctypes.byref(params), ctypes.byref(tens), cache._ref, _stream_handle(stream))
+    del keep
+    if check and st != GDN_OK:
+        raise GDNError(st, "gdn_kv_read")
+    return st
+
+
+def gdn_attn_workspace_bytes(N: int, R: int, Hq: int, cache: KVCache) -> int:
+    """Workspace bytes gdn_attn_forward needs for these sizes, whatever the lengths."""
+    params = GdnAttnParams(int(N), int(R), int(Hq), 0.0, 0, 0)
+    out = ctypes.c_size_t(0)
+    st = lib().gdn_attn_workspace_bytes(ctypes.byref(params), cache._ref, ctypes.byref(out))
+    if st != GDN_OK:
+        raise GDNError(st, "gdn_attn_workspace_bytes")
+    return int(out.value)
+
+
+def gdn_attn_forward(q, cache: KVCache, seq_lens, cu_seqlens, output, *, scale: float = 0.0, window: int = 0,
+                     num_reqs: Optional[int] = None, cu_seqlens_host=None, seq_lens_host=None, workspace=None,
+                     stream=None, check: bool = True) -> int:
+    """gdn_attn_forward of include/gdn_attn.h on torch tensors; returns the status.
+
+    q [N, Hq, D] in the cache's I/O type (the token dimension may be strided), output
+    [N, Hq, D] dense; seq_lens [R] int32; cu_seqlens [R + 1] int32 or None for N / R
+    tokens each; workspace a uint8 GPU tensor of gdn_attn_workspace_bytes().
+    """
+    D, dev, io = cache.head_dim, cache.device, cache.io_dtype
+    N, Hq = q.shape[0], q.shape[1]
+    qs = _token_rows(q, "q", Hq, D, io, dev)
+    if output.shape != q.shape or output.dtype != io or not output.is_contiguous() or output.device != dev:
+        raise ValueError("output must be contiguous and have q's shape, type and device")
+    ws_ptr, ws_bytes = None, 0
+    if workspace is not None:
+        if workspace.device != dev or not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous tensor on the cache's GPU")
+        ws_ptr, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    R, keep, cu_ptr, len_ptr = _cache_rows(cache, seq_lens, cu_seqlens, num_reqs, cu_seqlens_host, seq_lens_host)
+    params = GdnAttnParams(N, R, Hq, float(scale), int(window), qs)
+    tens = GdnAttnTensors(q.data_ptr(), _ptr(cu_seqlens), cu_ptr, _ptr(seq_lens), len_ptr, output.data_ptr())
+    st = lib().gdn_attn_forward(ctypes.byref(params), ctypes.byref(tens), cache._ref, ws_ptr, ws_bytes,
+                                _stream_handle(stream))
+    del keep
+    if check and st != GDN_OK:
+        raise GDNError(st, "gdn_attn_forward")
     return st

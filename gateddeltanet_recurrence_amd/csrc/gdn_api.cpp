@@ -17,25 +17,18 @@
 #include <utility>
 #include <vector>
 
+#include "gdn_host.h"
 #include "gdn_kernels.h"
 
 namespace {
 
+using gdn::Span;
+using gdn::aligned16;
+using gdn::io_bytes;
+
 constexpr int kRecurrentMaxLenForAuto = 32;
 
 bool supported_dim(int d) { return d == 16 || d == 32 || d == 64 || d == 128; }
-
-size_t io_bytes(int dtype) { return dtype == GDN_F16 ? 2 : 4; }
-
-struct Span {
-  uintptr_t lo = 0, hi = 0;  // [lo, hi); empty when lo == hi
-  Span() = default;
-  Span(const void* p, size_t bytes) : lo(reinterpret_cast<uintptr_t>(p)), hi(lo + (p ? bytes : 0)) {}
-  bool empty() const { return lo == hi; }
-  bool overlaps(const Span& o) const { return !empty() && !o.empty() && lo < o.hi && o.lo < hi; }
-};
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // Checks shared by every forward entry point; fills the resolved values.
 struct Resolved {
