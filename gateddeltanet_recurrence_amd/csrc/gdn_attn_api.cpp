@@ -75,7 +75,8 @@ int check_cache(const gdn_kv_cache* c, bool pointers) {
   if (c->k_pages == nullptr || c->v_pages == nullptr || c->page_table == nullptr) return GDN_ERR_NULL;
   if (e4m3 && (c->k_scales == nullptr || c->v_scales == nullptr)) return GDN_ERR_NULL;
   if (!e4m3 && (c->k_scales != nullptr || c->v_scales != nullptr)) return GDN_ERR_SHAPE;
-  if (!aligned16(c->k_pages) || !aligned16(c->v_pages)) return GDN_ERR_SHAPE;
+  for (const void* ptr : {c->k_pages, c->v_pages, (void*)c->k_scales, (void*)c->v_scales})
+    if (ptr != nullptr && !aligned16(ptr)) return GDN_ERR_SHAPE;
   return GDN_OK;
 }
 

@@ -24,7 +24,7 @@
  * all work is asynchronous on `stream` and can be captured in a HIP graph, and
  * the status codes are gdn_status. "io" is the element type named by io_dtype,
  * GDN_F16 or GDN_F32 (BF16 is rejected). Device pointers are 16-byte aligned
- * unless they are int32 or uint8 arrays.
+ * unless they are int32 arrays.
  */
 #ifndef GDN_ATTN_H_
 #define GDN_ATTN_H_

@@ -138,6 +138,7 @@ def test_e4m3_needs_scales_and_fp16(call):
     f = Fields(e4m3=True)
     assert call(f, _cache(f, e4m3=True, k_scales=None)) == gdn.GDN_ERR_NULL
     assert call(f, _cache(f, e4m3=True, io_dtype=gdn.GDN_F32)) == gdn.GDN_ERR_DTYPE
+    assert call(f, _cache(f, e4m3=True, v_scales=f.v_scales + 8)) == gdn.GDN_ERR_SHAPE       # alignment
 
 
 @pytest.mark.parametrize("call", ALL)
