@@ -21,14 +21,21 @@
 //  - v is loaded in rows too: a lane holds the same few columns of 8 positions and
 //    turns them into columns with byte permutes (half an instruction an element).
 //
+// Rows come in tiles of 16, and a workgroup takes up to 4 tiles of a request and key
+// head: with one tile its 4 waves take alternate positions, with two tiles 2 waves
+// each, with more one wave each. Waves of different tiles then read the same keys and
+// values at the same time, through one CU's L1, so HBM is read once for up to 64 rows.
+//
 // Work is split evenly over the workgroups whatever the lengths: the positions of
-// every (request, 16-row tile, key head) in chunks of 128 are laid end to end, and
+// every (request, group of tiles, key head) in chunks of 128 are laid end to end, and
 // workgroup b takes the b-th equal share of the chunks. A share that holds all of a
-// tile's chunks writes the output; the others leave (M, l, sum) in the workspace
+// segment's chunks writes the output; the others leave (M, l, sum) in the workspace
 // and gdn_attn_join_k, a second launch, joins them. Every workgroup forms the
 // prefix sums of the requests' chunks by itself: R loads and one scan instead of a
 // launch. The order of every sum is fixed by the lengths, so results repeat bit for
 // bit; no atomics are used.
+#include <type_traits>
+
 #include "gdn_attn_kernels.h"
 #include "gdn_common.h"
 
@@ -39,16 +46,20 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
 constexpr int kRows = 16;                 // rows of a tile: the N side of the MFMA
+constexpr int kTiles = 4;                 // tiles of a workgroup
 constexpr int kChunkShift = 7;            // positions of a unit of work: 128
+constexpr int kWholeShift = 30;           // one unit per segment: nothing is split
 constexpr int kGroups = 512;              // workgroups of a split launch: two per CU
 
 enum Format { kF32 = 0, kF16 = 1, kE4M3 = 2 };
 
+typedef uint32_t uint2_t __attribute__((ext_vector_type(2)));
 typedef uint32_t uint4_t __attribute__((ext_vector_type(4)));
 
 struct SplitArgs {
   int64_t* prefix;                        // [R + 1] chunks before a request; null: nothing is split
-  float* parts;                           // [2 * groups][kRows * (D + 2)]: M, l, sums
+  float* parts;                           // [2 * groups][part_rows * (D + 2)]: M, l, sums
+  int32_t part_rows;
   int32_t chunk_shift;
 };
 
@@ -57,7 +68,7 @@ struct Plan {
   int start, T;                           // first token, tokens
   int64_t len;                            // seq_lens[r] as given
   int base, hi;                           // positions [base, hi), base a multiple of 32
-  int tiles, chunks;
+  int segs, chunks;                       // groups of kTiles tiles, units of each
 };
 
 __device__ __forceinline__ int clamp_pos(int64_t x, int hi) { return (int)(x < 0 ? 0 : x > hi ? hi : x); }
@@ -70,12 +81,12 @@ __device__ __forceinline__ Plan plan_of(const AttnArgs& p, int r, int chunk_shif
   const int cap = p.cache.max_pages << p.cache.page_shift;
   s.hi = clamp_pos(s.len, cap);
   s.base = p.window > 0 ? clamp_pos(s.len - s.T + 1 - p.window, s.hi) & ~31 : 0;
-  s.tiles = (s.T * p.group + kRows - 1) / kRows;
+  s.segs = (s.T * p.group + kTiles * kRows - 1) / (kTiles * kRows);
   s.chunks = s.T > 0 ? max((int)(((int64_t)s.hi - s.base + (1ll << chunk_shift) - 1) >> chunk_shift), 1) : 0;
   return s;
 }
 
-__device__ __forceinline__ int64_t units_of(const Plan& s, int Hk) { return (int64_t)s.tiles * Hk * s.chunks; }
+__device__ __forceinline__ int64_t units_of(const Plan& s, int Hk) { return (int64_t)s.segs * Hk * s.chunks; }
 
 __device__ __forceinline__ int64_t share_of(int64_t total, int groups) { return max((total + groups - 1) / groups, (int64_t)1); }
 
@@ -124,15 +135,15 @@ struct Shape {
 template <int WORDS>
 __device__ __forceinline__ void load_words(const char* p, uint32_t (&w)[WORDS]) {
   if constexpr (WORDS == 4) {
-    const uint4_t x = *reinterpret_cast<const uint4_t*>(p);
+    const uint4_t x = __builtin_nontemporal_load(reinterpret_cast<const uint4_t*>(p));
 #pragma unroll
     for (int i = 0; i < 4; ++i) w[i] = x[i];
   } else if constexpr (WORDS == 2) {
-    const uint2 x = *reinterpret_cast<const uint2*>(p);
-    w[0] = x.x;
-    w[1] = x.y;
+    const uint2_t x = __builtin_nontemporal_load(reinterpret_cast<const uint2_t*>(p));
+    w[0] = x[0];
+    w[1] = x[1];
   } else {
-    w[0] = *reinterpret_cast<const uint32_t*>(p);
+    w[0] = __builtin_nontemporal_load(reinterpret_cast<const uint32_t*>(p));
   }
 }
 
@@ -225,23 +236,28 @@ __global__ void __launch_bounds__(kThreads, D == 256 && FMT == kF32 ? 1 : 2) gdn
     const int seg = __builtin_amdgcn_readfirstlane((int)(local / s.chunks));
     const int c0 = __builtin_amdgcn_readfirstlane((int)(local - (int64_t)seg * s.chunks));
     const int c1 = __builtin_amdgcn_readfirstlane((int)min((int64_t)s.chunks, c0 + (u_end - u)));
-    const int h = seg / s.tiles, tile = seg - h * s.tiles;
+    const int h = seg / s.segs, seg_row = (seg - h * s.segs) * (kTiles * kRows);
     u += c1 - c0;
 
-    // ---- this lane's row, and the positions the tile's rows attend
+    // ---- the wave's tile and stream of positions, this lane's row, and what the tile's rows attend
+    const int seg_rows = min(kTiles * kRows, s.T * p.group - seg_row);
+    const int streams = seg_rows <= kRows ? 4 : seg_rows <= 2 * kRows ? 2 : 1;
+    const int sub = wave / streams, stream = wave - sub * streams;
+    const int rows = max(min(kRows, seg_rows - sub * kRows), 0);       // 0: a wave without a tile
+    const int row0 = seg_row + (rows > 0 ? sub * kRows : 0), last_row = row0 + max(rows, 1) - 1;
     const int cap = p.cache.max_pages << p.cache.page_shift;
-    const int rows = min(kRows, s.T * p.group - tile * kRows);
-    const int row = tile * kRows + min(n, rows - 1);
+    const int row = min(row0 + n, last_row);
     const int j = row / p.group;
     const int64_t past = s.len - s.T + j + 1;              // one past the row's newest position
     const int hi = n < rows ? clamp_pos(past, cap) : 0;
     const int lo = p.window > 0 ? clamp_pos(past - p.window, cap) : 0;
-    const int j0 = tile * kRows / p.group, j1 = (tile * kRows + rows - 1) / p.group;
-    const int hi_min = clamp_pos(s.len - s.T + j0 + 1, cap), hi_max = clamp_pos(s.len - s.T + j1 + 1, cap);
-    const int lo_min = p.window > 0 ? clamp_pos(s.len - s.T + j0 + 1 - p.window, cap) : 0;
-    const int lo_max = p.window > 0 ? clamp_pos(s.len - s.T + j1 + 1 - p.window, cap) : 0;
+    const int64_t past0 = s.len - s.T + row0 / p.group + 1, past1 = s.len - s.T + last_row / p.group + 1;
+    const int hi_min = clamp_pos(past0, cap), hi_max = rows > 0 ? clamp_pos(past1, cap) : 0;
+    const int lo_min = p.window > 0 ? clamp_pos(past0 - p.window, cap) : 0;
+    const int lo_max = p.window > 0 ? clamp_pos(past1 - p.window, cap) : 0;
     const int t0 = s.base + (int)((int64_t)c0 << sp.chunk_shift);
     const int t1 = (int)min((int64_t)s.base + ((int64_t)c1 << sp.chunk_shift), (int64_t)hi_max);
+    const int step = streams * S::kTile;
 
     // q as the first product's second operand, in the order k is loaded in
     const IO* q = qs + (int64_t)(s.start + j) * p.q_stride + (int64_t)(h * p.group + row - j * p.group) * D;
@@ -268,12 +284,12 @@ __global__ void __launch_bounds__(kThreads, D == 256 && FMT == kF32 ? 1 : 2) gdn
     const int kpos = FMT == kF32 ? n : 8 * (n >> 2) + (n & 3), vpos = S::kPos * g;
 
     int kpage = -1, vpage = -1;
-    int t = t0 + wave * S::kTile;
+    int t = t0 + stream * S::kTile;
     if (t < t1) {
       kpage = page_of(p, table, t + kpos);
       vpage = page_of(p, table, t + vpos);
     }
-    for (; t < t1; t += kWaves * S::kTile) {
+    for (; t < t1; t += step) {
       const bool held = vpage >= 0;
       const int64_t krow = (((int64_t)max(kpage, 0) * p.cache.Hk + h) << p.cache.page_shift) + ((t + kpos) & in_page);
       const int64_t vrow = (((int64_t)max(vpage, 0) * p.cache.Hk + h) << p.cache.page_shift) + ((t + vpos) & in_page);
@@ -295,7 +311,7 @@ __global__ void __launch_bounds__(kThreads, D == 256 && FMT == kF32 ? 1 : 2) gdn
 #pragma unroll
         for (int c = 0; c < S::kSets; ++c)
           load_words(vp + (i * D + 16 * S::kCols * c) * S::kBytes, vw[i][c]);
-      const int next = t + kWaves * S::kTile;
+      const int next = t + step;
       if (next < t1) {
         kpage = page_of(p, table, next + kpos);
         vpage = page_of(p, table, next + vpos);
@@ -386,20 +402,35 @@ __global__ void __launch_bounds__(kThreads, D == 256 && FMT == kF32 ? 1 : 2) gdn
       }
 
       // ---- O^T += V^T P^T
-      auto product = [&](const float (&wt)[S::kPos], const uint32_t (&vv)[S::kPos][S::kSets][S::kVWords],
-                         float4_t (&to)[kAcc]) {
+      half8_t pw;
+      if constexpr (FMT != kF32) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) pw[i] = (_Float16)wgt[i];
+      }
+      // `seen`: a mask per position of what to keep of v; the sums of lanes with keep false stay
+      auto product = [&](auto all, const uint32_t (&seen)[S::kPos], bool keep) {
+        constexpr bool kAll = decltype(all)::value;
+        auto add = [&](int o, const float4_t& x) {
+          if constexpr (kAll) {
+            acc[o] = x;
+          } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[o][e] = keep ? x[e] : acc[o][e];
+          }
+        };
         if constexpr (FMT == kF32) {
 #pragma unroll
           for (int c = 0; c < S::kSets; ++c)
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
+            for (int e = 0; e < 4; ++e) {
+              float4_t x = acc[4 * c + e];
 #pragma unroll
               for (int i = 0; i < 4; ++i)
-                to[4 * c + e] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(vv[i][c][e]), wt[i], to[4 * c + e], 0, 0, 0);
+                x = __builtin_amdgcn_mfma_f32_16x16x4f32(
+                    __uint_as_float(kAll ? vw[i][c][e] : vw[i][c][e] & seen[i]), wgt[i], x, 0, 0, 0);
+              add(4 * c + e, x);
+            }
         } else {
-          half8_t pw;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) pw[i] = (_Float16)wt[i];
 #pragma unroll
           for (int c = 0; c < S::kSets; ++c)
 #pragma unroll
@@ -408,9 +439,10 @@ __global__ void __launch_bounds__(kThreads, D == 256 && FMT == kF32 ? 1 : 2) gdn
 #pragma unroll
               for (int i = 0; i < 8; ++i) {
                 if constexpr (FMT == kF16)
-                  pair[i] = vv[i][c][q2];
+                  pair[i] = vw[i][c][q2];
                 else
-                  pair[i] = (q2 & 1) ? codes_to_half2<true>(vv[i][c][q2 >> 1]) : codes_to_half2<false>(vv[i][c][q2 >> 1]);
+                  pair[i] = (q2 & 1) ? codes_to_half2<true>(vw[i][c][q2 >> 1]) : codes_to_half2<false>(vw[i][c][q2 >> 1]);
+                if constexpr (!kAll) pair[i] &= seen[i];
               }
               uint4_t a0, a1;
 #pragma unroll
@@ -419,35 +451,25 @@ __global__ void __launch_bounds__(kThreads, D == 256 && FMT == kF32 ? 1 : 2) gdn
                 a1[i] = __builtin_amdgcn_perm(pair[2 * i + 1], pair[2 * i], 0x07060302u);
               }
               const int o = S::kCols * c + 2 * q2;
-              to[o] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8_t, a0), pw, to[o], 0, 0, 0);
-              to[o + 1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8_t, a1), pw, to[o + 1], 0, 0, 0);
+              add(o, __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8_t, a0), pw, acc[o], 0, 0, 0));
+              add(o + 1, __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8_t, a1), pw, acc[o + 1], 0, 0, 0));
             }
         }
       };
+      uint32_t seen[S::kPos] = {};
       if (!mixed) {
-        product(wgt, vw, acc);
+        product(std::true_type{}, seen, true);
       } else {
         // a row at a time, with the values it does not attend taken out
+#pragma unroll 1
         for (int k = 0; k < rows; ++k) {
           const int row_hi = __shfl(hi, k), row_lo = __shfl(lo, k);
-          uint32_t own[S::kPos][S::kSets][S::kVWords];
 #pragma unroll
           for (int i = 0; i < S::kPos; ++i) {
             const int pos = t + vpos + i;
-            const bool sees = pos >= row_lo && pos < row_hi;
-#pragma unroll
-            for (int c = 0; c < S::kSets; ++c)
-#pragma unroll
-              for (int w = 0; w < S::kVWords; ++w) own[i][c][w] = sees ? vw[i][c][w] : 0u;
+            seen[i] = pos >= row_lo && pos < row_hi ? 0xffffffffu : 0u;
           }
-          float4_t to[kAcc];
-#pragma unroll
-          for (int i = 0; i < kAcc; ++i) to[i] = acc[i];
-          product(wgt, own, to);
-#pragma unroll
-          for (int i = 0; i < kAcc; ++i)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) acc[i][e] = n == k ? to[i][e] : acc[i][e];
+          product(std::false_type{}, seen, n == k);
         }
       }
     }
@@ -460,9 +482,9 @@ __global__ void __launch_bounds__(kThreads, D == 256 && FMT == kF32 ? 1 : 2) gdn
       stats[wave][n][1] = l;
     }
     __syncthreads();
-    float top = stats[0][n][0];
-#pragma unroll
-    for (int w = 1; w < kWaves; ++w) top = fmaxf(top, stats[w][n][0]);
+    const int w0 = sub * streams;                          // the waves of this wave's tile
+    float top = M;
+    for (int w = w0; w < w0 + streams; ++w) top = fmaxf(top, stats[w][n][0]);
     const float f = M == -INFINITY ? 0.f : exp2_fast(M - top);
     // acc[cols c + e] of row n, register i: column 16 cols c + cols (4 g + i) + e
 #pragma unroll
@@ -476,20 +498,19 @@ __global__ void __launch_bounds__(kThreads, D == 256 && FMT == kF32 ? 1 : 2) gdn
                        acc[S::kCols * c + e + 3][i] * f};
     __syncthreads();
     const bool complete = c0 == 0 && c1 == s.chunks;
-    float* part = complete ? nullptr : sp.parts + (2 * (int64_t)blockIdx.x + (c0 == 0 ? 1 : 0)) * (kRows * (D + 2));
-    for (int i = tid; i < rows * (D / 4); i += kThreads) {
-      const int rr = i / (D / 4), d = 4 * (i - rr * (D / 4));
-      float best = stats[0][rr][0], sum = 0.f;
-#pragma unroll
-      for (int w = 1; w < kWaves; ++w) best = fmaxf(best, stats[w][rr][0]);
-#pragma unroll
-      for (int w = 0; w < kWaves; ++w)
-        sum += stats[w][rr][0] == -INFINITY ? 0.f : stats[w][rr][1] * exp2_fast(stats[w][rr][0] - best);
-      float4_t o = *reinterpret_cast<const float4_t*>(&sums[0][rr][d]);
-#pragma unroll
-      for (int w = 1; w < kWaves; ++w) o += *reinterpret_cast<const float4_t*>(&sums[w][rr][d]);
+    float* part = complete ? nullptr
+                           : sp.parts + (2 * (int64_t)blockIdx.x + (c0 == 0 ? 1 : 0)) * (sp.part_rows * (D + 2));
+    for (int i = tid; i < seg_rows * (D / 4); i += kThreads) {
+      const int rr = i / (D / 4), d = 4 * (i - rr * (D / 4)), rn = rr % kRows, from = rr / kRows * streams;
+      float best = stats[from][rn][0], sum = 0.f;
+      for (int w = from + 1; w < from + streams; ++w) best = fmaxf(best, stats[w][rn][0]);
+      float4_t o = float4_t{0.f, 0.f, 0.f, 0.f};
+      for (int w = from; w < from + streams; ++w) {
+        sum += stats[w][rn][0] == -INFINITY ? 0.f : stats[w][rn][1] * exp2_fast(stats[w][rn][0] - best);
+        o += *reinterpret_cast<const float4_t*>(&sums[w][rn][d]);
+      }
       if (complete) {
-        const int grow = tile * kRows + rr, jj = grow / p.group;
+        const int grow = seg_row + rr, jj = grow / p.group;
         IO* out = static_cast<IO*>(p.output) + ((int64_t)(s.start + jj) * p.Hq + h * p.group + grow - jj * p.group) * D + d;
         const float norm = sum == 0.f ? 0.f : 1.f / sum;
         if constexpr (FMT == kF32)
@@ -498,27 +519,30 @@ __global__ void __launch_bounds__(kThreads, D == 256 && FMT == kF32 ? 1 : 2) gdn
           *reinterpret_cast<half4_t*>(out) = half4_t{(_Float16)(o[0] * norm), (_Float16)(o[1] * norm),
                                                      (_Float16)(o[2] * norm), (_Float16)(o[3] * norm)};
       } else {
-        *reinterpret_cast<float4_t*>(part + 2 * kRows + rr * D + d) = o;
+        *reinterpret_cast<float4_t*>(part + 2 * sp.part_rows + rr * D + d) = o;
         if (d == 0) {
           part[rr] = best;
-          part[kRows + rr] = sum;
+          part[sp.part_rows + rr] = sum;
         }
       }
     }
   }
 }
 
-// Joins the parts of the tiles that several workgroups shared: one workgroup per
-// (token, query head).
+// Joins the parts of the segments that several workgroups shared: a workgroup per
+// (token, query head, 64 columns), its 16 slices of 16 lanes taking alternate parts.
+// Parts are few and scattered, so latency counts: a slice loads several parts at once
+// and joins them with a running M of its own.
 template <int FMT, int D>
 __global__ void __launch_bounds__(kThreads) gdn_attn_join_k(AttnArgs p, SplitArgs sp, int groups) {
   typedef typename std::conditional<FMT == kF32, float, _Float16>::type IO;
-  constexpr int kLanes = D / 4, kSlices = kThreads / kLanes;
+  constexpr int kLanes = 16, kSlices = kThreads / kLanes, kSteps = D / 64, kAhead = 4;
   __shared__ float4_t sums[kSlices][kLanes];
-  __shared__ float tops[kWaves], ls[kSlices];
+  __shared__ float stats[kSlices][2];
   const int tid = threadIdx.x;
-  const int n = (int)(blockIdx.x / p.Hq), head = (int)(blockIdx.x % p.Hq);
-  if (n >= row_start(p.rows, p.rows.R)) return;
+  const int id = (int)(blockIdx.x / kSteps), column = (int)(blockIdx.x % kSteps) * 64;
+  const int n = id / p.Hq, head = id - n * p.Hq;
+  const int64_t total = sp.prefix[p.rows.R];
   int r = 0;
   if (p.rows.cu_seqlens == nullptr) {
     r = n / p.rows.dense_len;
@@ -530,43 +554,62 @@ __global__ void __launch_bounds__(kThreads) gdn_attn_join_k(AttnArgs p, SplitArg
     }
   }
   const Plan s = plan_of(p, r, sp.chunk_shift);
-  if (n < s.start || n >= s.start + s.T) return;
+  if (n < s.start || n >= s.start + s.T) return;           // behind the last request
   const int h = head / p.group, row = (n - s.start) * p.group + head - h * p.group;
-  const int tile = row / kRows, rr = row - tile * kRows;
-  const int64_t share = share_of(sp.prefix[p.rows.R], groups);
-  const int64_t from = sp.prefix[r] + ((int64_t)h * s.tiles + tile) * s.chunks;
+  const int seg = row / (kTiles * kRows), rr = row - seg * (kTiles * kRows);
+  const int64_t share = share_of(total, groups);
+  const int64_t from = sp.prefix[r] + ((int64_t)h * s.segs + seg) * s.chunks;
   const int64_t b0 = from / share;
   const int count = (int)((from + s.chunks - 1) / share - b0) + 1;
   if (count == 1) return;                                  // written by its one workgroup
-  // the first workgroup's part is its last segment, the others' their first
-  auto part = [&](int i) { return sp.parts + (2 * (b0 + i) + (i == 0 ? 1 : 0)) * (int64_t)(kRows * (D + 2)); };
-
-  float top = -INFINITY;
-  for (int i = tid; i < count; i += kThreads) top = fmaxf(top, part(i)[rr]);
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) top = fmaxf(top, __shfl_xor(top, d));
-  if ((tid & 63) == 0) tops[tid >> 6] = top;
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < kWaves; ++w) top = fmaxf(top, tops[w]);
-  const int slice = tid / kLanes, d = 4 * (tid - slice * kLanes);
+  const int64_t size = (int64_t)sp.part_rows * (D + 2);
+  const int slice = tid / kLanes, d = column + 4 * (tid - slice * kLanes);
   float4_t o = float4_t{0.f, 0.f, 0.f, 0.f};
-  float l = 0.f;
-  for (int i = slice; i < count; i += kSlices) {
-    const float* x = part(i);
-    const float f = x[rr] == -INFINITY ? 0.f : exp2_fast(x[rr] - top);
-    o += *reinterpret_cast<const float4_t*>(x + 2 * kRows + rr * D + d) * f;
-    l = fmaf(x[kRows + rr], f, l);
+  float M = -INFINITY, l = 0.f;
+  for (int i = slice; i < count; i += kSlices * kAhead) {
+    float m[kAhead], li[kAhead];
+    float4_t x[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      // the first workgroup's part is its last segment, the others' their first; loads past
+      // the last part repeat it
+      const int at = min(i + k * kSlices, count - 1);
+      const float* part = sp.parts + (2 * (b0 + at) + (at == 0 ? 1 : 0)) * size;
+      m[k] = part[rr];
+      li[k] = part[sp.part_rows + rr];
+      x[k] = *reinterpret_cast<const float4_t*>(part + 2 * sp.part_rows + rr * D + d);
+    }
+    float top = M;
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) top = i + k * kSlices < count ? fmaxf(top, m[k]) : top;
+    const float f = M == -INFINITY ? 0.f : exp2_fast(M - top);
+    o *= f;
+    l *= f;
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      const float w = i + k * kSlices < count && m[k] != -INFINITY ? exp2_fast(m[k] - top) : 0.f;
+      o += x[k] * w;
+      l = fmaf(li[k], w, l);
+    }
+    M = top;
   }
   sums[slice][tid - slice * kLanes] = o;
-  if (d == 0) ls[slice] = l;
+  if (tid % kLanes == 0) {
+    stats[slice][0] = M;
+    stats[slice][1] = l;
+  }
   __syncthreads();
   if (tid >= kLanes) return;
-  l = ls[0];
+  float top = stats[0][0];
 #pragma unroll
-  for (int i = 1; i < kSlices; ++i) {
-    o += sums[i][tid];
-    l += ls[i];
+  for (int i = 1; i < kSlices; ++i) top = fmaxf(top, stats[i][0]);
+  o = float4_t{0.f, 0.f, 0.f, 0.f};
+  l = 0.f;
+#pragma unroll
+  for (int i = 0; i < kSlices; ++i) {
+    const float f = stats[i][0] == -INFINITY ? 0.f : exp2_fast(stats[i][0] - top);
+    o += sums[i][tid] * f;
+    l = fmaf(stats[i][1], f, l);
   }
   const float norm = l == 0.f ? 0.f : 1.f / l;
   IO* out = static_cast<IO*>(p.output) + ((int64_t)n * p.Hq + head) * D + d;
@@ -579,15 +622,34 @@ __global__ void __launch_bounds__(kThreads) gdn_attn_join_k(AttnArgs p, SplitArg
 
 size_t prefix_bytes(int64_t R) { return ((size_t)(R + 1) * 8 + 255) & ~(size_t)255; }
 
+// Rows of a part: a segment's, of at most kTiles tiles.
+int part_rows(int64_t N, int group) {
+  const int64_t tiles = (N * group + kRows - 1) / kRows;
+  return (int)(tiles < kTiles ? tiles : kTiles) * kRows;
+}
+
+// Without a split a segment's positions pass through one workgroup, 128 at a time,
+// and the second launch falls away.
+constexpr int kWholeMax = 512;
+constexpr int64_t kWholeGroups = 4096;
+
 template <int FMT, int D>
 hipError_t launch_attn_d(const AttnArgs& p, void* workspace, hipStream_t stream) {
   SplitArgs sp{};
+  if (p.max_len <= kWholeMax) {
+    sp.chunk_shift = kWholeShift;
+    const int64_t segments = ((int64_t)p.rows.N * p.group / (kTiles * kRows) + p.rows.R) * p.cache.Hk;
+    hipLaunchKernelGGL((gdn_attn_k<FMT, D>), dim3((unsigned)(segments < kWholeGroups ? segments : kWholeGroups)),
+                       dim3(kThreads), 0, stream, p, sp);
+    return hipGetLastError();
+  }
   sp.prefix = static_cast<int64_t*>(workspace);
   sp.parts = reinterpret_cast<float*>(static_cast<char*>(workspace) + prefix_bytes(p.rows.R));
+  sp.part_rows = part_rows(p.rows.N, p.group);
   sp.chunk_shift = kChunkShift;
   hipLaunchKernelGGL((gdn_attn_k<FMT, D>), dim3(kGroups), dim3(kThreads), 0, stream, p, sp);
-  hipLaunchKernelGGL((gdn_attn_join_k<FMT, D>), dim3((unsigned)((int64_t)p.rows.N * p.Hq)), dim3(kThreads), 0, stream, p,
-                     sp, kGroups);
+  hipLaunchKernelGGL((gdn_attn_join_k<FMT, D>), dim3((unsigned)((int64_t)p.rows.N * p.Hq * (D / 64))), dim3(kThreads),
+                     0, stream, p, sp, kGroups);
   return hipGetLastError();
 }
 
@@ -611,7 +673,7 @@ hipError_t launch_attn(const AttnArgs& p, int io_dtype, void* workspace, hipStre
 
 size_t attn_workspace_bytes(int64_t N, int64_t R, int Hq, int Hk, int D) {
   if (N == 0 || R == 0) return 0;
-  return prefix_bytes(R) + (size_t)2 * kGroups * kRows * (D + 2) * sizeof(float);
+  return prefix_bytes(R) + (size_t)2 * kGroups * part_rows(N, Hq / Hk) * (D + 2) * sizeof(float);
 }
 
 }  // namespace gdn

@@ -77,6 +77,7 @@ struct AttnArgs {
   int64_t q_stride;
   int32_t Hq, group;            // group = Hq / Hk
   int32_t window;               // 0: none
+  int32_t max_len;              // no request attends more positions, as far as the host knows
   float scale;
   CacheArgs cache;
   RowArgs rows;
