@@ -7,30 +7,33 @@
 // weights) and the output's unnormalised sum, rescaling both when M grows; waves,
 // and workgroups that share a request's length, are joined by the same rule.
 //
-// Decode reads every key and value once for at most 16 rows (tokens x heads of a
-// key head), so it is bound by HBM; the matrix cores only keep the arithmetic out
-// of the way. The layouts follow from loading both operands straight into
-// registers, with no LDS and no barrier in the loop:
-//  - rows are the N side of both products: S^T = K Q^T and O^T = V^T P^T. A row's
-//    scores then lie in 4 lanes (l & 15 = row), its weights leave the first
-//    product in the order the second one takes them in, and the running M, l and
-//    the rescaling factor are one register each.
-//  - a wave's tile is 32 positions (16 for fp32). Lane group g = l >> 4 takes the
-//    positions 8 g .. 8 g + 7 in the second product's contraction, so the first
-//    product's two 16-position blocks hold the positions 8 g + 4 a + (0 .. 3).
-//  - v is loaded in rows too: a lane holds the same few columns of 8 positions and
-//    turns them into columns with byte permutes (half an instruction an element).
+// Reading every key and value once for a few dozen rows (tokens x heads of a key
+// head) is bound by HBM; the matrix cores keep the arithmetic out of the way. Rows
+// are the N side of both products, S^T = K Q^T and O^T = V^T P^T: a row's scores
+// lie in 4 lanes (l & 15 = row), its weights leave the first product in the order
+// the second one takes them in, and the running M, l and the rescaling factor are
+// one register each. Two kernels differ in how keys and values reach the registers:
 //
-// Rows come in tiles of 16, and a workgroup takes up to 4 tiles of a request and key
-// head: with one tile its 4 waves take alternate positions, with two tiles 2 waves
-// each, with more one wave each. Waves of different tiles then read the same keys and
-// values at the same time, through one CU's L1, so HBM is read once for up to 64 rows.
+//  gdn_attn_k, for at most 16 rows a request and key head (decode): straight from
+//  memory, with no LDS and no barrier in the loop. A wave's tile is 32 positions
+//  (16 for fp32) and its 4 waves take alternate tiles. Each byte is used once and
+//  loaded past the caches' retention (nontemporal).
+//
+//  gdn_attn_rows_k, for up to 64 rows (drafts, prompts): through LDS, so that 4
+//  waves with 16 rows each share one copy. A fifth wave does nothing but copy pages
+//  into a ring of 16 KiB stages, by buffer loads that write LDS directly; it needs
+//  no registers for them and runs ahead over the ring, and the loads' range check
+//  fills positions past the end and without a page with zeros. A counter of landed
+//  stages and one of finished stages per wave, both in LDS, hand the stages over,
+//  so the waves need not run in step. With one tile of rows this kernel is slower
+//  than the first (a wave's 16-position tile is a long chain of dependent steps,
+//  and LDS leaves room for 8 such waves a CU), with several it is faster.
 //
 // Work is split evenly over the workgroups whatever the lengths: the positions of
-// every (request, group of tiles, key head) in chunks of 128 are laid end to end, and
-// workgroup b takes the b-th equal share of the chunks. A share that holds all of a
-// segment's chunks writes the output; the others leave (M, l, sum) in the workspace
-// and gdn_attn_join_k, a second launch, joins them. Every workgroup forms the
+// every segment (request, 16 or 64 rows, key head) in chunks of 128 are laid end to
+// end, and workgroup b takes the b-th equal share of the chunks. A share that holds
+// all of a segment's chunks writes the output; the others leave (M, l, sum) in the
+// workspace and gdn_attn_join_k, a second launch, joins them. Every wave forms the
 // prefix sums of the requests' chunks by itself: R loads and one scan instead of a
 // launch. The order of every sum is fixed by the lengths, so results repeat bit for
 // bit; no atomics are used.
@@ -43,11 +46,12 @@ namespace gdn {
 
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWaves = kThreads / 64;
+constexpr int kWaves = 4;                 // computing waves
+constexpr int kThreads = 64 * kWaves;
+constexpr int kBlock = kThreads + 64;     // with a loader wave
 constexpr int kRows = 16;                 // rows of a tile: the N side of the MFMA
-constexpr int kTiles = 4;                 // tiles of a workgroup
-constexpr int kChunkShift = 7;            // positions of a unit of work: 128
+constexpr int kTiles = 4;                 // tiles of a segment of gdn_attn_rows_k
+constexpr int kChunkShift = 7;            // positions of a unit of work: 128 or more
 constexpr int kWholeShift = 30;           // one unit per segment: nothing is split
 constexpr int kGroups = 512;              // workgroups of a split launch: two per CU
 
@@ -57,9 +61,10 @@ typedef uint32_t uint2_t __attribute__((ext_vector_type(2)));
 typedef uint32_t uint4_t __attribute__((ext_vector_type(4)));
 
 struct SplitArgs {
-  int64_t* prefix;                        // [R + 1] chunks before a request; null: nothing is split
+  int32_t* prefix;                        // [R + 1] units before a request; null: nothing is split
   float* parts;                           // [2 * groups][part_rows * (D + 2)]: M, l, sums
   int32_t part_rows;
+  int32_t seg_rows;                       // rows of a segment: 16 or 64
   int32_t chunk_shift;
 };
 
@@ -68,12 +73,12 @@ struct Plan {
   int start, T;                           // first token, tokens
   int64_t len;                            // seq_lens[r] as given
   int base, hi;                           // positions [base, hi), base a multiple of 32
-  int segs, chunks;                       // groups of kTiles tiles, units of each
+  int segs, chunks;                       // segments of a key head, units of each
 };
 
 __device__ __forceinline__ int clamp_pos(int64_t x, int hi) { return (int)(x < 0 ? 0 : x > hi ? hi : x); }
 
-__device__ __forceinline__ Plan plan_of(const AttnArgs& p, int r, int chunk_shift) {
+__device__ __forceinline__ Plan plan_of(const AttnArgs& p, const SplitArgs& sp, int r) {
   Plan s;
   s.start = row_start(p.rows, r);
   s.T = max(row_start(p.rows, r + 1) - s.start, 0);
@@ -81,14 +86,119 @@ __device__ __forceinline__ Plan plan_of(const AttnArgs& p, int r, int chunk_shif
   const int cap = p.cache.max_pages << p.cache.page_shift;
   s.hi = clamp_pos(s.len, cap);
   s.base = p.window > 0 ? clamp_pos(s.len - s.T + 1 - p.window, s.hi) & ~31 : 0;
-  s.segs = (s.T * p.group + kTiles * kRows - 1) / (kTiles * kRows);
-  s.chunks = s.T > 0 ? max((int)(((int64_t)s.hi - s.base + (1ll << chunk_shift) - 1) >> chunk_shift), 1) : 0;
+  s.segs = (int)(((unsigned)(s.T * p.group) + sp.seg_rows - 1) / (unsigned)sp.seg_rows);
+  s.chunks = s.T > 0 ? max((int)(((int64_t)s.hi - s.base + (1ll << sp.chunk_shift) - 1) >> sp.chunk_shift), 1) : 0;
   return s;
 }
 
-__device__ __forceinline__ int64_t units_of(const Plan& s, int Hk) { return (int64_t)s.segs * Hk * s.chunks; }
+// The launch bounds the units of all requests by 2^30.
+__device__ __forceinline__ int units_of(const Plan& s, int Hk) { return s.segs * Hk * s.chunks; }
 
-__device__ __forceinline__ int64_t share_of(int64_t total, int groups) { return max((total + groups - 1) / groups, (int64_t)1); }
+__device__ __forceinline__ int share_of(int total, int groups) { return max((int)((unsigned)(total + groups - 1) / (unsigned)groups), 1); }
+
+// Inclusive sum over the lanes of a wave.
+__device__ __forceinline__ int wave_scan(int x) {
+  x += __builtin_amdgcn_update_dpp(0, x, 0x111, 0xf, 0xf, false);   // row_shr 1, 2, 4, 8
+  x += __builtin_amdgcn_update_dpp(0, x, 0x112, 0xf, 0xf, false);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x114, 0xf, 0xf, false);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x118, 0xf, 0xf, false);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x142, 0xa, 0xf, false);   // row 0's total to row 1, row 2's to row 3
+  x += __builtin_amdgcn_update_dpp(0, x, 0x143, 0xc, 0xf, false);   // the lower half's total to the upper
+  return x;
+}
+
+// This workgroup's share [u, u_end) of the units, and the request r that holds u,
+// whose units begin at r_first. Every wave finds it by itself. Workgroup 0 leaves
+// the prefix sums for the join.
+struct Share {
+  int u, u_end, r, r_first;
+};
+
+__device__ __forceinline__ Share find_share(const AttnArgs& p, const SplitArgs& sp, int lane, bool leave) {
+  const int R = p.rows.R, per = (R + 63) >> 6;             // requests a lane sums
+  const int r0 = min(lane * per, R), r1 = min(r0 + per, R);
+  int mine = 0;
+#pragma unroll 4
+  for (int r = r0; r < r1; ++r) mine += units_of(plan_of(p, sp, r), p.cache.Hk);
+  const int after = wave_scan(mine), before = after - mine;
+  const int total = __builtin_amdgcn_readlane(after, 63);
+  Share w;
+  const int share = share_of(total, (int)gridDim.x);
+  w.u = min((int)blockIdx.x * share, total);               // groups * share < total + groups
+  w.u_end = min(w.u + share, total);
+  w.r = w.r_first = 0;
+  if (leave) {
+    int at = before;
+    for (int r = r0; r < r1; ++r) {
+      sp.prefix[r] = at;
+      at += units_of(plan_of(p, sp, r), p.cache.Hk);
+    }
+    if (lane == 63) sp.prefix[R] = total;
+  }
+  if (w.u >= w.u_end) return w;
+  const int holder = __builtin_ctzll(__ballot(w.u >= before && w.u < after));
+  w.r = holder * per;
+  w.r_first = __builtin_amdgcn_readlane(before, holder);
+  return w;
+}
+
+// The next segment of a share: units [c0, c1) of (request, rows from seg_row on, key
+// head h); the share's u moves past it.
+struct Segment {
+  Plan s;
+  int h, seg_row, rows, c0, c1;
+  int t0, end;                                             // positions [t0, end)
+};
+
+__device__ __forceinline__ Segment next_segment(const AttnArgs& p, const SplitArgs& sp, Share& w) {
+  Segment x;
+  x.s = plan_of(p, sp, w.r);
+  while (w.u - w.r_first >= units_of(x.s, p.cache.Hk)) {   // requests without tokens have no units
+    w.r_first += units_of(x.s, p.cache.Hk);
+    x.s = plan_of(p, sp, ++w.r);
+  }
+  const unsigned local = w.u - w.r_first, seg = local / (unsigned)x.s.chunks;
+  x.c0 = local - seg * x.s.chunks;
+  x.c1 = min(x.s.chunks, x.c0 + (w.u_end - w.u));
+  x.h = seg / (unsigned)x.s.segs;
+  x.seg_row = (int)(seg - x.h * x.s.segs) * sp.seg_rows;
+  w.u += x.c1 - x.c0;
+  x.rows = min(sp.seg_rows, x.s.T * p.group - x.seg_row);
+  const int cap = p.cache.max_pages << p.cache.page_shift;
+  const int64_t past_last = x.s.len - x.s.T + (int)((unsigned)(x.seg_row + x.rows - 1) / (unsigned)p.group) + 1;
+  x.t0 = x.s.base + (int)((int64_t)x.c0 << sp.chunk_shift);
+  x.end = (int)min((int64_t)x.s.base + ((int64_t)x.c1 << sp.chunk_shift), (int64_t)clamp_pos(past_last, cap));
+  return x;
+}
+
+// A lane's row of a tile of `rows` rows from row0 on, and the positions that the
+// tile's rows attend: [lo, hi) of the lane's, within [lo_min, hi_max); every row
+// attends [lo_max, hi_min).
+struct Rows {
+  int j, head;                                             // token of the request, head of the group
+  int lo, hi, lo_min, lo_max, hi_min, hi_max;
+};
+
+__device__ __forceinline__ Rows rows_of(const AttnArgs& p, const Plan& s, int row0, int rows, int n) {
+  Rows x;
+  const int cap = p.cache.max_pages << p.cache.page_shift;
+  const int last = row0 + max(rows, 1) - 1, row = min(row0 + n, last);
+  x.j = (int)((unsigned)row / (unsigned)p.group);
+  x.head = row - x.j * p.group;
+  const int64_t before = s.len - s.T + 1;                  // one past the first token's newest position
+  const int64_t past = before + x.j, past0 = before + (int)((unsigned)row0 / (unsigned)p.group),
+                past1 = before + (int)((unsigned)last / (unsigned)p.group);
+  x.hi = n < rows ? clamp_pos(past, cap) : 0;
+  x.hi_min = clamp_pos(past0, cap);
+  x.hi_max = clamp_pos(past1, cap);
+  x.lo = x.lo_min = x.lo_max = 0;
+  if (p.window > 0) {
+    x.lo = clamp_pos(past - p.window, cap);
+    x.lo_min = clamp_pos(past0 - p.window, cap);
+    x.lo_max = clamp_pos(past1 - p.window, cap);
+  }
+  return x;
+}
 
 // Largest (sum) over the 4 lanes that hold a row: l & 15 the same.
 __device__ __forceinline__ float row_max(float x) {
@@ -112,10 +222,19 @@ __device__ __forceinline__ uint32_t codes_to_half2(uint32_t w) {
   return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.0f, HI));
 }
 
-template <int FMT> __device__ __forceinline__ bool any_nonfinite(uint32_t w) {
-  if constexpr (FMT == kF16) return (((w & 0x7c007c00u) + 0x04000400u) & 0x80008000u) != 0;
-  if constexpr (FMT == kE4M3) return (((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) != 0;
-  return (w & 0x7f800000u) == 0x7f800000u;
+// All bits of the elements of a dword (one float, two halves, four codes) that are infinite or NaN.
+template <int FMT> __device__ __forceinline__ uint32_t nonfinite(uint32_t w) {
+  if constexpr (FMT == kF32) return (w & 0x7f800000u) == 0x7f800000u ? 0xffffffffu : 0u;
+  constexpr uint32_t kMask = FMT == kF16 ? 0x7c007c00u : 0x7f7f7f7fu, kOne = FMT == kF16 ? 0x04000400u : 0x01010101u;
+  const uint32_t top = ((w & kMask) + kOne) & (FMT == kF16 ? 0x80008000u : 0x80808080u);
+  return top | (top - (top >> (FMT == kF16 ? 15 : 7)));
+}
+
+// Element e of the dwords that hold a lane's columns.
+template <int FMT> __device__ __forceinline__ float element(const uint32_t* w, int e) {
+  if constexpr (FMT == kF32) return __uint_as_float(w[e]);
+  const uint32_t pair = FMT == kF16 ? w[e >> 1] : (e & 2) ? codes_to_half2<true>(w[e >> 2]) : codes_to_half2<false>(w[e >> 2]);
+  return (float)__builtin_bit_cast(_Float16, (uint16_t)(e & 1 ? pair >> 16 : pair));
 }
 
 template <int FMT, int D>
@@ -161,106 +280,23 @@ __global__ void __launch_bounds__(kThreads, D == 256 && FMT == kF32 ? 1 : 2) gdn
   constexpr int kAcc = S::kSets * S::kCols;                // 16 x 16 blocks of the output
   __shared__ alignas(16) float sums[kWaves][kRows][S::kPitch];
   __shared__ float stats[kWaves][kRows][2];
-  __shared__ int64_t scan[kWaves + 1];
-  __shared__ int64_t first[2];
 
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int n = lane & 15, g = lane >> 4;
-
-  // ---- this workgroup's share of the units
-  const int per = (p.rows.R + kThreads - 1) / kThreads;    // requests a thread sums
-  int64_t mine = 0;
-  for (int i = 0; i < per; ++i) {
-    const int r = tid * per + i;
-    if (r < p.rows.R) mine += units_of(plan_of(p, r, sp.chunk_shift), p.cache.Hk);
-  }
-  int64_t before = mine;                                   // inclusive scan over the wave
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const int64_t x = __shfl_up(before, d);
-    if (lane >= d) before += x;
-  }
-  if (lane == 63) scan[wave] = before;
-  __syncthreads();
-  int64_t total = 0;
-#pragma unroll
-  for (int w = 0; w < kWaves; ++w) {
-    if (w < wave) before += scan[w];
-    total += scan[w];
-  }
-  before -= mine;
-  const int64_t share = share_of(total, (int)gridDim.x);
-  int64_t u = (int64_t)blockIdx.x * share;
-  const int64_t u_end = min(u + share, total);
-  {
-    int64_t at = before;
-    if (mine > 0 && u >= before && u < before + mine) {
-      for (int i = 0; i < per; ++i) {
-        const int64_t x = units_of(plan_of(p, tid * per + i, sp.chunk_shift), p.cache.Hk);
-        if (u < at + x) {
-          first[0] = tid * per + i;
-          first[1] = at;
-          break;
-        }
-        at += x;
-      }
-    }
-    if (blockIdx.x == 0 && sp.prefix != nullptr) {
-      at = before;
-      for (int i = 0; i < per; ++i) {
-        const int r = tid * per + i;
-        if (r < p.rows.R) {
-          sp.prefix[r] = at;
-          at += units_of(plan_of(p, r, sp.chunk_shift), p.cache.Hk);
-        }
-      }
-      if (tid == 0) sp.prefix[p.rows.R] = total;
-    }
-  }
-  __syncthreads();
-  if (u >= u_end) return;
-  int r = __builtin_amdgcn_readfirstlane((int)first[0]);
-  int64_t r_first = first[1];
-
+  Share sh = find_share(p, sp, lane, blockIdx.x == 0 && wave == 0 && sp.prefix != nullptr);
   const float to_log2 = p.scale * 1.4426950408889634f;
   const IO* __restrict__ qs = static_cast<const IO*>(p.q);
 
-  while (u < u_end) {
-    // ---- the next segment: chunks [c0, c1) of (request, tile, key head)
-    Plan s = plan_of(p, r, sp.chunk_shift);
-    while (u - r_first >= units_of(s, p.cache.Hk)) {       // requests without tokens have no units
-      r_first += units_of(s, p.cache.Hk);
-      s = plan_of(p, ++r, sp.chunk_shift);
-    }
-    const int64_t local = u - r_first;
-    const int seg = __builtin_amdgcn_readfirstlane((int)(local / s.chunks));
-    const int c0 = __builtin_amdgcn_readfirstlane((int)(local - (int64_t)seg * s.chunks));
-    const int c1 = __builtin_amdgcn_readfirstlane((int)min((int64_t)s.chunks, c0 + (u_end - u)));
-    const int h = seg / s.segs, seg_row = (seg - h * s.segs) * (kTiles * kRows);
-    u += c1 - c0;
-
-    // ---- the wave's tile and stream of positions, this lane's row, and what the tile's rows attend
-    const int seg_rows = min(kTiles * kRows, s.T * p.group - seg_row);
-    const int streams = seg_rows <= kRows ? 4 : seg_rows <= 2 * kRows ? 2 : 1;
-    const int sub = wave / streams, stream = wave - sub * streams;
-    const int rows = max(min(kRows, seg_rows - sub * kRows), 0);       // 0: a wave without a tile
-    const int row0 = seg_row + (rows > 0 ? sub * kRows : 0), last_row = row0 + max(rows, 1) - 1;
-    const int cap = p.cache.max_pages << p.cache.page_shift;
-    const int row = min(row0 + n, last_row);
-    const int j = row / p.group;
-    const int64_t past = s.len - s.T + j + 1;              // one past the row's newest position
-    const int hi = n < rows ? clamp_pos(past, cap) : 0;
-    const int lo = p.window > 0 ? clamp_pos(past - p.window, cap) : 0;
-    const int64_t past0 = s.len - s.T + row0 / p.group + 1, past1 = s.len - s.T + last_row / p.group + 1;
-    const int hi_min = clamp_pos(past0, cap), hi_max = rows > 0 ? clamp_pos(past1, cap) : 0;
-    const int lo_min = p.window > 0 ? clamp_pos(past0 - p.window, cap) : 0;
-    const int lo_max = p.window > 0 ? clamp_pos(past1 - p.window, cap) : 0;
-    const int t0 = s.base + (int)((int64_t)c0 << sp.chunk_shift);
-    const int t1 = (int)min((int64_t)s.base + ((int64_t)c1 << sp.chunk_shift), (int64_t)hi_max);
-    const int step = streams * S::kTile;
+  while (sh.u < sh.u_end) {
+    const Segment sg = next_segment(p, sp, sh);
+    const Plan& s = sg.s;
+    const int h = sg.h, rows = sg.rows, t1 = sg.end;
+    const bool complete = sg.c0 == 0 && sg.c1 == s.chunks;
+    const Rows rw = rows_of(p, s, sg.seg_row, rows, n);
+    const int lo = rw.lo, hi = rw.hi;
 
     // q as the first product's second operand, in the order k is loaded in
-    const IO* q = qs + (int64_t)(s.start + j) * p.q_stride + (int64_t)(h * p.group + row - j * p.group) * D;
+    const IO* q = qs + (int64_t)(s.start + rw.j) * p.q_stride + (int64_t)(h * p.group + rw.head) * D;
     half8_t qh[FMT == kF32 ? 1 : D / 32];
     float4_t qf[FMT == kF32 ? D / 16 : 1];
     if constexpr (FMT == kF32) {
@@ -278,18 +314,18 @@ __global__ void __launch_bounds__(kThreads, D == 256 && FMT == kF32 ? 1 : 2) gdn
     for (int i = 0; i < kAcc; ++i) acc[i] = float4_t{0.f, 0.f, 0.f, 0.f};
     float M = -INFINITY, l = 0.f;                          // l: this lane's positions only
 
-    const int32_t* table = p.cache.table + (int64_t)r * p.cache.max_pages;
+    const int32_t* table = p.cache.table + (int64_t)sh.r * p.cache.max_pages;
     const int in_page = (1 << p.cache.page_shift) - 1;
     // positions this lane loads: k of block a at kpos + 4 a (fp32: kpos), v at vpos + 0 .. kPos - 1
     const int kpos = FMT == kF32 ? n : 8 * (n >> 2) + (n & 3), vpos = S::kPos * g;
 
     int kpage = -1, vpage = -1;
-    int t = t0 + stream * S::kTile;
+    int t = sg.t0 + wave * S::kTile;
     if (t < t1) {
       kpage = page_of(p, table, t + kpos);
       vpage = page_of(p, table, t + vpos);
     }
-    for (; t < t1; t += step) {
+    for (; t < t1; t += kWaves * S::kTile) {
       const bool held = vpage >= 0;
       const int64_t krow = (((int64_t)max(kpage, 0) * p.cache.Hk + h) << p.cache.page_shift) + ((t + kpos) & in_page);
       const int64_t vrow = (((int64_t)max(vpage, 0) * p.cache.Hk + h) << p.cache.page_shift) + ((t + vpos) & in_page);
@@ -311,7 +347,7 @@ __global__ void __launch_bounds__(kThreads, D == 256 && FMT == kF32 ? 1 : 2) gdn
 #pragma unroll
         for (int c = 0; c < S::kSets; ++c)
           load_words(vp + (i * D + 16 * S::kCols * c) * S::kBytes, vw[i][c]);
-      const int next = t + step;
+      const int next = t + kWaves * S::kTile;
       if (next < t1) {
         kpage = page_of(p, table, next + kpos);
         vpage = page_of(p, table, next + vpos);
@@ -359,21 +395,26 @@ __global__ void __launch_bounds__(kThreads, D == 256 && FMT == kF32 ? 1 : 2) gdn
       }
 
       // ---- masks, where the tile reaches past what every row attends or has no page
-      const bool whole = t >= lo_max && t + S::kTile <= hi_min && __all(held);
+      const bool whole = t >= rw.lo_max && t + S::kTile <= rw.hi_min && __all(held);
       bool mixed = false;                                  // a non-finite value that only some rows attend
       if (!whole) {
 #pragma unroll
         for (int i = 0; i < S::kPos; ++i) {
           const int pos = t + vpos + i;
           if (!(held && pos >= lo && pos < hi)) xs[i] = -INFINITY;
-          const bool any = held && pos >= lo_min && pos < hi_max, all = held && pos >= lo_max && pos < hi_min;
+          // a value that not every row attends may have to count for some: 0 times it has to be 0
+          // for the others, whatever it is
+          const bool any = held && pos >= rw.lo_min && pos < rw.hi_max, all = held && pos >= rw.lo_max && pos < rw.hi_min;
+          if (!all) {
 #pragma unroll
-          for (int c = 0; c < S::kSets; ++c)
+            for (int c = 0; c < S::kSets; ++c)
 #pragma unroll
-            for (int w = 0; w < S::kVWords; ++w) {
-              if (!any) vw[i][c][w] = 0;                   // whatever lies there, 0 times it has to be 0
-              if (any && !all) mixed = mixed || any_nonfinite<FMT>(vw[i][c][w]);
-            }
+              for (int w = 0; w < S::kVWords; ++w) {
+                const uint32_t bad = nonfinite<FMT>(vw[i][c][w]);
+                mixed = mixed || (any && bad != 0);
+                vw[i][c][w] &= ~bad;
+              }
+          }
         }
         mixed = __any(mixed);
       }
@@ -402,74 +443,68 @@ __global__ void __launch_bounds__(kThreads, D == 256 && FMT == kF32 ? 1 : 2) gdn
       }
 
       // ---- O^T += V^T P^T
-      half8_t pw;
-      if constexpr (FMT != kF32) {
+      if constexpr (FMT == kF32) {
+#pragma unroll
+        for (int c = 0; c < S::kSets; ++c)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              acc[4 * c + e] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(vw[i][c][e]), wgt[i], acc[4 * c + e], 0, 0, 0);
+      } else {
+        half8_t pw;
 #pragma unroll
         for (int i = 0; i < 8; ++i) pw[i] = (_Float16)wgt[i];
+#pragma unroll
+        for (int c = 0; c < S::kSets; ++c)
+#pragma unroll
+          for (int k = 0; k < S::kCols / 2; ++k) {         // two columns at a time
+            uint32_t pair[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              if constexpr (FMT == kF16)
+                pair[i] = vw[i][c][k];
+              else
+                pair[i] = (k & 1) ? codes_to_half2<true>(vw[i][c][k >> 1]) : codes_to_half2<false>(vw[i][c][k >> 1]);
+            }
+            uint4_t a0, a1;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              a0[i] = __builtin_amdgcn_perm(pair[2 * i + 1], pair[2 * i], 0x05040100u);
+              a1[i] = __builtin_amdgcn_perm(pair[2 * i + 1], pair[2 * i], 0x07060302u);
+            }
+            const int o = S::kCols * c + 2 * k;
+            acc[o] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8_t, a0), pw, acc[o], 0, 0, 0);
+            acc[o + 1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8_t, a1), pw, acc[o + 1], 0, 0, 0);
+          }
       }
-      // `seen`: a mask per position of what to keep of v; the sums of lanes with keep false stay
-      auto product = [&](auto all, const uint32_t (&seen)[S::kPos], bool keep) {
-        constexpr bool kAll = decltype(all)::value;
-        auto add = [&](int o, const float4_t& x) {
-          if constexpr (kAll) {
-            acc[o] = x;
-          } else {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) acc[o][e] = keep ? x[e] : acc[o][e];
-          }
-        };
-        if constexpr (FMT == kF32) {
-#pragma unroll
-          for (int c = 0; c < S::kSets; ++c)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              float4_t x = acc[4 * c + e];
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                x = __builtin_amdgcn_mfma_f32_16x16x4f32(
-                    __uint_as_float(kAll ? vw[i][c][e] : vw[i][c][e] & seen[i]), wgt[i], x, 0, 0, 0);
-              add(4 * c + e, x);
-            }
-        } else {
-#pragma unroll
-          for (int c = 0; c < S::kSets; ++c)
-#pragma unroll
-            for (int q2 = 0; q2 < S::kCols / 2; ++q2) {    // two columns at a time
-              uint32_t pair[8];
-#pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                if constexpr (FMT == kF16)
-                  pair[i] = vw[i][c][q2];
-                else
-                  pair[i] = (q2 & 1) ? codes_to_half2<true>(vw[i][c][q2 >> 1]) : codes_to_half2<false>(vw[i][c][q2 >> 1]);
-                if constexpr (!kAll) pair[i] &= seen[i];
-              }
-              uint4_t a0, a1;
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                a0[i] = __builtin_amdgcn_perm(pair[2 * i + 1], pair[2 * i], 0x05040100u);
-                a1[i] = __builtin_amdgcn_perm(pair[2 * i + 1], pair[2 * i], 0x07060302u);
-              }
-              const int o = S::kCols * c + 2 * q2;
-              add(o, __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8_t, a0), pw, acc[o], 0, 0, 0));
-              add(o + 1, __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8_t, a1), pw, acc[o + 1], 0, 0, 0));
-            }
-        }
-      };
-      uint32_t seen[S::kPos] = {};
-      if (!mixed) {
-        product(std::true_type{}, seen, true);
-      } else {
-        // a row at a time, with the values it does not attend taken out
+      if (mixed) {
+        // the values left out above, for the rows that attend them: position by position, element by
+        // element, from memory
 #pragma unroll 1
-        for (int k = 0; k < rows; ++k) {
-          const int row_hi = __shfl(hi, k), row_lo = __shfl(lo, k);
+        for (int at = 0; at < S::kTile; ++at) {
+          const int page = page_of(p, table, t + at);
+          if (page < 0) continue;
+          float own = wgt[0];
 #pragma unroll
-          for (int i = 0; i < S::kPos; ++i) {
-            const int pos = t + vpos + i;
-            seen[i] = pos >= row_lo && pos < row_hi ? 0xffffffffu : 0u;
-          }
-          product(std::false_type{}, seen, n == k);
+          for (int i = 1; i < S::kPos; ++i) own = at % S::kPos == i ? wgt[i] : own;
+          const float w = __shfl(own, n + 16 * (at / S::kPos));
+          const bool sees = t + at >= lo && t + at < hi && !(t + at >= rw.lo_max && t + at < rw.hi_min);
+          const char* row = static_cast<const char*>(p.cache.v) +
+                            ((((int64_t)page * p.cache.Hk + h) << p.cache.page_shift) + ((t + at) & in_page)) * (D * S::kBytes);
+#pragma unroll
+          for (int c = 0; c < S::kSets; ++c)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              __builtin_amdgcn_sched_barrier(0);
+              uint32_t words[S::kVWords];
+              load_words(row + S::kCols * S::kBytes * (16 * c + 4 * g + i), words);
+#pragma unroll
+              for (int e = 0; e < S::kCols; ++e) {
+                const float v = element<FMT>(words, e);
+                if (sees && !(fabsf(v) < INFINITY)) acc[S::kCols * c + e][i] = fmaf(w, v, acc[S::kCols * c + e][i]);
+              }
+            }
         }
       }
     }
@@ -482,9 +517,9 @@ __global__ void __launch_bounds__(kThreads, D == 256 && FMT == kF32 ? 1 : 2) gdn
       stats[wave][n][1] = l;
     }
     __syncthreads();
-    const int w0 = sub * streams;                          // the waves of this wave's tile
-    float top = M;
-    for (int w = w0; w < w0 + streams; ++w) top = fmaxf(top, stats[w][n][0]);
+    float top = stats[0][n][0];
+#pragma unroll
+    for (int w = 1; w < kWaves; ++w) top = fmaxf(top, stats[w][n][0]);
     const float f = M == -INFINITY ? 0.f : exp2_fast(M - top);
     // acc[cols c + e] of row n, register i: column 16 cols c + cols (4 g + i) + e
 #pragma unroll
@@ -497,20 +532,21 @@ __global__ void __launch_bounds__(kThreads, D == 256 && FMT == kF32 ? 1 : 2) gdn
               float4_t{acc[S::kCols * c + e][i] * f, acc[S::kCols * c + e + 1][i] * f, acc[S::kCols * c + e + 2][i] * f,
                        acc[S::kCols * c + e + 3][i] * f};
     __syncthreads();
-    const bool complete = c0 == 0 && c1 == s.chunks;
     float* part = complete ? nullptr
-                           : sp.parts + (2 * (int64_t)blockIdx.x + (c0 == 0 ? 1 : 0)) * (sp.part_rows * (D + 2));
-    for (int i = tid; i < seg_rows * (D / 4); i += kThreads) {
-      const int rr = i / (D / 4), d = 4 * (i - rr * (D / 4)), rn = rr % kRows, from = rr / kRows * streams;
-      float best = stats[from][rn][0], sum = 0.f;
-      for (int w = from + 1; w < from + streams; ++w) best = fmaxf(best, stats[w][rn][0]);
+                           : sp.parts + (2 * (int64_t)blockIdx.x + (sg.c0 == 0 ? 1 : 0)) * (sp.part_rows * (D + 2));
+    for (int i = tid; i < rows * (D / 4); i += kThreads) {
+      const int rr = i / (D / 4), d = 4 * (i - rr * (D / 4));
+      float best = stats[0][rr][0], sum = 0.f;
+#pragma unroll
+      for (int w = 1; w < kWaves; ++w) best = fmaxf(best, stats[w][rr][0]);
       float4_t o = float4_t{0.f, 0.f, 0.f, 0.f};
-      for (int w = from; w < from + streams; ++w) {
-        sum += stats[w][rn][0] == -INFINITY ? 0.f : stats[w][rn][1] * exp2_fast(stats[w][rn][0] - best);
-        o += *reinterpret_cast<const float4_t*>(&sums[w][rn][d]);
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) {
+        sum += stats[w][rr][0] == -INFINITY ? 0.f : stats[w][rr][1] * exp2_fast(stats[w][rr][0] - best);
+        o += *reinterpret_cast<const float4_t*>(&sums[w][rr][d]);
       }
       if (complete) {
-        const int grow = seg_row + rr, jj = grow / p.group;
+        const int grow = sg.seg_row + rr, jj = grow / p.group;
         IO* out = static_cast<IO*>(p.output) + ((int64_t)(s.start + jj) * p.Hq + h * p.group + grow - jj * p.group) * D + d;
         const float norm = sum == 0.f ? 0.f : 1.f / sum;
         if constexpr (FMT == kF32)
@@ -529,6 +565,470 @@ __global__ void __launch_bounds__(kThreads, D == 256 && FMT == kF32 ? 1 : 2) gdn
   }
 }
 
+template <int FMT, int D>
+struct RingShape {
+  static constexpr int kBytes = FMT == kF32 ? 4 : FMT == kF16 ? 2 : 1;   // of a cache element
+  static constexpr int kRow = D * kBytes;                                // bytes of a position's k or v
+  static constexpr int kStage = kRow >= 512 ? 16 : 8192 / kRow;          // positions of a stage: 16 KiB of k and v
+  static constexpr int kStageBytes = 2 * kStage * kRow;                  // (32 KiB for fp32 at D = 256)
+  static constexpr int kBufs = 65536 / kStageBytes;
+  static constexpr int kTilesPerStage = kStage / 16;
+  static constexpr int kGroupLoads = 16 * kRow / 1024;                   // 1 KiB loads of 16 positions' k or v
+  static constexpr int kLoads = 2 * kTilesPerStage * kGroupLoads + (FMT == kE4M3 ? 1 : 0);   // of a stage
+  static constexpr int kUnits = kRow / 16;                               // 16-byte units of a row
+  // columns of v a lane holds: sets of kCols neighbours, 16 * kCols apart
+  static constexpr int kCols = FMT == kF32 ? 4 : FMT == kF16 ? (D / 16 < 8 ? D / 16 : 8) : D / 16;
+  static constexpr int kSets = D / (16 * kCols);
+  static constexpr int kVWords = kCols * kBytes / 4;                     // dwords of a set in one position
+  // reads of this many 16-byte units are put in flight together where registers are scarce
+  static constexpr bool kFew = FMT == kF32 ? D >= 128 : D == 256;
+  static_assert(kLoads * (kBufs - 1) < 64, "vmcnt holds 6 bits");
+};
+
+// 16-byte unit u of row r (r = position mod 16) of a stage is stored at unit
+// u ^ swizzle(r): the 16 rows that a k fragment takes at one u, and the units of one
+// row that a v fragment takes, then fall in distinct banks.
+template <int UNITS>
+__device__ __forceinline__ int swizzle(int r) {
+  return UNITS >= 16 ? r : UNITS == 8 ? r >> 1 : r >> 2;
+}
+
+typedef __attribute__((address_space(3))) void lds_void_t;
+typedef __attribute__((address_space(1))) const void global_void_t;
+
+// The loader's view of the hand-over counters. In inline assembly, so that the
+// compiler does not make the loader wait for its direct loads (which write LDS too)
+// at every access.
+__device__ __forceinline__ void lds_store(uint32_t at, int x) {
+  asm volatile("ds_write_b32 %0, %1" ::"v"(at), "v"(x) : "memory");
+}
+__device__ __forceinline__ int lds_min4(uint32_t at) {
+  uint4_t x;
+  asm volatile("ds_read_b128 %0, %1\n\ts_waitcnt lgkmcnt(0)" : "=&v"(x) : "v"(at) : "memory");
+  const int a = min((int)x[0], (int)x[1]), b = min((int)x[2], (int)x[3]);
+  return __builtin_amdgcn_readfirstlane(min(a, b));
+}
+__device__ __forceinline__ uint32_t lds_address(const void* p) {
+  return (uint32_t)(uintptr_t)(lds_void_t*)p;
+}
+
+// Waits until at most n stages of kLoads direct loads are in flight (n < kBufs).
+template <int LOADS, int N>
+__device__ __forceinline__ void wait_in_flight(int n) {
+  if constexpr (N == 0) {
+    __builtin_amdgcn_s_waitcnt((7 << 4) | (15 << 8));                     // vmcnt(0)
+  } else {
+    constexpr int k = LOADS * N;
+    if (n >= N)
+      __builtin_amdgcn_s_waitcnt((k & 15) | (7 << 4) | (15 << 8) | ((k >> 4) << 14));
+    else
+      wait_in_flight<LOADS, N - 1>(n);
+  }
+}
+
+constexpr int kStream = 2;                // cache policy of the loads: nontemporal, each byte is used once
+
+// Copies positions t .. t + kStage - 1 of one request and key head into a stage:
+// [k rows | v rows], zeros from position `end` on and where there is no page.
+template <int FMT, int D>
+struct Loader {
+  typedef RingShape<FMT, D> S;
+  const AttnArgs& p;
+  const __attribute__((address_space(4))) int32_t* table;                // read through the scalar cache
+  int h, end, lane;
+
+  // The pages of the positions from t on, 16 by 16; -1 where there is none. All entries are asked for
+  // before any is looked at, and a stage ahead: the scalar cache takes hundreds of cycles.
+  __device__ __forceinline__ void look_up(int t, int (&pages)[S::kTilesPerStage]) const {
+#pragma unroll
+    for (int q = 0; q < S::kTilesPerStage; ++q)
+      pages[q] = table[min((t + 16 * q) >> p.cache.page_shift, p.cache.max_pages - 1)];
+#pragma unroll
+    for (int q = 0; q < S::kTilesPerStage; ++q)
+      pages[q] = ((t + 16 * q) >> p.cache.page_shift) < p.cache.max_pages && pages[q] < p.cache.num_pages ? pages[q] : -1;
+  }
+  __device__ __forceinline__ int64_t first_row(int pg, int pos) const {
+    return (((int64_t)pg * p.cache.Hk + h) << p.cache.page_shift) + (pos & ((1 << p.cache.page_shift) - 1));
+  }
+
+  // Returns a bit per 16 positions that have a page.
+  __device__ __forceinline__ int issue(int t, const int (&pages)[S::kTilesPerStage], char* stage, uint8_t* scales) const {
+    constexpr int kRowsPerLoad = 1024 / S::kRow;
+    const int lrow = lane / S::kUnits, slot = lane % S::kUnits;
+    int held = 0;
+#pragma unroll
+    for (int q = 0; q < S::kTilesPerStage; ++q) held |= pages[q] >= 0 ? 1 << q : 0;
+#pragma unroll
+    for (int q = 0; q < S::kTilesPerStage; ++q) {
+      const int pos = t + 16 * q, pg = pages[q];
+      const int rows = __builtin_amdgcn_readfirstlane(pg >= 0 ? min(max(end - pos, 0), 16) : 0);
+      const int64_t at = first_row(max(pg, 0), pos) * S::kRow;
+      const rsrc_t rk = make_rsrc(static_cast<const char*>(p.cache.k) + at, rows * S::kRow);
+      const rsrc_t rv = make_rsrc(static_cast<const char*>(p.cache.v) + at, rows * S::kRow);
+#pragma unroll
+      for (int i = 0; i < S::kGroupLoads; ++i) {
+        const int row = kRowsPerLoad * i + lrow;
+        const int off = lrow * S::kRow + 16 * (slot ^ swizzle<S::kUnits>(row));
+        char* dst = stage + (16 * q * S::kRow) + 1024 * i;
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rk, (lds_void_t*)dst, 16, off, 1024 * i, 0, kStream);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rv, (lds_void_t*)(dst + S::kStage * S::kRow), 16, off, 1024 * i, 0,
+                                                 kStream);
+      }
+    }
+    if constexpr (FMT == kE4M3) {
+      // the exponent bytes, 4 positions a lane: k's, then v's
+      constexpr int kWords = S::kStage / 4;
+      if (lane < 2 * kWords) {
+        const int w = lane % kWords;
+        int pg = pages[0];
+#pragma unroll
+        for (int q = 1; q < S::kTilesPerStage; ++q) pg = (w >> 2) == q ? pages[q] : pg;
+        const uint8_t* src = (lane < kWords ? p.cache.k_scales : p.cache.v_scales) + first_row(max(pg, 0), t + 4 * w);
+        __builtin_amdgcn_global_load_lds((global_void_t*)src, (lds_void_t*)scales, 4, 0, 0);
+      }
+    }
+    return held;
+  }
+};
+
+template <int FMT, int D>
+__global__ void __launch_bounds__(kBlock, 3) gdn_attn_rows_k(AttnArgs p, SplitArgs sp) {
+  typedef RingShape<FMT, D> S;
+  typedef typename std::conditional<FMT == kF32, float, _Float16>::type IO;
+  constexpr int kAcc = S::kSets * S::kCols;                // 16 x 16 blocks of the output
+  __shared__ __attribute__((aligned(16))) char ring[S::kBufs][S::kStageBytes];
+  __shared__ __attribute__((aligned(16))) uint8_t scale_ring[FMT == kE4M3 ? S::kBufs : 1][FMT == kE4M3 ? 2 * S::kStage : 16];
+  __shared__ __attribute__((aligned(16))) int finished[kWaves];   // stages a wave is done with
+  __shared__ int landed;                                          // stages in LDS
+  __shared__ int held[S::kBufs];                                  // a stage's 16-position groups that have a page
+  __shared__ float stats[kWaves][kRows][2];
+  static_assert(sizeof(float) * kWaves * kRows * D <= sizeof(ring), "the waves' sums are joined in the ring");
+
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int n = lane & 15, g = lane >> 4;
+
+  Share w = find_share(p, sp, lane, blockIdx.x == 0 && wave == 0 && sp.prefix != nullptr);
+  if (tid < kWaves) finished[tid] = 0;
+  if (tid == 0) landed = 0;
+  __syncthreads();
+  const float to_log2 = p.scale * 1.4426950408889634f;
+  int stage0 = 0;                                          // stages of the segments before this one
+
+  while (w.u < w.u_end) {
+    const Segment sg = next_segment(p, sp, w);
+    const Plan& s = sg.s;
+    const int h = sg.h, seg_row = sg.seg_row, seg_rows = sg.rows, t0 = sg.t0, end = sg.end;
+    const int stages = end > t0 ? (end - t0 + S::kStage - 1) / S::kStage : 0;
+    const bool complete = sg.c0 == 0 && sg.c1 == s.chunks;
+
+    if (wave == kWaves) {
+      // ---- the loader: issue what the ring has room for, announce what has landed
+      const Loader<FMT, D> load{p, (const __attribute__((address_space(4))) int32_t*)(p.cache.table + (int64_t)w.r * p.cache.max_pages),
+                                h, end, lane};
+      const uint32_t done_at = lds_address(finished), landed_at = lds_address(&landed), held_at = lds_address(held);
+      int issued = 0, pages[S::kTilesPerStage];
+      load.look_up(t0, pages);
+      for (int i = 0; i < stages;) {
+        while (issued < stages) {
+          if (stage0 + issued - lds_min4(done_at) < S::kBufs) {
+            const int b = (stage0 + issued) % S::kBufs;
+            lds_store(held_at + 4 * b, load.issue(t0 + issued * S::kStage, pages, ring[b], scale_ring[FMT == kE4M3 ? b : 0]));
+            ++issued;
+            load.look_up(t0 + issued * S::kStage, pages);
+          } else if (issued > i) {
+            break;
+          } else {
+            __builtin_amdgcn_s_sleep(1);
+          }
+        }
+        wait_in_flight<S::kLoads, S::kBufs - 1>(issued - 1 - i);
+        lds_store(landed_at, stage0 + ++i);
+      }
+      stage0 += stages;
+      __syncthreads();                                     // A
+      __syncthreads();                                     // B
+      __syncthreads();                                     // C
+      continue;
+    }
+
+    // ---- the wave's tile and stream of positions, this lane's row, and what the tile's rows attend
+    const int streams = seg_rows <= kRows ? 4 : seg_rows <= 2 * kRows ? 2 : 1;
+    const int sub = wave / streams, stream = wave - sub * streams;
+    const int rows = max(min(kRows, seg_rows - sub * kRows), 0);       // 0: a wave without a tile
+    const int row0 = seg_row + (rows > 0 ? sub * kRows : 0);
+    const Rows rw = rows_of(p, s, row0, rows, n);
+    const int lo = rw.lo, hi = rw.hi, lo_max = rw.lo_max, hi_min = rw.hi_min;
+
+    // q as the first product's second operand, in the order k is read in
+    const IO* q = static_cast<const IO*>(p.q) + (int64_t)(s.start + rw.j) * p.q_stride +
+                  (int64_t)(h * p.group + rw.head) * D;
+    half8_t qh[FMT == kF32 ? 1 : D / 32];
+    float4_t qf[FMT == kF32 ? D / 16 : 1];
+    if constexpr (FMT == kF32) {
+#pragma unroll
+      for (int c = 0; c < D / 16; ++c) qf[c] = *reinterpret_cast<const float4_t*>(q + 16 * c + 4 * g);
+    } else {
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c)
+        qh[c] = *reinterpret_cast<const half8_t*>(
+            q + (FMT == kF16 ? 32 * c + 8 * g : 64 * (c >> 1) + 16 * g + 8 * (c & 1)));
+    }
+
+    float4_t acc[kAcc];
+#pragma unroll
+    for (int i = 0; i < kAcc; ++i) acc[i] = float4_t{0.f, 0.f, 0.f, 0.f};
+    float M = -INFINITY, l = 0.f;                          // l: this lane's positions only
+    const int tiles = rows > 0 ? stages * S::kTilesPerStage : 0;
+    if (lane == 0) *(volatile int*)&finished[wave] = stage0 + min(rows > 0 ? stream / S::kTilesPerStage : stages, stages);
+    for (int x = stream; x < tiles; x += streams) {
+      const int i = x / S::kTilesPerStage, xi = x - i * S::kTilesPerStage;
+      while (__builtin_amdgcn_readfirstlane(*(volatile int*)&landed) <= stage0 + i) __builtin_amdgcn_s_sleep(1);
+      asm volatile("" ::: "memory");
+      const int t = t0 + 16 * x;
+      const int b = (stage0 + i) % S::kBufs;
+      const char* kt = ring[b] + 16 * xi * S::kRow;
+      const char* vt = kt + S::kStage * S::kRow;
+      bool none = t >= rw.hi_max || t + 16 <= rw.lo_min;         // no row of the tile attends any of it
+      none = none || ((__builtin_amdgcn_readfirstlane(*(volatile int*)&held[b]) >> xi) & 1) == 0;
+      if (!none) {
+        // the lane's place, hidden from the compiler where registers are scarce: it then forms the LDS
+        // addresses here instead of keeping (and spilling) all of them across the loop
+        int n_ = n, g_ = g;
+        if (S::kFew) asm volatile("" : "+v"(n_), "+v"(g_));
+        // ---- scores: lane group g holds positions t + 4 g + (0 .. 3)
+        float4_t sc = float4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int c = 0; c < S::kUnits / 4; ++c) {
+          const uint4_t w = *reinterpret_cast<const uint4_t*>(kt + n_ * S::kRow + 16 * ((4 * c + g_) ^ swizzle<S::kUnits>(n_)));
+          if constexpr (FMT == kF32) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              sc = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(w[e]), qf[c][e], sc, 0, 0, 0);
+          } else if constexpr (FMT == kF16) {
+            sc = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8_t, w), qh[c], sc, 0, 0, 0);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const uint4_t v = uint4_t{codes_to_half2<false>(w[2 * e]), codes_to_half2<true>(w[2 * e]),
+                                        codes_to_half2<false>(w[2 * e + 1]), codes_to_half2<true>(w[2 * e + 1])};
+              sc = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8_t, v), qh[2 * c + e], sc, 0, 0, 0);
+            }
+          }
+          if (S::kFew && (c & 3) == 3) __builtin_amdgcn_sched_barrier(0);
+        }
+        // to base-2 exponents. With 8-bit values the weight carries the value's scale, so xs is the
+        // exponent of the product and `inv` takes the scale out of the weights' sum again; a zero row's
+        // scale counts as 2^-33, below that of every other fp16 row.
+        float xs[4], inv[4];
+        uint32_t kscale = 0, vscale = 0;
+        if constexpr (FMT == kE4M3) {
+          kscale = *reinterpret_cast<const uint32_t*>(scale_ring[b] + 16 * xi + 4 * g);
+          vscale = *reinterpret_cast<const uint32_t*>(scale_ring[b] + S::kStage + 16 * xi + 4 * g);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if constexpr (FMT == kE4M3) {
+            const uint32_t kb = (kscale >> (8 * e)) & 255u;
+            const uint32_t vb = max((vscale >> (8 * e)) & 255u, 94u);
+            xs[e] = fmaf(sc[e], to_log2 * __uint_as_float(kb << 23), (float)((int)vb - 127));
+            inv[e] = __uint_as_float((254u - min(vb, 253u)) << 23);
+          } else {
+            xs[e] = sc[e] * to_log2;
+          }
+        }
+
+        // ---- masks, where some row does not attend all of the tile
+        bool mixed = false;                                // a non-finite value that not every row attends
+        if (t < lo_max || t + 16 > hi_min) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int pos = t + 4 * g + e;
+            if (!(pos >= lo && pos < hi)) xs[e] = -INFINITY;
+            if (pos < lo_max || pos >= hi_min) {
+#pragma unroll
+              for (int w = 0; w < S::kUnits / 16 + (S::kUnits < 16); ++w) {
+                // this lane's share of the row: its 16 lanes hold the whole of it
+                if (S::kUnits >= 16 || n < S::kUnits) {
+                  const uint4_t v = *reinterpret_cast<const uint4_t*>(vt + (4 * g_ + e) * S::kRow + 16 * (n_ + 16 * w));
+                  mixed = mixed || (nonfinite<FMT>(v[0]) | nonfinite<FMT>(v[1]) | nonfinite<FMT>(v[2]) | nonfinite<FMT>(v[3])) != 0;
+                }
+              }
+            }
+          }
+          mixed = __any(mixed);
+        }
+
+        // ---- weights
+        float m = fmaxf(fmaxf(xs[0], xs[1]), fmaxf(xs[2], xs[3]));
+        m = fmaxf(row_max(m), M);
+        if (__any(m > M)) {
+          const float f = M == m ? 1.f : exp2_fast(M - m); // -inf - -inf is not asked for
+          l *= f;
+#pragma unroll
+          for (int k = 0; k < kAcc; ++k) acc[k] *= f;
+          M = m;
+        }
+        const float ref = M == -INFINITY ? 0.f : M;
+        float wgt[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          wgt[e] = exp2_fast(xs[e] - ref);
+          if constexpr (FMT == kE4M3)
+            l = fmaf(wgt[e], inv[e], l);
+          else
+            l += wgt[e];
+        }
+
+        // ---- O^T += V^T P^T. A lane reads the same few columns of its group's 4 positions and turns
+        // them into columns of 4 positions with byte permutes (half an instruction an element).
+        const half4_t pw = half4_t{(_Float16)wgt[0], (_Float16)wgt[1], (_Float16)wgt[2], (_Float16)wgt[3]};
+        // this lane's words of set c in position `at` for column block k (0 .. 15)
+        auto load_columns = [&](int at, int k, int c, uint32_t (&w)[S::kVWords]) {
+          const int byte = S::kCols * S::kBytes * k;
+          const char* src = vt + at * S::kRow + 16 * ((byte >> 4) ^ swizzle<S::kUnits>(at)) + (byte & 15) +
+                            16 * S::kCols * S::kBytes * c;
+          if constexpr (S::kVWords == 4) {
+            const uint4_t v = *reinterpret_cast<const uint4_t*>(src);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] = v[i];
+          } else if constexpr (S::kVWords == 2) {
+            const uint2_t v = *reinterpret_cast<const uint2_t*>(src);
+            w[0] = v[0];
+            w[1] = v[1];
+          } else {
+            w[0] = *reinterpret_cast<const uint32_t*>(src);
+          }
+        };
+#pragma unroll
+        for (int c = 0; c < S::kSets; ++c) {
+          if (S::kFew) __builtin_amdgcn_sched_barrier(0);
+          uint32_t vw[4][S::kVWords];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) load_columns(4 * g_ + e, n_, c, vw[e]);
+          if (mixed) {                                     // 0 times a value that is not finite has to be 0
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+#pragma unroll
+              for (int w = 0; w < S::kVWords; ++w) vw[e][w] &= ~nonfinite<FMT>(vw[e][w]);
+          }
+          if constexpr (FMT == kF32) {
+#pragma unroll
+            for (int w = 0; w < 4; ++w)
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                acc[4 * c + w] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(vw[e][w]), wgt[e], acc[4 * c + w], 0, 0, 0);
+          } else {
+#pragma unroll
+            for (int w = 0; w < S::kCols / 2; ++w) {       // two columns at a time
+              uint32_t pair[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                if constexpr (FMT == kF16)
+                  pair[e] = vw[e][w];
+                else
+                  pair[e] = (w & 1) ? codes_to_half2<true>(vw[e][w >> 1]) : codes_to_half2<false>(vw[e][w >> 1]);
+              }
+              const uint2_t a0 = uint2_t{__builtin_amdgcn_perm(pair[1], pair[0], 0x05040100u),
+                                         __builtin_amdgcn_perm(pair[3], pair[2], 0x05040100u)};
+              const uint2_t a1 = uint2_t{__builtin_amdgcn_perm(pair[1], pair[0], 0x07060302u),
+                                         __builtin_amdgcn_perm(pair[3], pair[2], 0x07060302u)};
+              const int o = S::kCols * c + 2 * w;
+              acc[o] = __builtin_amdgcn_mfma_f32_16x16x16f16(__builtin_bit_cast(half4_t, a0), pw, acc[o], 0, 0, 0);
+              acc[o + 1] = __builtin_amdgcn_mfma_f32_16x16x16f16(__builtin_bit_cast(half4_t, a1), pw, acc[o + 1], 0, 0, 0);
+            }
+          }
+        }
+        if (mixed) {
+          // the values left out above, for the rows that attend them: position by position, element by element
+#pragma unroll 1
+          for (int at = 0; at < 16; ++at) {
+            const float own = at & 2 ? (at & 1 ? wgt[3] : wgt[2]) : (at & 1 ? wgt[1] : wgt[0]);
+            const float w = __shfl(own, n + 16 * (at >> 2));
+            const bool sees = t + at >= lo && t + at < hi;
+#pragma unroll
+            for (int c = 0; c < S::kSets; ++c)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                __builtin_amdgcn_sched_barrier(0);
+                uint32_t words[S::kVWords];
+                load_columns(at, 4 * g_ + i, c, words);
+#pragma unroll
+                for (int e = 0; e < S::kCols; ++e) {
+                  const float v = element<FMT>(words, e);
+                  if (sees && !(fabsf(v) < INFINITY)) acc[S::kCols * c + e][i] = fmaf(w, v, acc[S::kCols * c + e][i]);
+                }
+              }
+          }
+        }
+      }
+      asm volatile("" ::: "memory");
+      const int next = min((x + streams) / S::kTilesPerStage, stages);
+      if (lane == 0) *(volatile int*)&finished[wave] = stage0 + next;
+    }
+    stage0 += stages;
+    if (lane == 0) *(volatile int*)&finished[wave] = stage0;
+
+    // ---- join the waves
+    l = row_sum(l);
+    if (g == 0) {
+      stats[wave][n][0] = M;
+      stats[wave][n][1] = l;
+    }
+    __syncthreads();                                       // A: the ring is free
+    const int w0 = sub * streams;                          // the waves of this wave's tile
+    float top = M;
+    for (int w = w0; w < w0 + streams; ++w) top = fmaxf(top, stats[w][n][0]);
+    const float f = M == -INFINITY ? 0.f : exp2_fast(M - top);
+    // acc[cols c + e] of row n, register i: column 16 cols c + cols (4 g + i) + e. The 16-byte units of
+    // a row are stored in the order of unit ^ row.
+    float* sums = reinterpret_cast<float*>(&ring[0][0]);
+    if (n < rows) {
+#pragma unroll
+      for (int c = 0; c < S::kSets; ++c)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int e = 0; e < S::kCols; e += 4) {
+            if (S::kFew) __builtin_amdgcn_sched_barrier(0);
+            const int unit = (16 * S::kCols * c + S::kCols * (4 * g + i) + e) / 4;
+            *reinterpret_cast<float4_t*>(sums + (wave * kRows + n) * D + 4 * (unit ^ n)) =
+                float4_t{acc[S::kCols * c + e][i] * f, acc[S::kCols * c + e + 1][i] * f,
+                         acc[S::kCols * c + e + 2][i] * f, acc[S::kCols * c + e + 3][i] * f};
+          }
+    }
+    __syncthreads();                                       // B
+    float* part = complete ? nullptr
+                           : sp.parts + (2 * (int64_t)blockIdx.x + (sg.c0 == 0 ? 1 : 0)) * (sp.part_rows * (D + 2));
+    for (int i = tid; i < seg_rows * (D / 4); i += kThreads) {
+      const int rr = i / (D / 4), unit = i - rr * (D / 4), d = 4 * unit, rn = rr % kRows, from = rr / kRows * streams;
+      float best = stats[from][rn][0], sum = 0.f;
+      for (int w = from + 1; w < from + streams; ++w) best = fmaxf(best, stats[w][rn][0]);
+      float4_t o = float4_t{0.f, 0.f, 0.f, 0.f};
+      for (int w = from; w < from + streams; ++w) {
+        sum += stats[w][rn][0] == -INFINITY ? 0.f : stats[w][rn][1] * exp2_fast(stats[w][rn][0] - best);
+        o += *reinterpret_cast<const float4_t*>(sums + (w * kRows + rn) * D + 4 * (unit ^ rn));
+      }
+      if (complete) {
+        const int grow = seg_row + rr, jj = grow / p.group;
+        IO* out = static_cast<IO*>(p.output) + ((int64_t)(s.start + jj) * p.Hq + h * p.group + grow - jj * p.group) * D + d;
+        const float norm = sum == 0.f ? 0.f : 1.f / sum;
+        if constexpr (FMT == kF32)
+          *reinterpret_cast<float4_t*>(out) = o * norm;
+        else
+          *reinterpret_cast<half4_t*>(out) = half4_t{(_Float16)(o[0] * norm), (_Float16)(o[1] * norm),
+                                                     (_Float16)(o[2] * norm), (_Float16)(o[3] * norm)};
+      } else {
+        *reinterpret_cast<float4_t*>(part + 2 * sp.part_rows + rr * D + d) = o;
+        if (d == 0) {
+          part[rr] = best;
+          part[sp.part_rows + rr] = sum;
+        }
+      }
+    }
+    __syncthreads();                                       // C: the ring is the loader's again
+  }
+}
+
 // Joins the parts of the segments that several workgroups shared: a workgroup per
 // (token, query head, 64 columns), its 16 slices of 16 lanes taking alternate parts.
 // Parts are few and scattered, so latency counts: a slice loads several parts at once
@@ -542,7 +1042,7 @@ __global__ void __launch_bounds__(kThreads) gdn_attn_join_k(AttnArgs p, SplitArg
   const int tid = threadIdx.x;
   const int id = (int)(blockIdx.x / kSteps), column = (int)(blockIdx.x % kSteps) * 64;
   const int n = id / p.Hq, head = id - n * p.Hq;
-  const int64_t total = sp.prefix[p.rows.R];
+  const int total = sp.prefix[p.rows.R];
   int r = 0;
   if (p.rows.cu_seqlens == nullptr) {
     r = n / p.rows.dense_len;
@@ -553,14 +1053,12 @@ __global__ void __launch_bounds__(kThreads) gdn_attn_join_k(AttnArgs p, SplitArg
       if (row_start(p.rows, mid + 1) <= n) r = mid + 1; else hi = mid;
     }
   }
-  const Plan s = plan_of(p, r, sp.chunk_shift);
+  const Plan s = plan_of(p, sp, r);
   if (n < s.start || n >= s.start + s.T) return;           // behind the last request
   const int h = head / p.group, row = (n - s.start) * p.group + head - h * p.group;
-  const int seg = row / (kTiles * kRows), rr = row - seg * (kTiles * kRows);
-  const int64_t share = share_of(total, groups);
-  const int64_t from = sp.prefix[r] + ((int64_t)h * s.segs + seg) * s.chunks;
-  const int64_t b0 = from / share;
-  const int count = (int)((from + s.chunks - 1) / share - b0) + 1;
+  const int seg = (int)((unsigned)row / (unsigned)sp.seg_rows), rr = row - seg * sp.seg_rows;
+  const unsigned share = share_of(total, groups), from = sp.prefix[r] + (h * s.segs + seg) * s.chunks;
+  const int b0 = from / share, count = (int)((from + s.chunks - 1) / share) - b0 + 1;
   if (count == 1) return;                                  // written by its one workgroup
   const int64_t size = (int64_t)sp.part_rows * (D + 2);
   const int slice = tid / kLanes, d = column + 4 * (tid - slice * kLanes);
@@ -574,7 +1072,7 @@ __global__ void __launch_bounds__(kThreads) gdn_attn_join_k(AttnArgs p, SplitArg
       // the first workgroup's part is its last segment, the others' their first; loads past
       // the last part repeat it
       const int at = min(i + k * kSlices, count - 1);
-      const float* part = sp.parts + (2 * (b0 + at) + (at == 0 ? 1 : 0)) * size;
+      const float* part = sp.parts + (2 * (int64_t)(b0 + at) + (at == 0 ? 1 : 0)) * size;
       m[k] = part[rr];
       li[k] = part[sp.part_rows + rr];
       x[k] = *reinterpret_cast<const float4_t*>(part + 2 * sp.part_rows + rr * D + d);
@@ -620,7 +1118,7 @@ __global__ void __launch_bounds__(kThreads) gdn_attn_join_k(AttnArgs p, SplitArg
         half4_t{(_Float16)(o[0] * norm), (_Float16)(o[1] * norm), (_Float16)(o[2] * norm), (_Float16)(o[3] * norm)};
 }
 
-size_t prefix_bytes(int64_t R) { return ((size_t)(R + 1) * 8 + 255) & ~(size_t)255; }
+size_t prefix_bytes(int64_t R) { return ((size_t)(R + 1) * 4 + 255) & ~(size_t)255; }
 
 // Rows of a part: a segment's, of at most kTiles tiles.
 int part_rows(int64_t N, int group) {
@@ -636,20 +1134,29 @@ constexpr int64_t kWholeGroups = 4096;
 template <int FMT, int D>
 hipError_t launch_attn_d(const AttnArgs& p, void* workspace, hipStream_t stream) {
   SplitArgs sp{};
-  if (p.max_len <= kWholeMax) {
+  const bool few = (int64_t)p.max_tokens * p.group <= kRows;
+  sp.seg_rows = few ? kRows : kTiles * kRows;
+  const int64_t segments = ((int64_t)p.rows.N * p.group / sp.seg_rows + p.rows.R) * p.cache.Hk;
+  int64_t groups = segments < kWholeGroups ? segments : kWholeGroups;
+  const bool whole = p.max_len <= kWholeMax;
+  if (whole) {
     sp.chunk_shift = kWholeShift;
-    const int64_t segments = ((int64_t)p.rows.N * p.group / (kTiles * kRows) + p.rows.R) * p.cache.Hk;
-    hipLaunchKernelGGL((gdn_attn_k<FMT, D>), dim3((unsigned)(segments < kWholeGroups ? segments : kWholeGroups)),
-                       dim3(kThreads), 0, stream, p, sp);
-    return hipGetLastError();
+  } else {
+    groups = kGroups;
+    sp.prefix = static_cast<int32_t*>(workspace);
+    sp.parts = reinterpret_cast<float*>(static_cast<char*>(workspace) + prefix_bytes(p.rows.R));
+    sp.part_rows = few ? kRows : part_rows(p.rows.N, p.group);
+    sp.chunk_shift = kChunkShift;
+    const int64_t cap = (int64_t)p.cache.max_pages << p.cache.page_shift;
+    while (segments * ((cap >> sp.chunk_shift) + 1) > ((int64_t)1 << 30)) ++sp.chunk_shift;
   }
-  sp.prefix = static_cast<int64_t*>(workspace);
-  sp.parts = reinterpret_cast<float*>(static_cast<char*>(workspace) + prefix_bytes(p.rows.R));
-  sp.part_rows = part_rows(p.rows.N, p.group);
-  sp.chunk_shift = kChunkShift;
-  hipLaunchKernelGGL((gdn_attn_k<FMT, D>), dim3(kGroups), dim3(kThreads), 0, stream, p, sp);
-  hipLaunchKernelGGL((gdn_attn_join_k<FMT, D>), dim3((unsigned)((int64_t)p.rows.N * p.Hq * (D / 64))), dim3(kThreads),
-                     0, stream, p, sp, kGroups);
+  if (few)
+    hipLaunchKernelGGL((gdn_attn_k<FMT, D>), dim3((unsigned)groups), dim3(kThreads), 0, stream, p, sp);
+  else
+    hipLaunchKernelGGL((gdn_attn_rows_k<FMT, D>), dim3((unsigned)groups), dim3(kBlock), 0, stream, p, sp);
+  if (!whole)
+    hipLaunchKernelGGL((gdn_attn_join_k<FMT, D>), dim3((unsigned)((int64_t)p.rows.N * p.Hq * (D / 64))), dim3(kThreads),
+                       0, stream, p, sp, (int)groups);
   return hipGetLastError();
 }
 

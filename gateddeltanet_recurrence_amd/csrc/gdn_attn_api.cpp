@@ -358,8 +358,8 @@ static int check_attn(const gdn_attn_params* p, const gdn_kv_cache* c, int64_t* 
   if (N < 0 || R < 0 || Hq < 1 || Hq % c->num_kv_heads != 0 || p->window < 0) return GDN_ERR_SHAPE;
   if (Hq * D > std::numeric_limits<int32_t>::max()) return GDN_ERR_SHAPE;
   if (std::isnan(p->scale) || std::isinf(p->scale)) return GDN_ERR_SHAPE;
-  // workgroups are numbered by (token, query head, 64 columns) in 32 bits
-  if ((N + R) * Hq * (D / 64) > std::numeric_limits<int32_t>::max()) return GDN_ERR_SHAPE;
+  // workgroups are numbered by (token, query head, 64 columns), and units of work counted, in 32 bits
+  if ((N + R) * Hq * (D / 64) > ((int64_t)1 << 30)) return GDN_ERR_SHAPE;
   *q_stride = token_stride(p->q_stride, Hq, D);
   return *q_stride < 0 ? GDN_ERR_SHAPE : GDN_OK;
 }
@@ -403,17 +403,17 @@ int gdn_attn_forward(const gdn_attn_params* p, const gdn_attn_tensors* t, const 
   a.q = t->q; a.output = t->output; a.q_stride = qs;
   a.Hq = (int32_t)Hq; a.group = (int32_t)(Hq / Hk); a.window = p->window;
   a.scale = p->scale > 0.f ? p->scale : 1.0f / std::sqrt((float)D);
-  // the longest request, from the mirror or else what the table holds; a window bounds it too
-  int64_t longest = (int64_t)c->max_pages * c->page_size;
-  if (w.lens_host != nullptr) longest = *std::max_element(w.lens_host, w.lens_host + R);
-  if (p->window > 0) {
-    int64_t tokens = N;
-    if (w.dense() || w.cu_host != nullptr) {
-      tokens = 0;
-      for (int64_t r = 0; r < R; ++r) tokens = std::max(tokens, w.tokens(r));
-    }
-    longest = std::min(longest, (int64_t)p->window + tokens);
+  // the most tokens of a request, and the most positions one attends, as far as they are known here: a
+  // mirror's, else what the call and the table hold
+  int64_t tokens = N, longest = (int64_t)c->max_pages * c->page_size;
+  if (w.dense()) tokens = w.dense_len();
+  if (w.cu_host != nullptr) {
+    tokens = 0;
+    for (int64_t r = 0; r < R; ++r) tokens = std::max(tokens, w.tokens(r));
   }
+  if (w.lens_host != nullptr) longest = *std::max_element(w.lens_host, w.lens_host + R);
+  if (p->window > 0) longest = std::min(longest, (int64_t)p->window + tokens);
+  a.max_tokens = (int32_t)tokens;
   a.max_len = (int32_t)longest;
   a.cache = cache_args(*c);
   a.rows = row_args(w);
