@@ -61,11 +61,12 @@ typedef uint32_t uint2_t __attribute__((ext_vector_type(2)));
 typedef uint32_t uint4_t __attribute__((ext_vector_type(4)));
 
 struct SplitArgs {
-  int32_t* prefix;                        // [R + 1] units before a request; null: nothing is split
+  int4* notes;                            // of the segments that may be split (see note_segment); null: none is
   float* parts;                           // [2 * groups][part_rows * (D + 2)]: M, l, sums
   int32_t part_rows;
   int32_t seg_rows;                       // rows of a segment: 16 or 64
   int32_t chunk_shift;
+  int32_t max_segs;                       // > 0: notes by segment, this many of a request and key head; 0: by workgroup
 };
 
 // What a request brings: its rows, the positions any of them attends and its units.
@@ -94,7 +95,9 @@ __device__ __forceinline__ Plan plan_of(const AttnArgs& p, const SplitArgs& sp, 
 // The launch bounds the units of all requests by 2^30.
 __device__ __forceinline__ int units_of(const Plan& s, int Hk) { return s.segs * Hk * s.chunks; }
 
-__device__ __forceinline__ int share_of(int total, int groups) { return max((int)((unsigned)(total + groups - 1) / (unsigned)groups), 1); }
+__device__ __forceinline__ int share_of(int total, int groups) {
+  return max((int)((unsigned)(total + groups - 1) / (unsigned)groups), 1);
+}
 
 // Inclusive sum over the lanes of a wave.
 __device__ __forceinline__ int wave_scan(int x) {
@@ -108,13 +111,12 @@ __device__ __forceinline__ int wave_scan(int x) {
 }
 
 // This workgroup's share [u, u_end) of the units, and the request r that holds u,
-// whose units begin at r_first. Every wave finds it by itself. Workgroup 0 leaves
-// the prefix sums for the join.
+// whose units begin at r_first. Every wave finds it by itself.
 struct Share {
-  int u, u_end, r, r_first;
+  int u, u_end, r, r_first, size;
 };
 
-__device__ __forceinline__ Share find_share(const AttnArgs& p, const SplitArgs& sp, int lane, bool leave) {
+__device__ __forceinline__ Share find_share(const AttnArgs& p, const SplitArgs& sp, int lane) {
   const int R = p.rows.R, per = (R + 63) >> 6;             // requests a lane sums
   const int r0 = min(lane * per, R), r1 = min(r0 + per, R);
   int mine = 0;
@@ -123,18 +125,10 @@ __device__ __forceinline__ Share find_share(const AttnArgs& p, const SplitArgs& 
   const int after = wave_scan(mine), before = after - mine;
   const int total = __builtin_amdgcn_readlane(after, 63);
   Share w;
-  const int share = share_of(total, (int)gridDim.x);
-  w.u = min((int)blockIdx.x * share, total);               // groups * share < total + groups
+  const int share = w.size = share_of(total, (int)gridDim.x);
+  w.u = (int)min((int64_t)blockIdx.x * share, (int64_t)total);
   w.u_end = min(w.u + share, total);
   w.r = w.r_first = 0;
-  if (leave) {
-    int at = before;
-    for (int r = r0; r < r1; ++r) {
-      sp.prefix[r] = at;
-      at += units_of(plan_of(p, sp, r), p.cache.Hk);
-    }
-    if (lane == 63) sp.prefix[R] = total;
-  }
   if (w.u >= w.u_end) return w;
   const int holder = __builtin_ctzll(__ballot(w.u >= before && w.u < after));
   w.r = holder * per;
@@ -148,6 +142,7 @@ struct Segment {
   Plan s;
   int h, seg_row, rows, c0, c1;
   int t0, end;                                             // positions [t0, end)
+  int note, parts;                                         // its place among the notes, the shares that hold it
 };
 
 __device__ __forceinline__ Segment next_segment(const AttnArgs& p, const SplitArgs& sp, Share& w) {
@@ -162,6 +157,9 @@ __device__ __forceinline__ Segment next_segment(const AttnArgs& p, const SplitAr
   x.c1 = min(x.s.chunks, x.c0 + (w.u_end - w.u));
   x.h = seg / (unsigned)x.s.segs;
   x.seg_row = (int)(seg - x.h * x.s.segs) * sp.seg_rows;
+  x.note = sp.max_segs > 0 ? (w.r * p.cache.Hk + x.h) * sp.max_segs + (int)(seg - x.h * x.s.segs) : (int)blockIdx.x;
+  // the shares from this one on that hold the segment, which begins in this one if c0 = 0
+  x.parts = (int)((unsigned)(w.u - x.c0 + x.s.chunks - 1) / (unsigned)w.size) - (int)blockIdx.x + 1;
   w.u += x.c1 - x.c0;
   x.rows = min(sp.seg_rows, x.s.T * p.group - x.seg_row);
   const int cap = p.cache.max_pages << p.cache.page_shift;
@@ -169,6 +167,15 @@ __device__ __forceinline__ Segment next_segment(const AttnArgs& p, const SplitAr
   x.t0 = x.s.base + (int)((int64_t)x.c0 << sp.chunk_shift);
   x.end = (int)min((int64_t)x.s.base + ((int64_t)x.c1 << sp.chunk_shift), (int64_t)clamp_pos(past_last, cap));
   return x;
+}
+
+// The workgroup that begins a segment notes what the join has to know of it: the
+// parts, the first of them, where the rows belong. In the order of workgroups there
+// is one note each, of the last segment that it begins and leaves to others.
+__device__ __forceinline__ void note_segment(const SplitArgs& sp, const Segment& x) {
+  const int parts = x.c0 == 0 && x.c1 == x.s.chunks ? 0 : x.parts;
+  sp.notes[2 * x.note] = int4{parts, (int)blockIdx.x, x.rows, x.seg_row};
+  sp.notes[2 * x.note + 1] = int4{x.s.start, x.h, 0, 0};
 }
 
 // A lane's row of a tile of `rows` rows from row0 on, and the positions that the
@@ -283,12 +290,14 @@ __global__ void __launch_bounds__(kThreads, D == 256 && FMT == kF32 ? 1 : 2) gdn
 
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int n = lane & 15, g = lane >> 4;
-  Share sh = find_share(p, sp, lane, blockIdx.x == 0 && wave == 0 && sp.prefix != nullptr);
+  Share sh = find_share(p, sp, lane);
   const float to_log2 = p.scale * 1.4426950408889634f;
   const IO* __restrict__ qs = static_cast<const IO*>(p.q);
+  if (tid == 0 && sp.notes != nullptr && sp.max_segs == 0) sp.notes[2 * blockIdx.x] = int4{0, 0, 0, 0};
 
   while (sh.u < sh.u_end) {
     const Segment sg = next_segment(p, sp, sh);
+    if (tid == 0 && sp.notes != nullptr && sg.c0 == 0 && (sp.max_segs > 0 || sg.c1 < sg.s.chunks)) note_segment(sp, sg);
     const Plan& s = sg.s;
     const int h = sg.h, rows = sg.rows, t1 = sg.end;
     const bool complete = sg.c0 == 0 && sg.c1 == s.chunks;
@@ -707,15 +716,17 @@ __global__ void __launch_bounds__(kBlock, 3) gdn_attn_rows_k(AttnArgs p, SplitAr
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int n = lane & 15, g = lane >> 4;
 
-  Share w = find_share(p, sp, lane, blockIdx.x == 0 && wave == 0 && sp.prefix != nullptr);
+  Share w = find_share(p, sp, lane);
   if (tid < kWaves) finished[tid] = 0;
   if (tid == 0) landed = 0;
   __syncthreads();
   const float to_log2 = p.scale * 1.4426950408889634f;
   int stage0 = 0;                                          // stages of the segments before this one
+  if (tid == 0 && sp.notes != nullptr && sp.max_segs == 0) sp.notes[2 * blockIdx.x] = int4{0, 0, 0, 0};
 
   while (w.u < w.u_end) {
     const Segment sg = next_segment(p, sp, w);
+    if (tid == 0 && sp.notes != nullptr && sg.c0 == 0 && (sp.max_segs > 0 || sg.c1 < sg.s.chunks)) note_segment(sp, sg);
     const Plan& s = sg.s;
     const int h = sg.h, seg_row = sg.seg_row, seg_rows = sg.rows, t0 = sg.t0, end = sg.end;
     const int stages = end > t0 ? (end - t0 + S::kStage - 1) / S::kStage : 0;
@@ -752,7 +763,8 @@ __global__ void __launch_bounds__(kBlock, 3) gdn_attn_rows_k(AttnArgs p, SplitAr
     }
 
     // ---- the wave's tile and stream of positions, this lane's row, and what the tile's rows attend
-    const int streams = seg_rows <= kRows ? 4 : seg_rows <= 2 * kRows ? 2 : 1;
+    // at most 2 stages of the ring are in use at a time, whatever the tiles of a stage
+    const int streams = seg_rows <= kRows ? min(4, 2 * S::kTilesPerStage) : seg_rows <= 2 * kRows ? 2 : 1;
     const int sub = wave / streams, stream = wave - sub * streams;
     const int rows = max(min(kRows, seg_rows - sub * kRows), 0);       // 0: a wave without a tile
     const int row0 = seg_row + (rows > 0 ? sub * kRows : 0);
@@ -778,7 +790,8 @@ __global__ void __launch_bounds__(kBlock, 3) gdn_attn_rows_k(AttnArgs p, SplitAr
 #pragma unroll
     for (int i = 0; i < kAcc; ++i) acc[i] = float4_t{0.f, 0.f, 0.f, 0.f};
     float M = -INFINITY, l = 0.f;                          // l: this lane's positions only
-    const int tiles = rows > 0 ? stages * S::kTilesPerStage : 0;
+    // `end` is a multiple of 128, or ends what the rows attend: a tile past it belongs to the next share
+    const int tiles = rows > 0 && end > t0 ? (end - t0 + 15) / 16 : 0;
     if (lane == 0) *(volatile int*)&finished[wave] = stage0 + min(rows > 0 ? stream / S::kTilesPerStage : stages, stages);
     for (int x = stream; x < tiles; x += streams) {
       const int i = x / S::kTilesPerStage, xi = x - i * S::kTilesPerStage;
@@ -796,26 +809,27 @@ __global__ void __launch_bounds__(kBlock, 3) gdn_attn_rows_k(AttnArgs p, SplitAr
         int n_ = n, g_ = g;
         if (S::kFew) asm volatile("" : "+v"(n_), "+v"(g_));
         // ---- scores: lane group g holds positions t + 4 g + (0 .. 3)
-        float4_t sc = float4_t{0.f, 0.f, 0.f, 0.f};
+        float4_t sc = float4_t{0.f, 0.f, 0.f, 0.f}, sd = sc;  // two chains of products
 #pragma unroll
         for (int c = 0; c < S::kUnits / 4; ++c) {
           const uint4_t w = *reinterpret_cast<const uint4_t*>(kt + n_ * S::kRow + 16 * ((4 * c + g_) ^ swizzle<S::kUnits>(n_)));
           if constexpr (FMT == kF32) {
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              sc = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(w[e]), qf[c][e], sc, 0, 0, 0);
+              (e & 1 ? sd : sc) = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(w[e]), qf[c][e], e & 1 ? sd : sc, 0, 0, 0);
           } else if constexpr (FMT == kF16) {
-            sc = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8_t, w), qh[c], sc, 0, 0, 0);
+            (c & 1 ? sd : sc) = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8_t, w), qh[c], c & 1 ? sd : sc, 0, 0, 0);
           } else {
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
               const uint4_t v = uint4_t{codes_to_half2<false>(w[2 * e]), codes_to_half2<true>(w[2 * e]),
                                         codes_to_half2<false>(w[2 * e + 1]), codes_to_half2<true>(w[2 * e + 1])};
-              sc = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8_t, v), qh[2 * c + e], sc, 0, 0, 0);
+              (e & 1 ? sd : sc) = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8_t, v), qh[2 * c + e], e & 1 ? sd : sc, 0, 0, 0);
             }
           }
           if (S::kFew && (c & 3) == 3) __builtin_amdgcn_sched_barrier(0);
         }
+        sc += sd;
         // to base-2 exponents. With 8-bit values the weight carries the value's scale, so xs is the
         // exponent of the product and `inv` takes the scale out of the weights' sum again; a zero row's
         // scale counts as 2^-33, below that of every other fp16 row.
@@ -1029,88 +1043,81 @@ __global__ void __launch_bounds__(kBlock, 3) gdn_attn_rows_k(AttnArgs p, SplitAr
   }
 }
 
-// Joins the parts of the segments that several workgroups shared: a workgroup per
-// (token, query head, 64 columns), its 16 slices of 16 lanes taking alternate parts.
-// Parts are few and scattered, so latency counts: a slice loads several parts at once
-// and joins them with a running M of its own.
-template <int FMT, int D>
-__global__ void __launch_bounds__(kThreads) gdn_attn_join_k(AttnArgs p, SplitArgs sp, int groups) {
+// Joins the parts of the segments that several workgroups shared, as noted by the
+// one that began them: a workgroup per note, kThreads / 16 / SLICES rows and 64
+// columns, SLICES slices of 16 lanes taking alternate parts of a row. Parts are few
+// and scattered, so latency counts: a slice loads several parts at once and joins
+// them with a running M of its own.
+template <int FMT, int D, int SLICES>
+__global__ void __launch_bounds__(kThreads) gdn_attn_join_k(AttnArgs p, SplitArgs sp) {
   typedef typename std::conditional<FMT == kF32, float, _Float16>::type IO;
-  constexpr int kLanes = 16, kSlices = kThreads / kLanes, kSteps = D / 64, kAhead = 4;
-  __shared__ float4_t sums[kSlices][kLanes];
-  __shared__ float stats[kSlices][2];
-  const int tid = threadIdx.x;
-  const int id = (int)(blockIdx.x / kSteps), column = (int)(blockIdx.x % kSteps) * 64;
-  const int n = id / p.Hq, head = id - n * p.Hq;
-  const int total = sp.prefix[p.rows.R];
-  int r = 0;
-  if (p.rows.cu_seqlens == nullptr) {
-    r = n / p.rows.dense_len;
-  } else {
-    int hi = p.rows.R - 1;
-    while (r < hi) {                                       // the first request that ends after n
-      const int mid = (r + hi) >> 1;
-      if (row_start(p.rows, mid + 1) <= n) r = mid + 1; else hi = mid;
-    }
+  constexpr int kLanes = 16, kRowsHere = kThreads / kLanes / SLICES, kAhead = 4;
+  __shared__ float4_t sums[kThreads];
+  __shared__ float stats[kThreads / kLanes][2];
+  const int tid = threadIdx.x, id = (int)blockIdx.x;
+  if (sp.max_segs > 0) {
+    // notes by segment: those of requests without that many rows are not written
+    const int r = id / (p.cache.Hk * sp.max_segs), seg = id % sp.max_segs;
+    const int T = row_start(p.rows, r + 1) - row_start(p.rows, r);
+    if ((int64_t)T * p.group <= (int64_t)seg * sp.seg_rows) return;
   }
-  const Plan s = plan_of(p, sp, r);
-  if (n < s.start || n >= s.start + s.T) return;           // behind the last request
-  const int h = head / p.group, row = (n - s.start) * p.group + head - h * p.group;
-  const int seg = (int)((unsigned)row / (unsigned)sp.seg_rows), rr = row - seg * sp.seg_rows;
-  const unsigned share = share_of(total, groups), from = sp.prefix[r] + (h * s.segs + seg) * s.chunks;
-  const int b0 = from / share, count = (int)((from + s.chunks - 1) / share) - b0 + 1;
-  if (count == 1) return;                                  // written by its one workgroup
+  const int4 a = sp.notes[2 * id], b = sp.notes[2 * id + 1];
+  const int count = a.x, b0 = a.y, rows = a.z, seg_row = a.w, start = b.x, h = b.y;
+  const int slot = tid / kLanes, slice = slot % SLICES;
+  const int row0 = (int)blockIdx.y * kRowsHere, rr = row0 + slot / SLICES;
+  if (count == 0 || row0 >= rows) return;
   const int64_t size = (int64_t)sp.part_rows * (D + 2);
-  const int slice = tid / kLanes, d = column + 4 * (tid - slice * kLanes);
+  const int d = (int)blockIdx.z * 64 + 4 * (tid % kLanes), mine = min(rr, rows - 1);
   float4_t o = float4_t{0.f, 0.f, 0.f, 0.f};
   float M = -INFINITY, l = 0.f;
-  for (int i = slice; i < count; i += kSlices * kAhead) {
+  for (int i = slice; i < count; i += SLICES * kAhead) {
     float m[kAhead], li[kAhead];
     float4_t x[kAhead];
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) {
       // the first workgroup's part is its last segment, the others' their first; loads past
       // the last part repeat it
-      const int at = min(i + k * kSlices, count - 1);
+      const int at = min(i + k * SLICES, count - 1);
       const float* part = sp.parts + (2 * (int64_t)(b0 + at) + (at == 0 ? 1 : 0)) * size;
-      m[k] = part[rr];
-      li[k] = part[sp.part_rows + rr];
-      x[k] = *reinterpret_cast<const float4_t*>(part + 2 * sp.part_rows + rr * D + d);
+      m[k] = part[mine];
+      li[k] = part[sp.part_rows + mine];
+      x[k] = *reinterpret_cast<const float4_t*>(part + 2 * sp.part_rows + mine * D + d);
     }
     float top = M;
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k) top = i + k * kSlices < count ? fmaxf(top, m[k]) : top;
+    for (int k = 0; k < kAhead; ++k) top = i + k * SLICES < count ? fmaxf(top, m[k]) : top;
     const float f = M == -INFINITY ? 0.f : exp2_fast(M - top);
     o *= f;
     l *= f;
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) {
-      const float w = i + k * kSlices < count && m[k] != -INFINITY ? exp2_fast(m[k] - top) : 0.f;
+      const float w = i + k * SLICES < count && m[k] != -INFINITY ? exp2_fast(m[k] - top) : 0.f;
       o += x[k] * w;
       l = fmaf(li[k], w, l);
     }
     M = top;
   }
-  sums[slice][tid - slice * kLanes] = o;
+  sums[tid] = o;
   if (tid % kLanes == 0) {
-    stats[slice][0] = M;
-    stats[slice][1] = l;
+    stats[slot][0] = M;
+    stats[slot][1] = l;
   }
   __syncthreads();
-  if (tid >= kLanes) return;
-  float top = stats[0][0];
+  if (slice != 0 || rr >= rows) return;
+  float top = M;
 #pragma unroll
-  for (int i = 1; i < kSlices; ++i) top = fmaxf(top, stats[i][0]);
+  for (int i = 1; i < SLICES; ++i) top = fmaxf(top, stats[slot + i][0]);
   o = float4_t{0.f, 0.f, 0.f, 0.f};
   l = 0.f;
 #pragma unroll
-  for (int i = 0; i < kSlices; ++i) {
-    const float f = stats[i][0] == -INFINITY ? 0.f : exp2_fast(stats[i][0] - top);
-    o += sums[i][tid] * f;
-    l = fmaf(stats[i][1], f, l);
+  for (int i = 0; i < SLICES; ++i) {
+    const float f = stats[slot + i][0] == -INFINITY ? 0.f : exp2_fast(stats[slot + i][0] - top);
+    o += sums[tid + i * kLanes] * f;
+    l = fmaf(stats[slot + i][1], f, l);
   }
   const float norm = l == 0.f ? 0.f : 1.f / l;
-  IO* out = static_cast<IO*>(p.output) + ((int64_t)n * p.Hq + head) * D + d;
+  const int row = seg_row + rr, j = (int)((unsigned)row / (unsigned)p.group);
+  IO* out = static_cast<IO*>(p.output) + ((int64_t)(start + j) * p.Hq + h * p.group + row - j * p.group) * D + d;
   if constexpr (FMT == kF32)
     *reinterpret_cast<float4_t*>(out) = o * norm;
   else
@@ -1118,7 +1125,8 @@ __global__ void __launch_bounds__(kThreads) gdn_attn_join_k(AttnArgs p, SplitArg
         half4_t{(_Float16)(o[0] * norm), (_Float16)(o[1] * norm), (_Float16)(o[2] * norm), (_Float16)(o[3] * norm)};
 }
 
-size_t prefix_bytes(int64_t R) { return ((size_t)(R + 1) * 4 + 255) & ~(size_t)255; }
+// Notes: two int4 each, at most kGroups of them.
+constexpr size_t kNoteBytes = (size_t)kGroups * 2 * sizeof(int4);
 
 // Rows of a part: a segment's, of at most kTiles tiles.
 int part_rows(int64_t N, int group) {
@@ -1134,29 +1142,41 @@ constexpr int64_t kWholeGroups = 4096;
 template <int FMT, int D>
 hipError_t launch_attn_d(const AttnArgs& p, void* workspace, hipStream_t stream) {
   SplitArgs sp{};
-  const bool few = (int64_t)p.max_tokens * p.group <= kRows;
+  const int64_t most = (int64_t)p.max_tokens * p.group;    // rows of a request and key head
+  const bool few = most <= kRows;
   sp.seg_rows = few ? kRows : kTiles * kRows;
   const int64_t segments = ((int64_t)p.rows.N * p.group / sp.seg_rows + p.rows.R) * p.cache.Hk;
   int64_t groups = segments < kWholeGroups ? segments : kWholeGroups;
   const bool whole = p.max_len <= kWholeMax;
+  int64_t notes = 0;
   if (whole) {
     sp.chunk_shift = kWholeShift;
   } else {
     groups = kGroups;
-    sp.prefix = static_cast<int32_t*>(workspace);
-    sp.parts = reinterpret_cast<float*>(static_cast<char*>(workspace) + prefix_bytes(p.rows.R));
+    sp.notes = static_cast<int4*>(workspace);
+    sp.parts = reinterpret_cast<float*>(static_cast<char*>(workspace) + kNoteBytes);
     sp.part_rows = few ? kRows : part_rows(p.rows.N, p.group);
     sp.chunk_shift = kChunkShift;
     const int64_t cap = (int64_t)p.cache.max_pages << p.cache.page_shift;
     while (segments * ((cap >> sp.chunk_shift) + 1) > ((int64_t)1 << 30)) ++sp.chunk_shift;
+    // notes by segment where there are fewer segments than workgroups
+    const int64_t segs = (most + sp.seg_rows - 1) / sp.seg_rows;
+    notes = segs * p.rows.R * p.cache.Hk;
+    if (notes <= kGroups) sp.max_segs = (int)segs; else notes = kGroups;
   }
   if (few)
     hipLaunchKernelGGL((gdn_attn_k<FMT, D>), dim3((unsigned)groups), dim3(kThreads), 0, stream, p, sp);
   else
     hipLaunchKernelGGL((gdn_attn_rows_k<FMT, D>), dim3((unsigned)groups), dim3(kBlock), 0, stream, p, sp);
-  if (!whole)
-    hipLaunchKernelGGL((gdn_attn_join_k<FMT, D>), dim3((unsigned)((int64_t)p.rows.N * p.Hq * (D / 64))), dim3(kThreads),
-                       0, stream, p, sp, (int)groups);
+  if (!whole) {
+    // 16 slices where a segment has many parts, else 2
+    const unsigned rows = (unsigned)(most < sp.seg_rows ? most : sp.seg_rows);
+    if (notes * 8 <= kGroups)
+      hipLaunchKernelGGL((gdn_attn_join_k<FMT, D, 16>), dim3((unsigned)notes, rows, D / 64), dim3(kThreads), 0, stream, p, sp);
+    else
+      hipLaunchKernelGGL((gdn_attn_join_k<FMT, D, 2>), dim3((unsigned)notes, (rows + 7) / 8, D / 64), dim3(kThreads), 0,
+                         stream, p, sp);
+  }
   return hipGetLastError();
 }
 
@@ -1180,7 +1200,7 @@ hipError_t launch_attn(const AttnArgs& p, int io_dtype, void* workspace, hipStre
 
 size_t attn_workspace_bytes(int64_t N, int64_t R, int Hq, int Hk, int D) {
   if (N == 0 || R == 0) return 0;
-  return prefix_bytes(R) + (size_t)2 * kGroups * part_rows(N, Hq / Hk) * (D + 2) * sizeof(float);
+  return kNoteBytes + (size_t)2 * kGroups * part_rows(N, Hq / Hk) * (D + 2) * sizeof(float);
 }
 
 }  // namespace gdn
