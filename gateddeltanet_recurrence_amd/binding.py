@@ -221,9 +221,15 @@ def make_params(N, R, Hk, Hv, Dk, Dv, io_dtype, *, scale=0.0, chunk=0, capacity=
 
 
 # ------------------------------------------------------------------ helpers
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _io_code(dtype) -> int:
@@ -256,7 +262,9 @@ def _need(x, name, shape, dtype=None):
 
 def _stream_handle(stream) -> Optional[int]:
     if stream is None:
-        return int(_torch().cuda.current_stream().cuda_stream)
+        # the raw handle: making the Stream object of torch.cuda.current_stream() takes 2.7 us
+        c = _torch()._C
+        return c._cuda_getCurrentRawStream(c._cuda_getDevice())
     if isinstance(stream, int):
         return stream
     return int(stream.cuda_stream)
@@ -264,9 +272,11 @@ def _stream_handle(stream) -> Optional[int]:
 
 def _host_i32(arr):
     """Keep-alive int32 host buffer and its address, from a sequence / numpy / CPU tensor."""
-    import numpy as np
     if arr is None:
         return None, None
+    import numpy as np
+    if type(arr) is np.ndarray and arr.dtype == np.int32 and arr.flags.c_contiguous:
+        return arr, arr.ctypes.data
     if hasattr(arr, "numpy") and hasattr(arr, "is_cuda"):
         if arr.is_cuda:
             raise ValueError("host mirrors must be CPU data")
@@ -769,79 +779,85 @@ class KVCache:
         if host is not None and host.shape != tuple(page_table.shape):
             raise ValueError("page_table_host must have page_table's shape")
         self.num_reqs, max_pages = page_table.shape
-        self.num_kv_heads, self.head_dim, self.device = Hk, D, k_pages.device
+        self.num_kv_heads, self.head_dim, self.index = Hk, D, k_pages.get_device()
         self._keep = (k_pages, v_pages, k_scales, v_scales, page_table, host)
         self.struct = GdnKvCache(_ptr(k_pages), _ptr(v_pages), _ptr(k_scales), _ptr(v_scales), _ptr(page_table),
                                  host_ptr, P, page_size, max_pages, Hk, D, _io_code(self.io_dtype),
                                  CACHE_E4M3 if self.e4m3 else CACHE_IO)
-        self._ref = ctypes.byref(self.struct)
 
 
-def _token_rows(x, name, heads, D, dtype, device):
-    """Token stride of x [N, heads, D] whose tokens may lie apart (0: dense): a slice of a
-    wider projection's output is taken as it is."""
-    if x.dim() != 3 or x.shape[1] != heads or x.shape[2] != D:
-        raise ValueError(f"{name}: shape {tuple(x.shape)} != expected (N, {heads}, {D})")
-    if x.dtype != dtype:
-        raise ValueError(f"{name}: dtype {x.dtype} != expected {dtype}")
-    if x.device != device:
-        raise ValueError(f"{name} is on {x.device}, expected {device}")
+# Decode calls take a few microseconds on the GPU, so the checks below are written to
+# be cheap: one attribute each, no helper objects.
+def _token_rows(x, name, heads, D, io, index):
+    """Token stride of x [N, heads, D] of type io on GPU `index`, whose tokens may lie apart
+    (0: dense): a slice of a wider projection's output is taken as it is."""
+    shape = x.shape
+    if len(shape) != 3 or shape[1] != heads or shape[2] != D:
+        raise ValueError(f"{name}: shape {tuple(shape)} != expected (N, {heads}, {D})")
+    if x.dtype is not io:
+        raise ValueError(f"{name}: dtype {x.dtype} != expected {io}")
+    if x.get_device() != index:
+        raise ValueError(f"{name} is on {x.device}, expected GPU {index}")
     if x.is_contiguous():
         return 0
-    if x.shape[0] > 1 and x.stride(2) == 1 and (heads <= 1 or x.stride(1) == D) and x.stride(0) >= heads * D:
-        return x.stride(0)
-    if x.shape[0] <= 1 and x.stride(2) == 1 and (heads <= 1 or x.stride(1) == D):
-        return 0
+    st = x.stride()
+    if st[2] == 1 and (heads <= 1 or st[1] == D):
+        if shape[0] <= 1:
+            return 0
+        if st[0] >= heads * D:
+            return st[0]
     raise ValueError(f"{name}: only the token dimension may be strided")
 
 
-def _out_rows(out, of, name, heads, D):
+def _out_rows(out, of, name):
     """An output of the rotation: dense, or `of` itself."""
-    if out is None or out.shape != of.shape or out.dtype != of.dtype or out.device != of.device:
+    if out is of:
+        return
+    if out is None or out.shape != of.shape or out.dtype is not of.dtype or out.get_device() != of.get_device():
         raise ValueError(f"{name} must have its input's shape, type and device")
     if not out.is_contiguous() and not (out.data_ptr() == of.data_ptr() and out.stride() == of.stride()):
         raise ValueError(f"{name} must be contiguous, or its input itself")
 
 
-def _on_current_device(device):
-    torch = _torch()
-    if device.type != "cuda":
+def _int_vector(x, name, n, index):
+    if x.dtype is not _torch().int32 or x.dim() != 1 or x.shape[0] != n or x.get_device() != index or \
+            not x.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 [{n}] on GPU {index}")
+    return x.data_ptr()
+
+
+def _frequencies(x, index):
+    if x is None or x.dtype is not _torch().float64 or x.dim() != 1 or x.get_device() != index or \
+            not x.is_contiguous():
+        raise ValueError(f"inv_freq must be a contiguous float64 [rotary_dim / 2] on GPU {index}")
+    return x.data_ptr()
+
+
+def _on_current_device(index):
+    if index < 0:
         raise ValueError("tensors must be GPU tensors")
-    if device.index != torch.cuda.current_device():
-        raise ValueError(f"tensors are on {device}, the current device is cuda:{torch.cuda.current_device()}")
-
-
-def _int_vector(x, name, n, device):
-    torch = _torch()
-    if x is None:
-        return
-    if x.dim() != 1 or x.shape[0] != n or x.dtype != torch.int32 or not x.is_contiguous() or x.device != device:
-        raise ValueError(f"{name} must be a contiguous int32 [{n}] on {device}")
-
-
-def _check_inv_freq(x, device):
-    torch = _torch()
-    if x is None or x.dim() != 1 or x.dtype != torch.float64 or not x.is_contiguous() or x.device != device:
-        raise ValueError(f"inv_freq must be a contiguous float64 [rotary_dim / 2] on {device}")
+    current = _torch()._C._cuda_getDevice()
+    if index != current:
+        raise ValueError(f"tensors are on GPU {index}, the current device is {current}")
 
 
 def _cache_rows(cache, seq_lens, cu_seqlens, num_reqs, cu_seqlens_host, seq_lens_host):
-    """(R, host arrays to keep alive, their addresses) of a call over a cache."""
-    R = int(num_reqs) if num_reqs is not None else \
+    """(R, seq_lens, cu_seqlens, their host mirrors as addresses, the mirrors to keep alive)."""
+    R = num_reqs if num_reqs is not None else \
         cu_seqlens.shape[0] - 1 if cu_seqlens is not None else seq_lens.shape[0]
-    dev = cache.device
+    index = cache.index
     if R > cache.num_reqs:
         raise ValueError(f"{R} requests, but page_table has {cache.num_reqs} rows")
-    _int_vector(seq_lens, "seq_lens", R, dev)
-    _int_vector(cu_seqlens, "cu_seqlens", R + 1, dev)
+    lens = _int_vector(seq_lens, "seq_lens", R, index)
+    cu = None if cu_seqlens is None else _int_vector(cu_seqlens, "cu_seqlens", R + 1, index)
     cu_h, cu_ptr = _host_i32(cu_seqlens_host)
     len_h, len_ptr = _host_i32(seq_lens_host)
     if cu_h is not None and cu_h.shape != (R + 1,):
         raise ValueError("cu_seqlens_host must have R + 1 entries")
     if len_h is not None and len_h.shape != (R,):
         raise ValueError("seq_lens_host must have R entries")
-    _on_current_device(dev)
-    return R, (cu_h, len_h), cu_ptr, len_ptr
+    _on_current_device(index)
+    return R, lens, cu, len_ptr, cu_ptr, (cu_h, len_h)
 
 
 def gdn_rope_frequencies(rotary_dim: int, *, base: float = 10000.0, scaling: int = ROPE_SCALING_NONE,
@@ -868,26 +884,29 @@ def gdn_rope_forward(q, k, positions, inv_freq, q_out, k_out, *, rope_layout: in
     q_out, k_out dense, or q, k themselves.
     """
     x = q if q is not None else k
-    if x is None:
-        raise ValueError("q or k is needed")
+    if x is None or x.dim() != 3:
+        raise ValueError("q or k [N, heads, D] is needed")
     N, _, D = x.shape
-    dev, io = x.device, x.dtype
-    Hq, Hk = (0 if y is None else y.shape[1] for y in (q, k))
-    strides = [0, 0]
-    for i, (y, out, name) in enumerate(((q, q_out, "q"), (k, k_out, "k"))):
-        if y is not None:
-            if y.shape[0] != N:
-                raise ValueError("q and k must have the same tokens")
-            strides[i] = _token_rows(y, name, y.shape[1], D, io, dev)
-            _out_rows(out, y, name + "_out", y.shape[1], D)
-    _int_vector(positions, "positions", N, dev)
-    _check_inv_freq(inv_freq, dev)
-    _on_current_device(dev)
-    params = GdnRopeParams(N, Hq, Hk, D, _io_code(io), 2 * inv_freq.shape[0], int(rope_layout), float(rope_factor),
-                           strides[0], strides[1])
-    tens = GdnRopeTensors(_ptr(q), _ptr(k), _ptr(positions), _ptr(inv_freq), _ptr(q_out) if q is not None else None,
-                          _ptr(k_out) if k is not None else None)
-    st = lib().gdn_rope_forward(ctypes.byref(params), ctypes.byref(tens), _stream_handle(stream))
+    index, io = x.get_device(), x.dtype
+    Hq = Hk = qs = ks = 0
+    qp = kp = qop = kop = None
+    if q is not None:
+        Hq, qp = q.shape[1], q.data_ptr()
+        qs = _token_rows(q, "q", Hq, D, io, index)
+        _out_rows(q_out, q, "q_out")
+        qop = q_out.data_ptr()
+    if k is not None:
+        if k.shape[0] != N:
+            raise ValueError("q and k must have the same tokens")
+        Hk, kp = k.shape[1], k.data_ptr()
+        ks = _token_rows(k, "k", Hk, D, io, index)
+        _out_rows(k_out, k, "k_out")
+        kop = k_out.data_ptr()
+    pos, freq = _int_vector(positions, "positions", N, index), _frequencies(inv_freq, index)
+    _on_current_device(index)
+    st = lib().gdn_rope_forward(
+        GdnRopeParams(N, Hq, Hk, D, _io_code(io), 2 * inv_freq.shape[0], rope_layout, rope_factor, qs, ks),
+        GdnRopeTensors(qp, kp, pos, freq, qop, kop), _stream_handle(stream))
     if check and st != GDN_OK:
         raise GDNError(st, "gdn_rope_forward")
     return st
@@ -905,29 +924,32 @@ def gdn_kv_write(k, v, cache: KVCache, seq_lens, cu_seqlens=None, *, q=None, q_o
     as it is written, and q [N, Hq, D], when given, into q_out; positions [N] int32
     default to the positions in the cache.
     """
-    Hk, D, dev, io = cache.num_kv_heads, cache.head_dim, cache.device, cache.io_dtype
+    Hk, D, index, io = cache.num_kv_heads, cache.head_dim, cache.index, cache.io_dtype
     N = k.shape[0]
-    ks, vs = _token_rows(k, "k", Hk, D, io, dev), _token_rows(v, "v", Hk, D, io, dev)
+    ks, vs = _token_rows(k, "k", Hk, D, io, index), _token_rows(v, "v", Hk, D, io, index)
     if v.shape[0] != N:
         raise ValueError("k and v must have the same tokens")
     Hq = qs = rot = 0
+    qp = qop = pos = freq = None
     if inv_freq is not None:
-        _check_inv_freq(inv_freq, dev)
+        freq = _frequencies(inv_freq, index)
         rot = 2 * inv_freq.shape[0]
-        _int_vector(positions, "positions", N, dev)
+        if positions is not None:
+            pos = _int_vector(positions, "positions", N, index)
         if q is not None:
-            Hq = q.shape[1]
-            qs = _token_rows(q, "q", Hq, D, io, dev)
             if q.shape[0] != N:
                 raise ValueError("q and k must have the same tokens")
-            _out_rows(q_out, q, "q_out", Hq, D)
+            Hq, qp = q.shape[1], q.data_ptr()
+            qs = _token_rows(q, "q", Hq, D, io, index)
+            _out_rows(q_out, q, "q_out")
+            qop = q_out.data_ptr()
     elif q is not None or positions is not None:
         raise ValueError("q and positions go with a rotation (inv_freq)")
-    R, keep, cu_ptr, len_ptr = _cache_rows(cache, seq_lens, cu_seqlens, num_reqs, cu_seqlens_host, seq_lens_host)
-    params = GdnKvParams(N, R, Hq, rot, int(rope_layout), float(rope_factor), qs, ks, vs)
-    tens = GdnKvTensors(_ptr(k), _ptr(v), _ptr(cu_seqlens), cu_ptr, _ptr(seq_lens), len_ptr, _ptr(q),
-                        _ptr(q_out) if q is not None else None, _ptr(positions), _ptr(inv_freq))
-    st = lib().gdn_kv_write(ctypes.byref(params), ctypes.byref(tens), cache._ref, _stream_handle(stream))
+    R, lens, cu, len_h, cu_h, keep = _cache_rows(cache, seq_lens, cu_seqlens, num_reqs, cu_seqlens_host,
+                                                 seq_lens_host)
+    st = lib().gdn_kv_write(GdnKvParams(N, R, Hq, rot, rope_layout, rope_factor, qs, ks, vs),
+                            GdnKvTensors(k.data_ptr(), v.data_ptr(), cu, cu_h, lens, len_h, qp, qop, pos, freq),
+                            cache.struct, _stream_handle(stream))
     del keep
     if check and st != GDN_OK:
         raise GDNError(st, "gdn_kv_write")
@@ -938,16 +960,15 @@ def gdn_kv_read(k, v, cache: KVCache, seq_lens, cu_seqlens=None, *, num_reqs: Op
                 cu_seqlens_host=None, seq_lens_host=None, stream=None, check: bool = True) -> int:
     """gdn_kv_read of include/gdn_attn.h: the newest T_r of every request's seq_lens[r]
     cached tokens into k, v [N, Hk, D] (dense, the cache's I/O type); returns the status."""
-    Hk, D, dev, io = cache.num_kv_heads, cache.head_dim, cache.device, cache.io_dtype
+    Hk, D, index, io = cache.num_kv_heads, cache.head_dim, cache.index, cache.io_dtype
     N = k.shape[0]
-    if v.shape[0] != N or not k.is_contiguous() or not v.is_contiguous():
+    if _token_rows(k, "k", Hk, D, io, index) or _token_rows(v, "v", Hk, D, io, index) or v.shape[0] != N or \
+            not k.is_contiguous() or not v.is_contiguous():
         raise ValueError("k and v must be contiguous and have the same tokens")
-    _token_rows(k, "k", Hk, D, io, dev)
-    _token_rows(v, "v", Hk, D, io, dev)
-    R, keep, cu_ptr, len_ptr = _cache_rows(cache, seq_lens, cu_seqlens, num_reqs, cu_seqlens_host, seq_lens_host)
-    params = GdnKvParams(N, R, 0, 0, 0, 0.0, 0, 0, 0)
-    tens = GdnKvTensors(_ptr(k), _ptr(v), _ptr(cu_seqlens), cu_ptr, _ptr(seq_lens), len_ptr, None, None, None, None)
-    st = lib().gdn_kv_read(ctypes.byref(params), ctypes.byref(tens), cache._ref, _stream_handle(stream))
+    R, lens, cu, len_h, cu_h, keep = _cache_rows(cache, seq_lens, cu_seqlens, num_reqs, cu_seqlens_host,
+                                                 seq_lens_host)
+    st = lib().gdn_kv_read(GdnKvParams(N, R), GdnKvTensors(k.data_ptr(), v.data_ptr(), cu, cu_h, lens, len_h),
+                           cache.struct, _stream_handle(stream))
     del keep
     if check and st != GDN_OK:
         raise GDNError(st, "gdn_kv_read")
@@ -958,7 +979,7 @@ def gdn_attn_workspace_bytes(N: int, R: int, Hq: int, cache: KVCache) -> int:
     """Workspace bytes gdn_attn_forward needs for these sizes, whatever the lengths."""
     params = GdnAttnParams(int(N), int(R), int(Hq), 0.0, 0, 0)
     out = ctypes.c_size_t(0)
-    st = lib().gdn_attn_workspace_bytes(ctypes.byref(params), cache._ref, ctypes.byref(out))
+    st = lib().gdn_attn_workspace_bytes(ctypes.byref(params), ctypes.byref(cache.struct), ctypes.byref(out))
     if st != GDN_OK:
         raise GDNError(st, "gdn_attn_workspace_bytes")
     return int(out.value)
@@ -973,21 +994,22 @@ def gdn_attn_forward(q, cache: KVCache, seq_lens, cu_seqlens, output, *, scale: 
     [N, Hq, D] dense; seq_lens [R] int32; cu_seqlens [R + 1] int32 or None for N / R
     tokens each; workspace a uint8 GPU tensor of gdn_attn_workspace_bytes().
     """
-    D, dev, io = cache.head_dim, cache.device, cache.io_dtype
-    N, Hq = q.shape[0], q.shape[1]
-    qs = _token_rows(q, "q", Hq, D, io, dev)
-    if output.shape != q.shape or output.dtype != io or not output.is_contiguous() or output.device != dev:
+    index, io = cache.index, cache.io_dtype
+    shape = q.shape
+    N, Hq = shape[0], shape[1]
+    qs = _token_rows(q, "q", Hq, cache.head_dim, io, index)
+    if output.shape != shape or output.dtype is not io or output.get_device() != index or not output.is_contiguous():
         raise ValueError("output must be contiguous and have q's shape, type and device")
-    ws_ptr, ws_bytes = None, 0
+    ws, ws_bytes = None, 0
     if workspace is not None:
-        if workspace.device != dev or not workspace.is_contiguous():
+        if workspace.get_device() != index or not workspace.is_contiguous():
             raise ValueError("workspace must be a contiguous tensor on the cache's GPU")
-        ws_ptr, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    R, keep, cu_ptr, len_ptr = _cache_rows(cache, seq_lens, cu_seqlens, num_reqs, cu_seqlens_host, seq_lens_host)
-    params = GdnAttnParams(N, R, Hq, float(scale), int(window), qs)
-    tens = GdnAttnTensors(q.data_ptr(), _ptr(cu_seqlens), cu_ptr, _ptr(seq_lens), len_ptr, output.data_ptr())
-    st = lib().gdn_attn_forward(ctypes.byref(params), ctypes.byref(tens), cache._ref, ws_ptr, ws_bytes,
-                                _stream_handle(stream))
+        ws, ws_bytes = workspace.data_ptr(), workspace.nbytes
+    R, lens, cu, len_h, cu_h, keep = _cache_rows(cache, seq_lens, cu_seqlens, num_reqs, cu_seqlens_host,
+                                                 seq_lens_host)
+    st = lib().gdn_attn_forward(GdnAttnParams(N, R, Hq, scale, window, qs),
+                                GdnAttnTensors(q.data_ptr(), cu, cu_h, lens, len_h, output.data_ptr()), cache.struct,
+                                ws, ws_bytes, _stream_handle(stream))
     del keep
     if check and st != GDN_OK:
         raise GDNError(st, "gdn_attn_forward")
