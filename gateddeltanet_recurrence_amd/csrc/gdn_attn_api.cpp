@@ -173,10 +173,15 @@ gdn::RowArgs row_args(const Rows& w) {
   return a;
 }
 
-// Tokens per workgroup: one while there are fewer than 4 workgroups per CU, then
-// up to kRopeMaxTokens, which share a workgroup's start-up.
-int tokens_per_block(int64_t N) {
-  const int64_t t = N / 1024;
+// Tokens per workgroup of the rotation and cache kernels: about two items (32 bytes of
+// a head each) a thread, and at least 4 workgroups per CU where there are tokens for
+// them. More tokens leave fewer workgroups with more items in a row, and too little
+// in flight: 15,352 tokens of 28 heads x 256 fp16, one a workgroup 76 us, 4 90 us,
+// 14 99 us; reading 32,768 tokens of 4 key heads, 1, 2, 4, 8 a workgroup 45, 34, 31,
+// 39 us.
+int tokens_per_block(int64_t N, int64_t heads, int64_t D, size_t io) {
+  const int64_t items = heads * D * (int64_t)io / 32;
+  const int64_t t = std::min<int64_t>(512 / std::max<int64_t>(items, 1), N / 1024);
   return (int)std::min<int64_t>(std::max<int64_t>(t, 1), gdn::kRopeMaxTokens);
 }
 
@@ -256,7 +261,7 @@ int gdn_rope_forward(const gdn_rope_params* p, const gdn_rope_tensors* t, void* 
   a.factor = p->factor == 0.f ? 1.f : p->factor;
   a.q_stride = qs; a.k_stride = ks; a.q_out_stride = qos; a.k_out_stride = kos;
   a.q_in_place = q_in ? 1 : 0; a.k_in_place = k_in ? 1 : 0;
-  a.tokens_per_block = tokens_per_block(N);
+  a.tokens_per_block = tokens_per_block(N, Hq + Hk, D, io);
   return status_of(gdn::launch_rope(a, p->io_dtype, static_cast<hipStream_t>(stream)));
 }
 
@@ -312,7 +317,7 @@ int gdn_kv_write(const gdn_kv_params* p, const gdn_kv_tensors* t, const gdn_kv_c
   a.factor = p->rope_factor == 0.f ? 1.f : p->rope_factor;
   a.q_stride = qs; a.k_stride = ks; a.v_stride = vs; a.q_out_stride = qos;
   a.q_in_place = q_in ? 1 : 0;
-  a.tokens_per_block = tokens_per_block(N);
+  a.tokens_per_block = tokens_per_block(N, Hq + 2 * Hk, D, io);
   a.to_cache = 1;
   a.cache = cache_args(*c);
   a.rows = row_args(w);
@@ -344,7 +349,7 @@ int gdn_kv_read(const gdn_kv_params* p, const gdn_kv_tensors* t, const gdn_kv_ca
     if (k.overlaps(s) || v.overlaps(s)) return GDN_ERR_ALIAS;
   gdn::ReadArgs a{};
   a.k = t->k; a.v = t->v;
-  a.tokens_per_block = tokens_per_block(N);
+  a.tokens_per_block = tokens_per_block(N, 2 * Hk, D, io_bytes(c->io_dtype));
   a.cache = cache_args(*c);
   a.rows = row_args(w);
   return status_of(gdn::launch_kv_read(a, c->io_dtype, static_cast<hipStream_t>(stream)));

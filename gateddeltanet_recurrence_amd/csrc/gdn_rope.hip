@@ -30,6 +30,15 @@ template <> struct Vec<float> {
   typedef float4_t type;
 };
 
+typedef uint32_t uint2_t __attribute__((ext_vector_type(2)));
+
+// Outputs are written once and not read here: nontemporal stores (32,768 tokens read
+// back 39 -> 31 us, 15,352 written in 8 bits 36 -> 30 us). Nontemporal loads of the
+// inputs were slower (31 -> 38 us, 30 -> 35 us): two loads share a 128-byte line.
+template <typename T, typename P> __device__ __forceinline__ void store_stream(P* p, T x) {
+  __builtin_nontemporal_store(x, reinterpret_cast<T*>(p));
+}
+
 // Largest of x over aligned groups of LANES lanes.
 template <int LANES>
 __device__ __forceinline__ float group_max(float x) {
@@ -54,7 +63,7 @@ __device__ __forceinline__ bool is_finite(float x) { return (__float_as_uint(x) 
 
 // e4m3 codes of 8 values times inv (a power of two, so the products are exact);
 // v_cvt_pk_fp8_f32 rounds to nearest even.
-__device__ __forceinline__ uint2 encode8(const float (&x)[8], float inv) {
+__device__ __forceinline__ uint2_t encode8(const float (&x)[8], float inv) {
   float y[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) y[i] = is_finite(x[i]) ? x[i] * inv : __uint_as_float(0x7fc00000u);
@@ -63,7 +72,7 @@ __device__ __forceinline__ uint2 encode8(const float (&x)[8], float inv) {
   a = __builtin_amdgcn_cvt_pk_fp8_f32(y[2], y[3], a, true);
   b = __builtin_amdgcn_cvt_pk_fp8_f32(y[4], y[5], b, false);
   b = __builtin_amdgcn_cvt_pk_fp8_f32(y[6], y[7], b, true);
-  return uint2{(uint32_t)a, (uint32_t)b};
+  return uint2_t{(uint32_t)a, (uint32_t)b};
 }
 
 // Request of the workgroup's first token n0 (the same in every thread): the
@@ -203,8 +212,8 @@ __global__ void __launch_bounds__(kThreads) gdn_rope_k(RopeArgs p) {
       if (keep) continue;
       IO* dst = (is_q ? static_cast<IO*>(p.q_out) + n * p.q_out_stride
                       : static_cast<IO*>(p.k_out) + n * p.k_out_stride) + hh * D;
-      *reinterpret_cast<vec_t*>(dst + a) = ra;
-      *reinterpret_cast<vec_t*>(dst + b) = rb;
+      store_stream(dst + a, ra);
+      store_stream(dst + b, rb);
       continue;
     }
     if constexpr (CACHE) {
@@ -225,13 +234,13 @@ __global__ void __launch_bounds__(kThreads) gdn_rope_k(RopeArgs p) {
         const int s = scale_byte(m);
         const float inv = __uint_as_float((uint32_t)(s > 0 ? 254 - s : 127) << 23);
         uint8_t* dst = static_cast<uint8_t*>(is_v ? p.cache.v : p.cache.k) + row * D;
-        *reinterpret_cast<uint2*>(dst + a) = encode8(x, inv);
-        *reinterpret_cast<uint2*>(dst + b) = encode8(y, inv);
+        store_stream(dst + a, encode8(x, inv));
+        store_stream(dst + b, encode8(y, inv));
         if (e == 0) (is_v ? p.cache.v_scales : p.cache.k_scales)[row] = (uint8_t)s;
       } else {
         IO* dst = static_cast<IO*>(is_v ? p.cache.v : p.cache.k) + row * D;
-        *reinterpret_cast<vec_t*>(dst + a) = ra;
-        *reinterpret_cast<vec_t*>(dst + b) = rb;
+        store_stream(dst + a, ra);
+        store_stream(dst + b, rb);
       }
     }
   }
@@ -269,7 +278,7 @@ __global__ void __launch_bounds__(kThreads) gdn_kv_read_k(ReadArgs p) {
       const int64_t row = row_of[t] + ((int64_t)hh << p.cache.page_shift);
       if constexpr (E4M3) {
         const uint8_t* src = static_cast<const uint8_t*>(is_v ? p.cache.v : p.cache.k) + row * D;
-        const uint2 ca = *reinterpret_cast<const uint2*>(src + a), cb = *reinterpret_cast<const uint2*>(src + b);
+        const uint2_t ca = *reinterpret_cast<const uint2_t*>(src + a), cb = *reinterpret_cast<const uint2_t*>(src + b);
         const int s = (is_v ? p.cache.v_scales : p.cache.k_scales)[row];
         const float scale = __uint_as_float(s > 0 ? (uint32_t)s << 23 : 0x00400000u);   // 2^(s - 127)
         const uint32_t w[4] = {ca.x, ca.y, cb.x, cb.y};
@@ -290,8 +299,8 @@ __global__ void __launch_bounds__(kThreads) gdn_kv_read_k(ReadArgs p) {
       }
     }
     IO* dst = static_cast<IO*>(is_v ? p.v : p.k) + ((int64_t)(n0 + t) * Hk + hh) * D;
-    *reinterpret_cast<vec_t*>(dst + a) = xa;
-    *reinterpret_cast<vec_t*>(dst + b) = xb;
+    store_stream(dst + a, xa);
+    store_stream(dst + b, xb);
   }
 }
 
