@@ -19,15 +19,13 @@
 //  (16 for fp32) and its 4 waves take alternate tiles. Each byte is used once and
 //  loaded past the caches' retention (nontemporal).
 //
-//  gdn_attn_rows_k, for up to 64 rows (drafts, prompts): through LDS, so that 4
-//  waves with 16 rows each share one copy. A fifth wave does nothing but copy pages
-//  into a ring of 16 KiB stages, by buffer loads that write LDS directly; it needs
-//  no registers for them and runs ahead over the ring, and the loads' range check
+//  gdn_attn_rows_k, for up to 64 rows (drafts, prompts): through LDS, so that the
+//  8 computing waves, up to 4 tiles of 16 rows, share one copy. Two more waves do nothing but copy
+//  pages into a ring of 16 KiB stages, by buffer loads that write LDS directly; they
+//  need no registers for them and run ahead over the ring, and the loads' range check
 //  fills positions past the end and without a page with zeros. A counter of landed
 //  stages and one of finished stages per wave, both in LDS, hand the stages over,
-//  so the waves need not run in step. With one tile of rows this kernel is slower
-//  than the first (a wave's 16-position tile is a long chain of dependent steps,
-//  and LDS leaves room for 8 such waves a CU), with several it is faster.
+//  so the waves need not run in step.
 //
 // Work is split evenly over the workgroups whatever the lengths: the positions of
 // every segment (request, 16 or 64 rows, key head) in chunks of 128 are laid end to
@@ -46,14 +44,17 @@ namespace gdn {
 
 namespace {
 
-constexpr int kWaves = 4;                 // computing waves
+constexpr int kWaves = 4;                 // of gdn_attn_k
 constexpr int kThreads = 64 * kWaves;
-constexpr int kBlock = kThreads + 64;     // with a loader wave
+constexpr int kRingWaves = 8;             // computing waves of gdn_attn_rows_k
+constexpr int kRingThreads = 64 * kRingWaves;
+constexpr int kRingBlock = kRingThreads + 128;   // with a loader wave each for k and v
 constexpr int kRows = 16;                 // rows of a tile: the N side of the MFMA
 constexpr int kTiles = 4;                 // tiles of a segment of gdn_attn_rows_k
 constexpr int kChunkShift = 7;            // positions of a unit of work: 128 or more
 constexpr int kWholeShift = 30;           // one unit per segment: nothing is split
-constexpr int kGroups = 512;              // workgroups of a split launch: two per CU
+constexpr int kGroups = 512;              // workgroups of a split launch, at most: two per CU
+constexpr int kRingGroups = 256;          // of gdn_attn_rows_k, whose ring fills a CU's LDS
 
 enum Format { kF32 = 0, kF16 = 1, kE4M3 = 2 };
 
@@ -244,6 +245,31 @@ template <int FMT> __device__ __forceinline__ float element(const uint32_t* w, i
   return (float)__builtin_bit_cast(_Float16, (uint16_t)(e & 1 ? pair >> 16 : pair));
 }
 
+// Four columns from d on of row rr of a segment, joined over the workgroup's waves:
+// the output, or this workgroup's part.
+template <int FMT, int D>
+__device__ __forceinline__ void store_row(const AttnArgs& p, const SplitArgs& sp, const Segment& sg, bool complete, int rr,
+                                          int d, float M, float l, float4_t o) {
+  if (complete) {
+    typedef typename std::conditional<FMT == kF32, float, _Float16>::type IO;
+    const int row = sg.seg_row + rr, j = (int)((unsigned)row / (unsigned)p.group);
+    IO* out = static_cast<IO*>(p.output) + ((int64_t)(sg.s.start + j) * p.Hq + sg.h * p.group + row - j * p.group) * D + d;
+    const float norm = l == 0.f ? 0.f : 1.f / l;
+    if constexpr (FMT == kF32)
+      *reinterpret_cast<float4_t*>(out) = o * norm;
+    else
+      *reinterpret_cast<half4_t*>(out) =
+          half4_t{(_Float16)(o[0] * norm), (_Float16)(o[1] * norm), (_Float16)(o[2] * norm), (_Float16)(o[3] * norm)};
+  } else {
+    float* part = sp.parts + (2 * (int64_t)blockIdx.x + (sg.c0 == 0 ? 1 : 0)) * (sp.part_rows * (D + 2));
+    *reinterpret_cast<float4_t*>(part + 2 * sp.part_rows + rr * D + d) = o;
+    if (d == 0) {
+      part[rr] = M;
+      part[sp.part_rows + rr] = l;
+    }
+  }
+}
+
 template <int FMT, int D>
 struct Shape {
   static constexpr int kBytes = FMT == kF32 ? 4 : FMT == kF16 ? 2 : 1;   // of a cache element
@@ -287,6 +313,7 @@ __global__ void __launch_bounds__(kThreads, D == 256 && FMT == kF32 ? 1 : 2) gdn
   constexpr int kAcc = S::kSets * S::kCols;                // 16 x 16 blocks of the output
   __shared__ alignas(16) float sums[kWaves][kRows][S::kPitch];
   __shared__ float stats[kWaves][kRows][2];
+  __shared__ float joined[kRows][2];
 
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int n = lane & 15, g = lane >> 4;
@@ -530,46 +557,33 @@ __global__ void __launch_bounds__(kThreads, D == 256 && FMT == kF32 ? 1 : 2) gdn
 #pragma unroll
     for (int w = 1; w < kWaves; ++w) top = fmaxf(top, stats[w][n][0]);
     const float f = M == -INFINITY ? 0.f : exp2_fast(M - top);
+    if (tid < kRows) {
+      float total = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w)
+        total += stats[w][n][0] == -INFINITY ? 0.f : stats[w][n][1] * exp2_fast(stats[w][n][0] - top);
+      joined[n][0] = top;
+      joined[n][1] = total;
+    }
     // acc[cols c + e] of row n, register i: column 16 cols c + cols (4 g + i) + e
+    if (n < rows) {
 #pragma unroll
-    for (int c = 0; c < S::kSets; ++c)
+      for (int c = 0; c < S::kSets; ++c)
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int e = 0; e < S::kCols; e += 4)
-          *reinterpret_cast<float4_t*>(&sums[wave][n][16 * S::kCols * c + S::kCols * (4 * g + i) + e]) =
-              float4_t{acc[S::kCols * c + e][i] * f, acc[S::kCols * c + e + 1][i] * f, acc[S::kCols * c + e + 2][i] * f,
-                       acc[S::kCols * c + e + 3][i] * f};
+          for (int e = 0; e < S::kCols; e += 4)
+            *reinterpret_cast<float4_t*>(&sums[wave][n][16 * S::kCols * c + S::kCols * (4 * g + i) + e]) =
+                float4_t{acc[S::kCols * c + e][i] * f, acc[S::kCols * c + e + 1][i] * f,
+                         acc[S::kCols * c + e + 2][i] * f, acc[S::kCols * c + e + 3][i] * f};
+    }
     __syncthreads();
-    float* part = complete ? nullptr
-                           : sp.parts + (2 * (int64_t)blockIdx.x + (sg.c0 == 0 ? 1 : 0)) * (sp.part_rows * (D + 2));
     for (int i = tid; i < rows * (D / 4); i += kThreads) {
       const int rr = i / (D / 4), d = 4 * (i - rr * (D / 4));
-      float best = stats[0][rr][0], sum = 0.f;
+      float4_t o = *reinterpret_cast<const float4_t*>(&sums[0][rr][d]);
 #pragma unroll
-      for (int w = 1; w < kWaves; ++w) best = fmaxf(best, stats[w][rr][0]);
-      float4_t o = float4_t{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int w = 0; w < kWaves; ++w) {
-        sum += stats[w][rr][0] == -INFINITY ? 0.f : stats[w][rr][1] * exp2_fast(stats[w][rr][0] - best);
-        o += *reinterpret_cast<const float4_t*>(&sums[w][rr][d]);
-      }
-      if (complete) {
-        const int grow = sg.seg_row + rr, jj = grow / p.group;
-        IO* out = static_cast<IO*>(p.output) + ((int64_t)(s.start + jj) * p.Hq + h * p.group + grow - jj * p.group) * D + d;
-        const float norm = sum == 0.f ? 0.f : 1.f / sum;
-        if constexpr (FMT == kF32)
-          *reinterpret_cast<float4_t*>(out) = o * norm;
-        else
-          *reinterpret_cast<half4_t*>(out) = half4_t{(_Float16)(o[0] * norm), (_Float16)(o[1] * norm),
-                                                     (_Float16)(o[2] * norm), (_Float16)(o[3] * norm)};
-      } else {
-        *reinterpret_cast<float4_t*>(part + 2 * sp.part_rows + rr * D + d) = o;
-        if (d == 0) {
-          part[rr] = best;
-          part[sp.part_rows + rr] = sum;
-        }
-      }
+      for (int w = 1; w < kWaves; ++w) o += *reinterpret_cast<const float4_t*>(&sums[w][rr][d]);
+      store_row<FMT, D>(p, sp, sg, complete, rr, d, joined[rr][0], joined[rr][1], o);
     }
   }
 }
@@ -580,10 +594,10 @@ struct RingShape {
   static constexpr int kRow = D * kBytes;                                // bytes of a position's k or v
   static constexpr int kStage = kRow >= 512 ? 16 : 8192 / kRow;          // positions of a stage: 16 KiB of k and v
   static constexpr int kStageBytes = 2 * kStage * kRow;                  // (32 KiB for fp32 at D = 256)
-  static constexpr int kBufs = 65536 / kStageBytes;
+  static constexpr int kBufs = 131072 / kStageBytes;
   static constexpr int kTilesPerStage = kStage / 16;
   static constexpr int kGroupLoads = 16 * kRow / 1024;                   // 1 KiB loads of 16 positions' k or v
-  static constexpr int kLoads = 2 * kTilesPerStage * kGroupLoads + (FMT == kE4M3 ? 1 : 0);   // of a stage
+  static constexpr int kLoads = kTilesPerStage * kGroupLoads + (FMT == kE4M3 ? 1 : 0);       // a loader's, of a stage
   static constexpr int kUnits = kRow / 16;                               // 16-byte units of a row
   // columns of v a lane holds: sets of kCols neighbours, 16 * kCols apart
   static constexpr int kCols = FMT == kF32 ? 4 : FMT == kF16 ? (D / 16 < 8 ? D / 16 : 8) : D / 16;
@@ -611,10 +625,12 @@ typedef __attribute__((address_space(1))) const void global_void_t;
 __device__ __forceinline__ void lds_store(uint32_t at, int x) {
   asm volatile("ds_write_b32 %0, %1" ::"v"(at), "v"(x) : "memory");
 }
-__device__ __forceinline__ int lds_min4(uint32_t at) {
-  uint4_t x;
-  asm volatile("ds_read_b128 %0, %1\n\ts_waitcnt lgkmcnt(0)" : "=&v"(x) : "v"(at) : "memory");
-  const int a = min((int)x[0], (int)x[1]), b = min((int)x[2], (int)x[3]);
+__device__ __forceinline__ int lds_min8(uint32_t at) {
+  uint4_t x, y;
+  asm volatile("ds_read_b128 %0, %2\n\tds_read_b128 %1, %2 offset:16\n\ts_waitcnt lgkmcnt(0)"
+               : "=&v"(x), "=&v"(y) : "v"(at) : "memory");
+  const int a = min(min((int)x[0], (int)x[1]), min((int)x[2], (int)x[3]));
+  const int b = min(min((int)y[0], (int)y[1]), min((int)y[2], (int)y[3]));
   return __builtin_amdgcn_readfirstlane(min(a, b));
 }
 __device__ __forceinline__ uint32_t lds_address(const void* p) {
@@ -637,12 +653,14 @@ __device__ __forceinline__ void wait_in_flight(int n) {
 
 constexpr int kStream = 2;                // cache policy of the loads: nontemporal, each byte is used once
 
-// Copies positions t .. t + kStage - 1 of one request and key head into a stage:
-// [k rows | v rows], zeros from position `end` on and where there is no page.
+// Copies the k or v rows of positions t .. t + kStage - 1 of one request and key head
+// into a stage, zeros from position `end` on and where there is no page.
 template <int FMT, int D>
 struct Loader {
   typedef RingShape<FMT, D> S;
   const AttnArgs& p;
+  const void* pool;                                                      // k or v pages
+  const uint8_t* pool_scales;
   const __attribute__((address_space(4))) int32_t* table;                // read through the scalar cache
   int h, end, lane;
 
@@ -672,28 +690,23 @@ struct Loader {
       const int pos = t + 16 * q, pg = pages[q];
       const int rows = __builtin_amdgcn_readfirstlane(pg >= 0 ? min(max(end - pos, 0), 16) : 0);
       const int64_t at = first_row(max(pg, 0), pos) * S::kRow;
-      const rsrc_t rk = make_rsrc(static_cast<const char*>(p.cache.k) + at, rows * S::kRow);
-      const rsrc_t rv = make_rsrc(static_cast<const char*>(p.cache.v) + at, rows * S::kRow);
+      const rsrc_t rs = make_rsrc(static_cast<const char*>(pool) + at, rows * S::kRow);
 #pragma unroll
       for (int i = 0; i < S::kGroupLoads; ++i) {
         const int row = kRowsPerLoad * i + lrow;
         const int off = lrow * S::kRow + 16 * (slot ^ swizzle<S::kUnits>(row));
-        char* dst = stage + (16 * q * S::kRow) + 1024 * i;
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(rk, (lds_void_t*)dst, 16, off, 1024 * i, 0, kStream);
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(rv, (lds_void_t*)(dst + S::kStage * S::kRow), 16, off, 1024 * i, 0,
-                                                 kStream);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void_t*)(stage + 16 * q * S::kRow + 1024 * i), 16, off, 1024 * i,
+                                                 0, kStream);
       }
     }
     if constexpr (FMT == kE4M3) {
-      // the exponent bytes, 4 positions a lane: k's, then v's
-      constexpr int kWords = S::kStage / 4;
-      if (lane < 2 * kWords) {
-        const int w = lane % kWords;
+      // the exponent bytes, 4 positions a lane
+      if (lane < S::kStage / 4) {
         int pg = pages[0];
 #pragma unroll
-        for (int q = 1; q < S::kTilesPerStage; ++q) pg = (w >> 2) == q ? pages[q] : pg;
-        const uint8_t* src = (lane < kWords ? p.cache.k_scales : p.cache.v_scales) + first_row(max(pg, 0), t + 4 * w);
-        __builtin_amdgcn_global_load_lds((global_void_t*)src, (lds_void_t*)scales, 4, 0, 0);
+        for (int q = 1; q < S::kTilesPerStage; ++q) pg = (lane >> 2) == q ? pages[q] : pg;
+        __builtin_amdgcn_global_load_lds((global_void_t*)(pool_scales + first_row(max(pg, 0), t + 4 * lane)),
+                                         (lds_void_t*)scales, 4, 0, 0);
       }
     }
     return held;
@@ -701,24 +714,25 @@ struct Loader {
 };
 
 template <int FMT, int D>
-__global__ void __launch_bounds__(kBlock, 3) gdn_attn_rows_k(AttnArgs p, SplitArgs sp) {
+__global__ void __launch_bounds__(kRingBlock, 3) gdn_attn_rows_k(AttnArgs p, SplitArgs sp) {
   typedef RingShape<FMT, D> S;
   typedef typename std::conditional<FMT == kF32, float, _Float16>::type IO;
   constexpr int kAcc = S::kSets * S::kCols;                // 16 x 16 blocks of the output
   __shared__ __attribute__((aligned(16))) char ring[S::kBufs][S::kStageBytes];
   __shared__ __attribute__((aligned(16))) uint8_t scale_ring[FMT == kE4M3 ? S::kBufs : 1][FMT == kE4M3 ? 2 * S::kStage : 16];
-  __shared__ __attribute__((aligned(16))) int finished[kWaves];   // stages a wave is done with
-  __shared__ int landed;                                          // stages in LDS
+  __shared__ __attribute__((aligned(16))) int finished[kRingWaves];   // stages a wave is done with
+  __shared__ int landed[2];                                       // stages of k and of v in LDS
   __shared__ int held[S::kBufs];                                  // a stage's 16-position groups that have a page
-  __shared__ float stats[kWaves][kRows][2];
-  static_assert(sizeof(float) * kWaves * kRows * D <= sizeof(ring), "the waves' sums are joined in the ring");
+  __shared__ float stats[kRingWaves][kRows][2];
+  __shared__ float joined[kTiles][kRows][2];
+  static_assert(sizeof(float) * kRingWaves * kRows * D <= sizeof(ring), "the waves' sums are joined in the ring");
 
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int n = lane & 15, g = lane >> 4;
 
   Share w = find_share(p, sp, lane);
-  if (tid < kWaves) finished[tid] = 0;
-  if (tid == 0) landed = 0;
+  if (tid < kRingWaves) finished[tid] = 0;
+  if (tid < 2) landed[tid] = 0;
   __syncthreads();
   const float to_log2 = p.scale * 1.4426950408889634f;
   int stage0 = 0;                                          // stages of the segments before this one
@@ -732,18 +746,22 @@ __global__ void __launch_bounds__(kBlock, 3) gdn_attn_rows_k(AttnArgs p, SplitAr
     const int stages = end > t0 ? (end - t0 + S::kStage - 1) / S::kStage : 0;
     const bool complete = sg.c0 == 0 && sg.c1 == s.chunks;
 
-    if (wave == kWaves) {
-      // ---- the loader: issue what the ring has room for, announce what has landed
-      const Loader<FMT, D> load{p, (const __attribute__((address_space(4))) int32_t*)(p.cache.table + (int64_t)w.r * p.cache.max_pages),
+    if (wave >= kRingWaves) {
+      // ---- a loader: issue what the ring has room for, announce what has landed
+      const int side = wave - kRingWaves;                  // 0: k, 1: v
+      const Loader<FMT, D> load{p, side ? p.cache.v : p.cache.k, side ? p.cache.v_scales : p.cache.k_scales,
+                                (const __attribute__((address_space(4))) int32_t*)(p.cache.table + (int64_t)w.r * p.cache.max_pages),
                                 h, end, lane};
-      const uint32_t done_at = lds_address(finished), landed_at = lds_address(&landed), held_at = lds_address(held);
+      const uint32_t done_at = lds_address(finished), landed_at = lds_address(&landed[side]), held_at = lds_address(held);
       int issued = 0, pages[S::kTilesPerStage];
       load.look_up(t0, pages);
       for (int i = 0; i < stages;) {
         while (issued < stages) {
-          if (stage0 + issued - lds_min4(done_at) < S::kBufs) {
+          if (stage0 + issued - lds_min8(done_at) < S::kBufs) {
             const int b = (stage0 + issued) % S::kBufs;
-            lds_store(held_at + 4 * b, load.issue(t0 + issued * S::kStage, pages, ring[b], scale_ring[FMT == kE4M3 ? b : 0]));
+            const int bits = load.issue(t0 + issued * S::kStage, pages, ring[b] + side * (S::kStageBytes / 2),
+                                        scale_ring[FMT == kE4M3 ? b : 0] + (FMT == kE4M3 ? side * S::kStage : 0));
+            if (side == 0) lds_store(held_at + 4 * b, bits);
             ++issued;
             load.look_up(t0 + issued * S::kStage, pages);
           } else if (issued > i) {
@@ -763,8 +781,9 @@ __global__ void __launch_bounds__(kBlock, 3) gdn_attn_rows_k(AttnArgs p, SplitAr
     }
 
     // ---- the wave's tile and stream of positions, this lane's row, and what the tile's rows attend
-    // at most 2 stages of the ring are in use at a time, whatever the tiles of a stage
-    const int streams = seg_rows <= kRows ? min(4, 2 * S::kTilesPerStage) : seg_rows <= 2 * kRows ? 2 : 1;
+    // the streams of a tile hold at most half of the ring's stages at a time
+    constexpr int kMost = S::kBufs / 2 * S::kTilesPerStage;
+    const int streams = min(seg_rows <= kRows ? kRingWaves : seg_rows <= 2 * kRows ? kRingWaves / 2 : kRingWaves / 4, kMost);
     const int sub = wave / streams, stream = wave - sub * streams;
     const int rows = max(min(kRows, seg_rows - sub * kRows), 0);       // 0: a wave without a tile
     const int row0 = seg_row + (rows > 0 ? sub * kRows : 0);
@@ -795,8 +814,11 @@ __global__ void __launch_bounds__(kBlock, 3) gdn_attn_rows_k(AttnArgs p, SplitAr
     if (lane == 0) *(volatile int*)&finished[wave] = stage0 + min(rows > 0 ? stream / S::kTilesPerStage : stages, stages);
     for (int x = stream; x < tiles; x += streams) {
       const int i = x / S::kTilesPerStage, xi = x - i * S::kTilesPerStage;
-      while (__builtin_amdgcn_readfirstlane(*(volatile int*)&landed) <= stage0 + i) __builtin_amdgcn_s_sleep(1);
-      asm volatile("" ::: "memory");
+      auto wait = [&](int side) {
+        while (__builtin_amdgcn_readfirstlane(*(volatile int*)&landed[side]) <= stage0 + i) __builtin_amdgcn_s_sleep(1);
+        asm volatile("" ::: "memory");
+      };
+      wait(0);
       const int t = t0 + 16 * x;
       const int b = (stage0 + i) % S::kBufs;
       const char* kt = ring[b] + 16 * xi * S::kRow;
@@ -830,6 +852,7 @@ __global__ void __launch_bounds__(kBlock, 3) gdn_attn_rows_k(AttnArgs p, SplitAr
           if (S::kFew && (c & 3) == 3) __builtin_amdgcn_sched_barrier(0);
         }
         sc += sd;
+        wait(1);
         // to base-2 exponents. With 8-bit values the weight carries the value's scale, so xs is the
         // exponent of the product and `inv` takes the scale out of the weights' sum again; a zero row's
         // scale counts as 2^-33, below that of every other fp16 row.
@@ -990,9 +1013,15 @@ __global__ void __launch_bounds__(kBlock, 3) gdn_attn_rows_k(AttnArgs p, SplitAr
     }
     __syncthreads();                                       // A: the ring is free
     const int w0 = sub * streams;                          // the waves of this wave's tile
-    float top = M;
-    for (int w = w0; w < w0 + streams; ++w) top = fmaxf(top, stats[w][n][0]);
+    float top = M, total = 0.f;
+    for (int k = w0; k < w0 + streams; ++k) top = fmaxf(top, stats[k][n][0]);
     const float f = M == -INFINITY ? 0.f : exp2_fast(M - top);
+    if (stream == 0 && rows > 0 && g == 0) {
+      for (int k = w0; k < w0 + streams; ++k)
+        total += stats[k][n][0] == -INFINITY ? 0.f : stats[k][n][1] * exp2_fast(stats[k][n][0] - top);
+      joined[sub][n][0] = top;
+      joined[sub][n][1] = total;
+    }
     // acc[cols c + e] of row n, register i: column 16 cols c + cols (4 g + i) + e. The 16-byte units of
     // a row are stored in the order of unit ^ row.
     float* sums = reinterpret_cast<float*>(&ring[0][0]);
@@ -1011,35 +1040,15 @@ __global__ void __launch_bounds__(kBlock, 3) gdn_attn_rows_k(AttnArgs p, SplitAr
           }
     }
     __syncthreads();                                       // B
-    float* part = complete ? nullptr
-                           : sp.parts + (2 * (int64_t)blockIdx.x + (sg.c0 == 0 ? 1 : 0)) * (sp.part_rows * (D + 2));
-    for (int i = tid; i < seg_rows * (D / 4); i += kThreads) {
-      const int rr = i / (D / 4), unit = i - rr * (D / 4), d = 4 * unit, rn = rr % kRows, from = rr / kRows * streams;
-      float best = stats[from][rn][0], sum = 0.f;
-      for (int w = from + 1; w < from + streams; ++w) best = fmaxf(best, stats[w][rn][0]);
-      float4_t o = float4_t{0.f, 0.f, 0.f, 0.f};
-      for (int w = from; w < from + streams; ++w) {
-        sum += stats[w][rn][0] == -INFINITY ? 0.f : stats[w][rn][1] * exp2_fast(stats[w][rn][0] - best);
-        o += *reinterpret_cast<const float4_t*>(sums + (w * kRows + rn) * D + 4 * (unit ^ rn));
-      }
-      if (complete) {
-        const int grow = seg_row + rr, jj = grow / p.group;
-        IO* out = static_cast<IO*>(p.output) + ((int64_t)(s.start + jj) * p.Hq + h * p.group + grow - jj * p.group) * D + d;
-        const float norm = sum == 0.f ? 0.f : 1.f / sum;
-        if constexpr (FMT == kF32)
-          *reinterpret_cast<float4_t*>(out) = o * norm;
-        else
-          *reinterpret_cast<half4_t*>(out) = half4_t{(_Float16)(o[0] * norm), (_Float16)(o[1] * norm),
-                                                     (_Float16)(o[2] * norm), (_Float16)(o[3] * norm)};
-      } else {
-        *reinterpret_cast<float4_t*>(part + 2 * sp.part_rows + rr * D + d) = o;
-        if (d == 0) {
-          part[rr] = best;
-          part[sp.part_rows + rr] = sum;
-        }
-      }
+    for (int i = tid; i < seg_rows * (D / 4); i += kRingThreads) {
+      const int rr = i / (D / 4), unit = i - rr * (D / 4), rn = rr % kRows;
+      const float* from = sums + (rr / kRows * streams * kRows + rn) * D + 4 * (unit ^ rn);
+      float4_t o = *reinterpret_cast<const float4_t*>(from);
+#pragma unroll 2
+      for (int k = 1; k < streams; ++k) o += *reinterpret_cast<const float4_t*>(from + k * (kRows * D));
+      store_row<FMT, D>(p, sp, sg, complete, rr, 4 * unit, joined[rr / kRows][rn][0], joined[rr / kRows][rn][1], o);
     }
-    __syncthreads();                                       // C: the ring is the loader's again
+    __syncthreads();                                       // C: the ring is the loaders' again
   }
 }
 
@@ -1152,7 +1161,7 @@ hipError_t launch_attn_d(const AttnArgs& p, void* workspace, hipStream_t stream)
   if (whole) {
     sp.chunk_shift = kWholeShift;
   } else {
-    groups = kGroups;
+    groups = few ? kGroups : kRingGroups;
     sp.notes = static_cast<int4*>(workspace);
     sp.parts = reinterpret_cast<float*>(static_cast<char*>(workspace) + kNoteBytes);
     sp.part_rows = few ? kRows : part_rows(p.rows.N, p.group);
@@ -1162,16 +1171,16 @@ hipError_t launch_attn_d(const AttnArgs& p, void* workspace, hipStream_t stream)
     // notes by segment where there are fewer segments than workgroups
     const int64_t segs = (most + sp.seg_rows - 1) / sp.seg_rows;
     notes = segs * p.rows.R * p.cache.Hk;
-    if (notes <= kGroups) sp.max_segs = (int)segs; else notes = kGroups;
+    if (notes <= groups) sp.max_segs = (int)segs; else notes = groups;
   }
   if (few)
     hipLaunchKernelGGL((gdn_attn_k<FMT, D>), dim3((unsigned)groups), dim3(kThreads), 0, stream, p, sp);
   else
-    hipLaunchKernelGGL((gdn_attn_rows_k<FMT, D>), dim3((unsigned)groups), dim3(kBlock), 0, stream, p, sp);
+    hipLaunchKernelGGL((gdn_attn_rows_k<FMT, D>), dim3((unsigned)groups), dim3(kRingBlock), 0, stream, p, sp);
   if (!whole) {
-    // 16 slices where a segment has many parts, else 2
+    // 16 slices where a segment has more than 16 parts on average, else 2
     const unsigned rows = (unsigned)(most < sp.seg_rows ? most : sp.seg_rows);
-    if (notes * 8 <= kGroups)
+    if (notes * 16 < groups)
       hipLaunchKernelGGL((gdn_attn_join_k<FMT, D, 16>), dim3((unsigned)notes, rows, D / 64), dim3(kThreads), 0, stream, p, sp);
     else
       hipLaunchKernelGGL((gdn_attn_join_k<FMT, D, 2>), dim3((unsigned)notes, (rows + 7) / 8, D / 64), dim3(kThreads), 0,
