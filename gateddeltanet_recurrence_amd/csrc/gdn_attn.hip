@@ -284,19 +284,17 @@ struct Shape {
   static constexpr int kPitch = D + 4;                                   // floats between rows in LDS
 };
 
-template <int WORDS>
+template <int WORDS, bool STREAM>
 __device__ __forceinline__ void load_words(const char* p, uint32_t (&w)[WORDS]) {
-  if constexpr (WORDS == 4) {
-    const uint4_t x = __builtin_nontemporal_load(reinterpret_cast<const uint4_t*>(p));
+  typedef uint32_t words_t __attribute__((ext_vector_type(WORDS)));
+  const words_t* from = reinterpret_cast<const words_t*>(p);
+  words_t x;
+  if constexpr (STREAM)
+    x = __builtin_nontemporal_load(from);
+  else
+    x = *from;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = x[i];
-  } else if constexpr (WORDS == 2) {
-    const uint2_t x = __builtin_nontemporal_load(reinterpret_cast<const uint2_t*>(p));
-    w[0] = x[0];
-    w[1] = x[1];
-  } else {
-    w[0] = __builtin_nontemporal_load(reinterpret_cast<const uint32_t*>(p));
-  }
+  for (int i = 0; i < WORDS; ++i) w[i] = x[i];
 }
 
 // The page-table entry of a position, or -1. The position is below 2^30.
@@ -367,11 +365,15 @@ __global__ void __launch_bounds__(kThreads, D == 256 && FMT == kF32 ? 1 : 2) gdn
       const int64_t vrow = (((int64_t)max(vpage, 0) * p.cache.Hk + h) << p.cache.page_shift) + ((t + vpos) & in_page);
       const char* kp = static_cast<const char*>(p.cache.k) + krow * (D * S::kBytes) + 16 * g;
       const char* vp = static_cast<const char*>(p.cache.v) + vrow * (D * S::kBytes) + S::kCols * S::kBytes * n;
+      // a load of v takes 16 lanes' neighbouring units of one position, whole lines that are used once:
+      // nontemporal; one of k takes 64 bytes of 16 positions, half of each line, and the next one the
+      // other half (64 requests, 8,192 positions, D = 128: both nontemporal 350 us, v only 339, neither
+      // 375)
       uint32_t kw[S::kBlocks][S::kKLoads][4];
 #pragma unroll
       for (int a = 0; a < S::kBlocks; ++a)
 #pragma unroll
-        for (int c = 0; c < S::kKLoads; ++c) load_words(kp + 4 * a * D * S::kBytes + 64 * c, kw[a][c]);
+        for (int c = 0; c < S::kKLoads; ++c) load_words<4, false>(kp + 4 * a * D * S::kBytes + 64 * c, kw[a][c]);
       uint2 kscale, vscale;                                // exponent bytes of this lane group's 8 positions
       if constexpr (FMT == kE4M3) {
         kscale = *reinterpret_cast<const uint2*>(p.cache.k_scales + vrow);
@@ -382,7 +384,7 @@ __global__ void __launch_bounds__(kThreads, D == 256 && FMT == kF32 ? 1 : 2) gdn
       for (int i = 0; i < S::kPos; ++i)
 #pragma unroll
         for (int c = 0; c < S::kSets; ++c)
-          load_words(vp + (i * D + 16 * S::kCols * c) * S::kBytes, vw[i][c]);
+          load_words<S::kVWords, true>(vp + (i * D + 16 * S::kCols * c) * S::kBytes, vw[i][c]);
       const int next = t + kWaves * S::kTile;
       if (next < t1) {
         kpage = page_of(p, table, next + kpos);
@@ -534,7 +536,7 @@ __global__ void __launch_bounds__(kThreads, D == 256 && FMT == kF32 ? 1 : 2) gdn
             for (int i = 0; i < 4; ++i) {
               __builtin_amdgcn_sched_barrier(0);
               uint32_t words[S::kVWords];
-              load_words(row + S::kCols * S::kBytes * (16 * c + 4 * g + i), words);
+              load_words<S::kVWords, false>(row + S::kCols * S::kBytes * (16 * c + 4 * g + i), words);
 #pragma unroll
               for (int e = 0; e < S::kCols; ++e) {
                 const float v = element<FMT>(words, e);
@@ -1145,11 +1147,19 @@ int part_rows(int64_t N, int group) {
 
 // Without a split a segment's positions pass through one workgroup, 128 at a time,
 // and the second launch falls away.
-constexpr int kWholeMax = 512;
+constexpr int kWholeMax = 256;
 constexpr int64_t kWholeGroups = 4096;
+
+// Workgroups of a split gdn_attn_k launch, whose 4 waves have a tile of tile_bytes in
+// flight each: about 32 MiB in all. More than the memory can serve in a few
+// microseconds only makes the first loads late, and unevenly so (16 requests of 2,048
+// positions, D = 256 fp16, 32 KiB tiles: 256 workgroups 33 us, 512 36, 1024 41; 64
+// requests of 8,192, D = 128, 16 KiB: 256 394 us, 512 350, 1024 347).
+constexpr int few_groups(int tile_bytes) { return tile_bytes >= 32768 ? kGroups / 2 : kGroups; }
 
 template <int FMT, int D>
 hipError_t launch_attn_d(const AttnArgs& p, void* workspace, hipStream_t stream) {
+  typedef Shape<FMT, D> S;
   SplitArgs sp{};
   const int64_t most = (int64_t)p.max_tokens * p.group;    // rows of a request and key head
   const bool few = most <= kRows;
@@ -1161,7 +1171,7 @@ hipError_t launch_attn_d(const AttnArgs& p, void* workspace, hipStream_t stream)
   if (whole) {
     sp.chunk_shift = kWholeShift;
   } else {
-    groups = few ? kGroups : kRingGroups;
+    groups = few ? few_groups(S::kTile * 2 * S::kBytes * D) : kRingGroups;
     sp.notes = static_cast<int4*>(workspace);
     sp.parts = reinterpret_cast<float*>(static_cast<char*>(workspace) + kNoteBytes);
     sp.part_rows = few ? kRows : part_rows(p.rows.N, p.group);
