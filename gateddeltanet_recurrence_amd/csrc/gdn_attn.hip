@@ -53,8 +53,7 @@ constexpr int kRows = 16;                 // rows of a tile: the N side of the M
 constexpr int kTiles = 4;                 // tiles of a segment of gdn_attn_rows_k
 constexpr int kChunkShift = 7;            // positions of a unit of work: 128 or more
 constexpr int kWholeShift = 30;           // one unit per segment: nothing is split
-constexpr int kGroups = 512;              // workgroups of a split launch, at most: two per CU
-constexpr int kRingGroups = 256;          // of gdn_attn_rows_k, whose ring fills a CU's LDS
+constexpr int kGroups = 256;              // workgroups of a split launch: one per CU
 
 enum Format { kF32 = 0, kF16 = 1, kE4M3 = 2 };
 
@@ -273,42 +272,72 @@ __device__ __forceinline__ void store_row(const AttnArgs& p, const SplitArgs& sp
 template <int FMT, int D>
 struct Shape {
   static constexpr int kBytes = FMT == kF32 ? 4 : FMT == kF16 ? 2 : 1;   // of a cache element
-  static constexpr int kTile = FMT == kF32 ? 16 : 32;                    // positions of a wave's tile
-  static constexpr int kBlocks = kTile / 16;                             // 16-position blocks of the first product
-  static constexpr int kPos = kTile / 4;                                 // positions of a lane group: 4 or 8
-  static constexpr int kKLoads = D * kBytes / 64;                        // 16-byte loads of a lane per block of k
+  static constexpr int kRow = D * kBytes;                                // bytes of a position's k or v
+  static constexpr int kBlocks = FMT == kF32 ? 1 : 2;                    // 16-position blocks of a wave's tile
+  static constexpr int kTile = 16 * kBlocks;                             // positions of a tile
+  static constexpr int kPos = 4 * kBlocks;                               // of them a lane group's
+  static constexpr int kKLoads = kRow / 64;                              // 16-byte loads of a lane per block of k
   // columns of v a lane holds: sets of kCols neighbours, 16 * kCols apart
   static constexpr int kCols = FMT == kF32 ? 4 : FMT == kF16 ? (D / 16 < 8 ? D / 16 : 8) : D / 16;
   static constexpr int kSets = D / (16 * kCols);
   static constexpr int kVWords = kCols * kBytes / 4;                     // dwords of a set in one position
+  // tiles a wave has in flight: 32 KiB, at most 4
+  static constexpr int kAhead = 32768 / (2 * kTile * kRow) < 4 ? 32768 / (2 * kTile * kRow) : 4;
   static constexpr int kPitch = D + 4;                                   // floats between rows in LDS
 };
+static_assert(Shape<kE4M3, 128>::kAhead * 64 * 128 == 32768 && Shape<kE4M3, 64>::kAhead == 4, "see split_groups");
 
-template <int WORDS, bool STREAM>
-__device__ __forceinline__ void load_words(const char* p, uint32_t (&w)[WORDS]) {
-  typedef uint32_t words_t __attribute__((ext_vector_type(WORDS)));
-  const words_t* from = reinterpret_cast<const words_t*>(p);
-  words_t x;
-  if constexpr (STREAM)
-    x = __builtin_nontemporal_load(from);
-  else
-    x = *from;
+constexpr int kStream = 2;                // cache policy of a buffer access: nontemporal
+
+template <int WORDS, int POLICY>
+__device__ __forceinline__ void load_words(rsrc_t rs, int offset, uint32_t (&w)[WORDS]) {
+  if constexpr (WORDS == 4) {
+    const uint4_t x = __builtin_bit_cast(uint4_t, __builtin_amdgcn_raw_buffer_load_b128(rs, offset, 0, POLICY));
 #pragma unroll
-  for (int i = 0; i < WORDS; ++i) w[i] = x[i];
+    for (int i = 0; i < 4; ++i) w[i] = x[i];
+  } else if constexpr (WORDS == 2) {
+    const uint2_t x = __builtin_bit_cast(uint2_t, __builtin_amdgcn_raw_buffer_load_b64(rs, offset, 0, POLICY));
+    w[0] = x[0];
+    w[1] = x[1];
+  } else {
+    w[0] = __builtin_amdgcn_raw_buffer_load_b32(rs, offset, 0, POLICY);
+  }
 }
 
-// The page-table entry of a position, or -1. The position is below 2^30.
-__device__ __forceinline__ int page_of(const AttnArgs& p, const int32_t* table, int pos) {
-  const int i = pos >> p.cache.page_shift;
-  const int page = i < p.cache.max_pages ? table[i] : -1;
-  return page < p.cache.num_pages ? page : -1;
-}
+typedef const __attribute__((address_space(4))) int32_t* table_t;        // read through the scalar cache
+
+// Where a request's positions of one key head lie. Positions come in aligned blocks of
+// 16, which never cross a page.
+struct Pages {
+  const AttnArgs& p;
+  table_t table;
+  int h, end;
+
+  __device__ __forceinline__ Pages(const AttnArgs& args, int r, int head, int past)
+      : p(args), table((table_t)(args.cache.table + (int64_t)r * args.cache.max_pages)), h(head), end(past) {}
+
+  // The table's entry for the block at pos (any entry where pos is past the table), to be checked below.
+  __device__ __forceinline__ int entry(int pos) const {
+    return table[min(pos >> p.cache.page_shift, p.cache.max_pages - 1)];
+  }
+  __device__ __forceinline__ int page(int entry, int pos) const {
+    return (pos >> p.cache.page_shift) < p.cache.max_pages && entry < p.cache.num_pages ? entry : -1;
+  }
+  __device__ __forceinline__ int64_t row(int page, int pos) const {
+    return (((int64_t)max(page, 0) * p.cache.Hk + h) << p.cache.page_shift) + (pos & ((1 << p.cache.page_shift) - 1));
+  }
+  // Rows of the block that exist: up to `end`, none without a page. Scalar, so that the resources made of it are.
+  __device__ __forceinline__ int rows(int page, int pos) const {
+    return __builtin_amdgcn_readfirstlane(page >= 0 ? min(max(end - pos, 0), 16) : 0);
+  }
+};
 
 template <int FMT, int D>
-__global__ void __launch_bounds__(kThreads, D == 256 && FMT == kF32 ? 1 : 2) gdn_attn_k(AttnArgs p, SplitArgs sp) {
+__global__ void __launch_bounds__(kThreads, 1) gdn_attn_k(AttnArgs p, SplitArgs sp) {
   typedef Shape<FMT, D> S;
   typedef typename std::conditional<FMT == kF32, float, _Float16>::type IO;
   constexpr int kAcc = S::kSets * S::kCols;                // 16 x 16 blocks of the output
+  constexpr int U = S::kAhead;
   __shared__ alignas(16) float sums[kWaves][kRows][S::kPitch];
   __shared__ float stats[kWaves][kRows][2];
   __shared__ float joined[kRows][2];
@@ -319,18 +348,67 @@ __global__ void __launch_bounds__(kThreads, D == 256 && FMT == kF32 ? 1 : 2) gdn
   const float to_log2 = p.scale * 1.4426950408889634f;
   const IO* __restrict__ qs = static_cast<const IO*>(p.q);
   if (tid == 0 && sp.notes != nullptr && sp.max_segs == 0) sp.notes[2 * blockIdx.x] = int4{0, 0, 0, 0};
+  // byte offsets of this lane in a block: 16 bytes of k in row n; its columns of v in rows 4 g + (0 .. 3)
+  const int k_at = n * S::kRow + 16 * g, v_at = 4 * g * S::kRow + S::kCols * S::kBytes * n;
 
   while (sh.u < sh.u_end) {
     const Segment sg = next_segment(p, sp, sh);
     if (tid == 0 && sp.notes != nullptr && sg.c0 == 0 && (sp.max_segs > 0 || sg.c1 < sg.s.chunks)) note_segment(sp, sg);
     const Plan& s = sg.s;
-    const int h = sg.h, rows = sg.rows, t1 = sg.end;
+    const int rows = sg.rows, end = sg.end;
     const bool complete = sg.c0 == 0 && sg.c1 == s.chunks;
     const Rows rw = rows_of(p, s, sg.seg_row, rows, n);
     const int lo = rw.lo, hi = rw.hi;
+    const Pages pages(p, sh.r, sg.h, end);
+
+    // ---- tiles: this wave's are t0 + (wave + kWaves i) kTile; U of them are in flight, tile i in buffer i % U.
+    // A load past `end` or without a page has an empty range: it costs no traffic, and the number of
+    // loads in flight stays the same, so that the wait for a tile waits for nothing younger.
+    uint32_t kw[U][S::kBlocks][S::kKLoads][4], vw[U][S::kPos][S::kSets][S::kVWords];
+    uint32_t kscale[U][S::kBlocks], vscale[U][S::kBlocks];  // exponent bytes of this lane's positions
+    int entry[U][S::kBlocks], held[U][S::kBlocks];          // table entries of the next tile, pages of this one
+    constexpr int kStep = kWaves * S::kTile;
+    auto look_up = [&](int u, int t) {
+#pragma unroll
+      for (int a = 0; a < S::kBlocks; ++a) entry[u][a] = pages.entry(t + 16 * a);
+    };
+    auto load_k = [&](int u, int t) {
+#pragma unroll
+      for (int a = 0; a < S::kBlocks; ++a) {
+        const int pos = t + 16 * a, page = pages.page(entry[u][a], pos);
+        const int64_t row = pages.row(page, pos);
+        const int count = pages.rows(page, pos);
+        held[u][a] = page;
+        const rsrc_t rs = make_rsrc(static_cast<const char*>(p.cache.k) + row * S::kRow, count * S::kRow);
+#pragma unroll
+        for (int c = 0; c < S::kKLoads; ++c) load_words<4, 0>(rs, k_at + 64 * c, kw[u][a][c]);
+        if constexpr (FMT == kE4M3)
+          kscale[u][a] = __builtin_amdgcn_raw_buffer_load_b32(make_rsrc(p.cache.k_scales + row, count > 0 ? 16 : 0), 4 * g, 0, 0);
+      }
+    };
+    auto load_v = [&](int u, int t) {
+#pragma unroll
+      for (int a = 0; a < S::kBlocks; ++a) {
+        const int pos = t + 16 * a, page = held[u][a];
+        const int64_t row = pages.row(page, pos);
+        const int count = pages.rows(page, pos);
+        const rsrc_t rs = make_rsrc(static_cast<const char*>(p.cache.v) + row * S::kRow, count * S::kRow);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+#pragma unroll
+          for (int c = 0; c < S::kSets; ++c)
+            load_words<S::kVWords, kStream>(rs, v_at + e * S::kRow + 16 * S::kCols * S::kBytes * c, vw[u][4 * a + e][c]);
+        if constexpr (FMT == kE4M3)
+          vscale[u][a] = __builtin_amdgcn_raw_buffer_load_b32(make_rsrc(p.cache.v_scales + row, count > 0 ? 16 : 0), 4 * g, 0, 0);
+      }
+    };
+
+    int t = sg.t0 + wave * S::kTile;
+#pragma unroll
+    for (int u = 0; u < U; ++u) look_up(u, t + u * kStep);
 
     // q as the first product's second operand, in the order k is loaded in
-    const IO* q = qs + (int64_t)(s.start + rw.j) * p.q_stride + (int64_t)(h * p.group + rw.head) * D;
+    const IO* q = qs + (int64_t)(s.start + rw.j) * p.q_stride + (int64_t)(sg.h * p.group + rw.head) * D;
     half8_t qh[FMT == kF32 ? 1 : D / 32];
     float4_t qf[FMT == kF32 ? D / 16 : 1];
     if constexpr (FMT == kF32) {
@@ -342,208 +420,203 @@ __global__ void __launch_bounds__(kThreads, D == 256 && FMT == kF32 ? 1 : 2) gdn
         qh[c] = *reinterpret_cast<const half8_t*>(
             q + (FMT == kF16 ? 32 * c + 8 * g : 64 * (c >> 1) + 16 * g + 8 * (c & 1)));
     }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      // in the order of the loop below: its waits count the younger loads on either way in
+      __builtin_amdgcn_sched_barrier(0);
+      load_k(u, t + u * kStep);
+      __builtin_amdgcn_sched_barrier(0);
+      load_v(u, t + u * kStep);
+      look_up(u, t + (u + U) * kStep);
+    }
+    __builtin_amdgcn_sched_barrier(0);
 
     float4_t acc[kAcc];
 #pragma unroll
     for (int i = 0; i < kAcc; ++i) acc[i] = float4_t{0.f, 0.f, 0.f, 0.f};
     float M = -INFINITY, l = 0.f;                          // l: this lane's positions only
 
-    const int32_t* table = p.cache.table + (int64_t)sh.r * p.cache.max_pages;
-    const int in_page = (1 << p.cache.page_shift) - 1;
-    // positions this lane loads: k of block a at kpos + 4 a (fp32: kpos), v at vpos + 0 .. kPos - 1
-    const int kpos = FMT == kF32 ? n : 8 * (n >> 2) + (n & 3), vpos = S::kPos * g;
-
-    int kpage = -1, vpage = -1;
-    int t = sg.t0 + wave * S::kTile;
-    if (t < t1) {
-      kpage = page_of(p, table, t + kpos);
-      vpage = page_of(p, table, t + vpos);
-    }
-    for (; t < t1; t += kWaves * S::kTile) {
-      const bool held = vpage >= 0;
-      const int64_t krow = (((int64_t)max(kpage, 0) * p.cache.Hk + h) << p.cache.page_shift) + ((t + kpos) & in_page);
-      const int64_t vrow = (((int64_t)max(vpage, 0) * p.cache.Hk + h) << p.cache.page_shift) + ((t + vpos) & in_page);
-      const char* kp = static_cast<const char*>(p.cache.k) + krow * (D * S::kBytes) + 16 * g;
-      const char* vp = static_cast<const char*>(p.cache.v) + vrow * (D * S::kBytes) + S::kCols * S::kBytes * n;
-      // a load of v takes 16 lanes' neighbouring units of one position, whole lines that are used once:
-      // nontemporal; one of k takes 64 bytes of 16 positions, half of each line, and the next one the
-      // other half (64 requests, 8,192 positions, D = 128: both nontemporal 350 us, v only 339, neither
-      // 375)
-      uint32_t kw[S::kBlocks][S::kKLoads][4];
+    while (t < end) {
 #pragma unroll
-      for (int a = 0; a < S::kBlocks; ++a)
+      for (int u = 0; u < U; ++u) {
+        const bool some = t < end;
+        // ---- scores: block a of lane group g holds positions t + 16 a + 4 g + (0 .. 3)
+        float4_t x[S::kBlocks];
+        if (some) {
 #pragma unroll
-        for (int c = 0; c < S::kKLoads; ++c) load_words<4, false>(kp + 4 * a * D * S::kBytes + 64 * c, kw[a][c]);
-      uint2 kscale, vscale;                                // exponent bytes of this lane group's 8 positions
-      if constexpr (FMT == kE4M3) {
-        kscale = *reinterpret_cast<const uint2*>(p.cache.k_scales + vrow);
-        vscale = *reinterpret_cast<const uint2*>(p.cache.v_scales + vrow);
-      }
-      uint32_t vw[S::kPos][S::kSets][S::kVWords];
+          for (int a = 0; a < S::kBlocks; ++a) {
+            x[a] = float4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int i = 0; i < S::kPos; ++i)
+            for (int c = 0; c < S::kKLoads; ++c) {
+              const uint32_t(&w)[4] = kw[u][a][c];
+              if constexpr (FMT == kF32) {
 #pragma unroll
-        for (int c = 0; c < S::kSets; ++c)
-          load_words<S::kVWords, true>(vp + (i * D + 16 * S::kCols * c) * S::kBytes, vw[i][c]);
-      const int next = t + kWaves * S::kTile;
-      if (next < t1) {
-        kpage = page_of(p, table, next + kpos);
-        vpage = page_of(p, table, next + vpos);
-      }
-
-      // ---- scores: block a of lane group g holds positions t + kPos g + 4 a + (0 .. 3)
-      float4_t x[S::kBlocks];
+                for (int e = 0; e < 4; ++e)
+                  x[a] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(w[e]), qf[c][e], x[a], 0, 0, 0);
+              } else if constexpr (FMT == kF16) {
+                x[a] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8_t, uint4_t{w[0], w[1], w[2], w[3]}),
+                                                              qh[c], x[a], 0, 0, 0);
+              } else {
 #pragma unroll
-      for (int a = 0; a < S::kBlocks; ++a) {
-        x[a] = float4_t{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int c = 0; c < S::kKLoads; ++c) {
-          if constexpr (FMT == kF32) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              x[a] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(kw[a][c][e]), qf[c][e], x[a], 0, 0, 0);
-          } else if constexpr (FMT == kF16) {
-            const uint4_t w = uint4_t{kw[a][c][0], kw[a][c][1], kw[a][c][2], kw[a][c][3]};
-            x[a] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8_t, w), qh[c], x[a], 0, 0, 0);
-          } else {
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const uint4_t w = uint4_t{codes_to_half2<false>(kw[a][c][2 * e]), codes_to_half2<true>(kw[a][c][2 * e]),
-                                        codes_to_half2<false>(kw[a][c][2 * e + 1]),
-                                        codes_to_half2<true>(kw[a][c][2 * e + 1])};
-              x[a] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8_t, w), qh[2 * c + e], x[a], 0, 0, 0);
+                for (int e = 0; e < 2; ++e) {
+                  const uint4_t v = uint4_t{codes_to_half2<false>(w[2 * e]), codes_to_half2<true>(w[2 * e]),
+                                            codes_to_half2<false>(w[2 * e + 1]), codes_to_half2<true>(w[2 * e + 1])};
+                  x[a] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8_t, v), qh[2 * c + e], x[a], 0, 0, 0);
+                }
+              }
             }
           }
         }
-      }
-      // to base-2 exponents. With 8-bit values the weight carries the value's scale, so x is the
-      // exponent of the product and `inv` takes the scale out of the weights' sum again; a zero row's
-      // scale counts as 2^-33, below that of every other fp16 row.
-      float xs[S::kPos], inv[S::kPos];
+        int page[S::kBlocks];                              // of this tile: the next one's are looked up below
+        uint32_t ks[S::kBlocks];
 #pragma unroll
-      for (int i = 0; i < S::kPos; ++i) {
-        if constexpr (FMT == kE4M3) {
-          const uint32_t kb = ((i < 4 ? kscale.x : kscale.y) >> (8 * (i & 3))) & 255u;
-          const uint32_t vb = max(((i < 4 ? vscale.x : vscale.y) >> (8 * (i & 3))) & 255u, 94u);
-          xs[i] = fmaf(x[i >> 2][i & 3], to_log2 * __uint_as_float(kb << 23), (float)((int)vb - 127));
-          inv[i] = __uint_as_float((254u - min(vb, 253u)) << 23);
-        } else {
-          xs[i] = x[i >> 2][i & 3] * to_log2;
+        for (int a = 0; a < S::kBlocks; ++a) {
+          page[a] = held[u][a];
+          ks[a] = FMT == kE4M3 ? kscale[u][a] : 0;
         }
-      }
-
-      // ---- masks, where the tile reaches past what every row attends or has no page
-      const bool whole = t >= rw.lo_max && t + S::kTile <= rw.hi_min && __all(held);
-      bool mixed = false;                                  // a non-finite value that only some rows attend
-      if (!whole) {
+        // not before the products above: the loads then need registers of their own, and copies that wait
+        // for them
+        __builtin_amdgcn_sched_barrier(0);
+        load_k(u, t + U * kStep);
+        look_up(u, t + 2 * U * kStep);
+        __builtin_amdgcn_sched_barrier(0);
+        if (some) {
+          // to base-2 exponents. With 8-bit values the weight carries the value's scale, so xs is the
+          // exponent of the product and `inv` takes the scale out of the weights' sum again; a zero row's
+          // scale counts as 2^-33, below that of every other fp16 row.
+          float xs[S::kPos], inv[S::kPos];
 #pragma unroll
-        for (int i = 0; i < S::kPos; ++i) {
-          const int pos = t + vpos + i;
-          if (!(held && pos >= lo && pos < hi)) xs[i] = -INFINITY;
-          // a value that not every row attends may have to count for some: 0 times it has to be 0
-          // for the others, whatever it is
-          const bool any = held && pos >= rw.lo_min && pos < rw.hi_max, all = held && pos >= rw.lo_max && pos < rw.hi_min;
-          if (!all) {
+          for (int i = 0; i < S::kPos; ++i) {
+            if constexpr (FMT == kE4M3) {
+              const uint32_t kb = (ks[i >> 2] >> (8 * (i & 3))) & 255u;
+              const uint32_t vb = max((vscale[u][i >> 2] >> (8 * (i & 3))) & 255u, 94u);
+              xs[i] = fmaf(x[i >> 2][i & 3], to_log2 * __uint_as_float(kb << 23), (float)((int)vb - 127));
+              inv[i] = __uint_as_float((254u - min(vb, 253u)) << 23);
+            } else {
+              xs[i] = x[i >> 2][i & 3] * to_log2;
+            }
+          }
+
+          // ---- masks, where some row does not attend all of the tile, or part of it has no page
+          bool whole = t >= rw.lo_max && t + S::kTile <= rw.hi_min && t + S::kTile <= end;
+#pragma unroll
+          for (int a = 0; a < S::kBlocks; ++a) whole = whole && page[a] >= 0;
+          bool mixed = false;                              // a non-finite value that only some rows attend
+          if (!whole) {
+#pragma unroll
+            for (int i = 0; i < S::kPos; ++i) {
+              const int pos = t + 16 * (i >> 2) + 4 * g + (i & 3);
+              const bool there = page[i >> 2] >= 0 && pos < end;
+              if (!(there && pos >= lo && pos < hi)) xs[i] = -INFINITY;
+              // a value that not every row attends may have to count for some: 0 times it has to be 0
+              // for the others, whatever it is
+              if (!(there && pos >= rw.lo_max && pos < rw.hi_min)) {
+#pragma unroll
+                for (int c = 0; c < S::kSets; ++c)
+#pragma unroll
+                  for (int w = 0; w < S::kVWords; ++w) {
+                    const uint32_t bad = nonfinite<FMT>(vw[u][i][c][w]);
+                    mixed = mixed || bad != 0;
+                    vw[u][i][c][w] &= ~bad;
+                  }
+              }
+            }
+            mixed = __any(mixed);
+          }
+
+          // ---- weights
+          float m = xs[0];
+#pragma unroll
+          for (int i = 1; i < S::kPos; ++i) m = fmaxf(m, xs[i]);
+          m = fmaxf(row_max(m), M);
+          if (__any(m > M)) {
+            const float f = M == m ? 1.f : exp2_fast(M - m);   // -inf - -inf is not asked for
+            l *= f;
+#pragma unroll
+            for (int i = 0; i < kAcc; ++i) acc[i] *= f;
+            M = m;
+          }
+          const float ref = M == -INFINITY ? 0.f : M;
+          float wgt[S::kPos];
+#pragma unroll
+          for (int i = 0; i < S::kPos; ++i) {
+            wgt[i] = exp2_fast(xs[i] - ref);
+            if constexpr (FMT == kE4M3)
+              l = fmaf(wgt[i], inv[i], l);
+            else
+              l += wgt[i];
+          }
+
+          // ---- O^T += V^T P^T. A lane holds the same few columns of its 4 or 8 positions and turns them into
+          // columns of positions with byte permutes (half an instruction an element).
+          if constexpr (FMT == kF32) {
 #pragma unroll
             for (int c = 0; c < S::kSets; ++c)
 #pragma unroll
-              for (int w = 0; w < S::kVWords; ++w) {
-                const uint32_t bad = nonfinite<FMT>(vw[i][c][w]);
-                mixed = mixed || (any && bad != 0);
-                vw[i][c][w] &= ~bad;
+              for (int e = 0; e < 4; ++e)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                  acc[4 * c + e] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(vw[u][i][c][e]), wgt[i], acc[4 * c + e], 0, 0, 0);
+          } else {
+            half8_t pw;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) pw[i] = (_Float16)wgt[i];
+#pragma unroll
+            for (int c = 0; c < S::kSets; ++c)
+#pragma unroll
+              for (int k = 0; k < S::kCols / 2; ++k) {     // two columns at a time
+                uint32_t pair[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                  if constexpr (FMT == kF16)
+                    pair[i] = vw[u][i][c][k];
+                  else
+                    pair[i] = (k & 1) ? codes_to_half2<true>(vw[u][i][c][k >> 1]) : codes_to_half2<false>(vw[u][i][c][k >> 1]);
+                }
+                uint4_t a0, a1;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  a0[i] = __builtin_amdgcn_perm(pair[2 * i + 1], pair[2 * i], 0x05040100u);
+                  a1[i] = __builtin_amdgcn_perm(pair[2 * i + 1], pair[2 * i], 0x07060302u);
+                }
+                const int o = S::kCols * c + 2 * k;
+                acc[o] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8_t, a0), pw, acc[o], 0, 0, 0);
+                acc[o + 1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8_t, a1), pw, acc[o + 1], 0, 0, 0);
               }
           }
-        }
-        mixed = __any(mixed);
-      }
-
-      // ---- weights
-      float m = xs[0];
-#pragma unroll
-      for (int i = 1; i < S::kPos; ++i) m = fmaxf(m, xs[i]);
-      m = fmaxf(row_max(m), M);
-      if (__any(m > M)) {
-        const float f = M == m ? 1.f : exp2_fast(M - m);   // -inf - -inf is not asked for
-        l *= f;
-#pragma unroll
-        for (int i = 0; i < kAcc; ++i) acc[i] *= f;
-        M = m;
-      }
-      const float ref = M == -INFINITY ? 0.f : M;
-      float wgt[S::kPos];
-#pragma unroll
-      for (int i = 0; i < S::kPos; ++i) {
-        wgt[i] = exp2_fast(xs[i] - ref);
-        if constexpr (FMT == kE4M3)
-          l = fmaf(wgt[i], inv[i], l);
-        else
-          l += wgt[i];
-      }
-
-      // ---- O^T += V^T P^T
-      if constexpr (FMT == kF32) {
-#pragma unroll
-        for (int c = 0; c < S::kSets; ++c)
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              acc[4 * c + e] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(vw[i][c][e]), wgt[i], acc[4 * c + e], 0, 0, 0);
-      } else {
-        half8_t pw;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) pw[i] = (_Float16)wgt[i];
-#pragma unroll
-        for (int c = 0; c < S::kSets; ++c)
-#pragma unroll
-          for (int k = 0; k < S::kCols / 2; ++k) {         // two columns at a time
-            uint32_t pair[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              if constexpr (FMT == kF16)
-                pair[i] = vw[i][c][k];
-              else
-                pair[i] = (k & 1) ? codes_to_half2<true>(vw[i][c][k >> 1]) : codes_to_half2<false>(vw[i][c][k >> 1]);
-            }
-            uint4_t a0, a1;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              a0[i] = __builtin_amdgcn_perm(pair[2 * i + 1], pair[2 * i], 0x05040100u);
-              a1[i] = __builtin_amdgcn_perm(pair[2 * i + 1], pair[2 * i], 0x07060302u);
-            }
-            const int o = S::kCols * c + 2 * k;
-            acc[o] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8_t, a0), pw, acc[o], 0, 0, 0);
-            acc[o + 1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8_t, a1), pw, acc[o + 1], 0, 0, 0);
-          }
-      }
-      if (mixed) {
-        // the values left out above, for the rows that attend them: position by position, element by
-        // element, from memory
+          if (mixed) {
+            // the values left out above, for the rows that attend them: position by position, element by
+            // element, from memory
 #pragma unroll 1
-        for (int at = 0; at < S::kTile; ++at) {
-          const int page = page_of(p, table, t + at);
-          if (page < 0) continue;
-          float own = wgt[0];
+            for (int at = 0; at < S::kTile; ++at) {
+              const int pos = t + at, pg = pages.page(pages.entry(pos & ~15), pos & ~15);
+              if (pg < 0 || pos >= end) continue;
+              float own = wgt[0];
 #pragma unroll
-          for (int i = 1; i < S::kPos; ++i) own = at % S::kPos == i ? wgt[i] : own;
-          const float w = __shfl(own, n + 16 * (at / S::kPos));
-          const bool sees = t + at >= lo && t + at < hi && !(t + at >= rw.lo_max && t + at < rw.hi_min);
-          const char* row = static_cast<const char*>(p.cache.v) +
-                            ((((int64_t)page * p.cache.Hk + h) << p.cache.page_shift) + ((t + at) & in_page)) * (D * S::kBytes);
+              for (int i = 1; i < S::kPos; ++i) own = 4 * (at >> 4) + (at & 3) == i ? wgt[i] : own;
+              const float w = __shfl(own, n + 16 * ((at >> 2) & 3));
+              const bool sees = pos >= lo && pos < hi && !(pos >= rw.lo_max && pos < rw.hi_min);
+              const rsrc_t rs = make_rsrc(static_cast<const char*>(p.cache.v) + pages.row(pg, pos) * S::kRow, S::kRow);
 #pragma unroll
-          for (int c = 0; c < S::kSets; ++c)
+              for (int c = 0; c < S::kSets; ++c)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              __builtin_amdgcn_sched_barrier(0);
-              uint32_t words[S::kVWords];
-              load_words<S::kVWords, false>(row + S::kCols * S::kBytes * (16 * c + 4 * g + i), words);
+                for (int i = 0; i < 4; ++i) {
+                  __builtin_amdgcn_sched_barrier(0);
+                  uint32_t words[S::kVWords];
+                  load_words<S::kVWords, 0>(rs, S::kCols * S::kBytes * (16 * c + 4 * g + i), words);
 #pragma unroll
-              for (int e = 0; e < S::kCols; ++e) {
-                const float v = element<FMT>(words, e);
-                if (sees && !(fabsf(v) < INFINITY)) acc[S::kCols * c + e][i] = fmaf(w, v, acc[S::kCols * c + e][i]);
-              }
+                  for (int e = 0; e < S::kCols; ++e) {
+                    const float v = element<FMT>(words, e);
+                    if (sees && !(fabsf(v) < INFINITY)) acc[S::kCols * c + e][i] = fmaf(w, v, acc[S::kCols * c + e][i]);
+                  }
+                }
             }
+          }
         }
+        __builtin_amdgcn_sched_barrier(0);
+        load_v(u, t + U * kStep);
+        __builtin_amdgcn_sched_barrier(0);
+        t += kStep;
       }
     }
 
@@ -652,8 +725,6 @@ __device__ __forceinline__ void wait_in_flight(int n) {
       wait_in_flight<LOADS, N - 1>(n);
   }
 }
-
-constexpr int kStream = 2;                // cache policy of the loads: nontemporal, each byte is used once
 
 // Copies the k or v rows of positions t .. t + kStage - 1 of one request and key head
 // into a stage, zeros from position `end` on and where there is no page.
@@ -1136,8 +1207,19 @@ __global__ void __launch_bounds__(kThreads) gdn_attn_join_k(AttnArgs p, SplitArg
         half4_t{(_Float16)(o[0] * norm), (_Float16)(o[1] * norm), (_Float16)(o[2] * norm), (_Float16)(o[3] * norm)};
 }
 
-// Notes: two int4 each, at most kGroups of them.
-constexpr size_t kNoteBytes = (size_t)kGroups * 2 * sizeof(int4);
+// Workgroups of a split launch: one per CU keeps the waves' shares equal in time (of two
+// on a CU the older one's loads go first: 64 requests of 8,192 positions, D = 128, the
+// first 256 workgroups were done after 230 us and the others after 313), two where a
+// wave's tiles in flight are small (8-bit heads of 64: 222 -> 195 us).
+template <int FMT, int D>
+constexpr int split_groups() {
+  typedef Shape<FMT, D> S;
+  return S::kAhead * 2 * S::kTile * S::kRow < 32768 ? 2 * kGroups : kGroups;
+}
+constexpr int kMostGroups = 2 * kGroups;
+
+// Notes: two int4 each, one a workgroup or segment, at most kMostGroups.
+constexpr size_t kNoteBytes = (size_t)kMostGroups * 2 * sizeof(int4);
 
 // Rows of a part: a segment's, of at most kTiles tiles.
 int part_rows(int64_t N, int group) {
@@ -1145,33 +1227,34 @@ int part_rows(int64_t N, int group) {
   return (int)(tiles < kTiles ? tiles : kTiles) * kRows;
 }
 
-// Without a split a segment's positions pass through one workgroup, 128 at a time,
-// and the second launch falls away.
-constexpr int kWholeMax = 256;
+// Whether every segment passes through one workgroup of its own, which spares the
+// second launch (about 5 us with what it waits for). A workgroup alone takes in about
+// 47 KB a us; split evenly, the whole call runs at about 6.4 GB a ms. Half of that time
+// is what the longest segment may take before the others wait for it. Measured, whole
+// against split: 64 requests of 1,000 positions, 8 key heads of 128 fp16 47 and 51 us,
+// 16 of 600 14 and 17; 16 of 2,048 with 4 heads 28 and 18 us, of 64 columns 18 and 15.
+// Without the host's lengths the sum is not known and counts as nothing.
+bool one_group_each(int64_t longest, int64_t sum, int heads, int64_t position_bytes) {
+  const double alone = (double)longest * position_bytes / 47e3;
+  const double together = (double)sum * heads * position_bytes / 6.4e6;
+  return alone <= together / 2 + 5.0;
+}
 constexpr int64_t kWholeGroups = 4096;
-
-// Workgroups of a split gdn_attn_k launch, whose 4 waves have a tile of tile_bytes in
-// flight each: about 32 MiB in all. More than the memory can serve in a few
-// microseconds only makes the first loads late, and unevenly so (16 requests of 2,048
-// positions, D = 256 fp16, 32 KiB tiles: 256 workgroups 33 us, 512 36, 1024 41; 64
-// requests of 8,192, D = 128, 16 KiB: 256 394 us, 512 350, 1024 347).
-constexpr int few_groups(int tile_bytes) { return tile_bytes >= 32768 ? kGroups / 2 : kGroups; }
 
 template <int FMT, int D>
 hipError_t launch_attn_d(const AttnArgs& p, void* workspace, hipStream_t stream) {
-  typedef Shape<FMT, D> S;
   SplitArgs sp{};
   const int64_t most = (int64_t)p.max_tokens * p.group;    // rows of a request and key head
   const bool few = most <= kRows;
   sp.seg_rows = few ? kRows : kTiles * kRows;
   const int64_t segments = ((int64_t)p.rows.N * p.group / sp.seg_rows + p.rows.R) * p.cache.Hk;
   int64_t groups = segments < kWholeGroups ? segments : kWholeGroups;
-  const bool whole = p.max_len <= kWholeMax;
+  const bool whole = one_group_each(p.max_len, p.sum_len, p.cache.Hk, 2 * Shape<FMT, D>::kRow);
   int64_t notes = 0;
   if (whole) {
     sp.chunk_shift = kWholeShift;
   } else {
-    groups = few ? few_groups(S::kTile * 2 * S::kBytes * D) : kRingGroups;
+    groups = few ? split_groups<FMT, D>() : kGroups;
     sp.notes = static_cast<int4*>(workspace);
     sp.parts = reinterpret_cast<float*>(static_cast<char*>(workspace) + kNoteBytes);
     sp.part_rows = few ? kRows : part_rows(p.rows.N, p.group);
@@ -1219,7 +1302,7 @@ hipError_t launch_attn(const AttnArgs& p, int io_dtype, void* workspace, hipStre
 
 size_t attn_workspace_bytes(int64_t N, int64_t R, int Hq, int Hk, int D) {
   if (N == 0 || R == 0) return 0;
-  return kNoteBytes + (size_t)2 * kGroups * part_rows(N, Hq / Hk) * (D + 2) * sizeof(float);
+  return kNoteBytes + (size_t)2 * (D == 64 ? kMostGroups : kGroups) * part_rows(N, Hq / Hk) * (D + 2) * sizeof(float);
 }
 
 }  // namespace gdn

@@ -416,10 +416,20 @@ int gdn_attn_forward(const gdn_attn_params* p, const gdn_attn_tensors* t, const 
     tokens = 0;
     for (int64_t r = 0; r < R; ++r) tokens = std::max(tokens, w.tokens(r));
   }
-  if (w.lens_host != nullptr) longest = *std::max_element(w.lens_host, w.lens_host + R);
+  int64_t sum = 0;
   if (p->window > 0) longest = std::min(longest, (int64_t)p->window + tokens);
+  if (w.lens_host != nullptr) {
+    const int64_t most = longest;
+    longest = 0;
+    for (int64_t r = 0; r < R; ++r) {
+      const int64_t n = std::min<int64_t>(w.lens_host[r], most);
+      longest = std::max(longest, n);
+      sum += n;
+    }
+  }
   a.max_tokens = (int32_t)tokens;
   a.max_len = (int32_t)longest;
+  a.sum_len = sum;
   a.cache = cache_args(*c);
   a.rows = row_args(w);
   return status_of(gdn::launch_attn(a, c->io_dtype, workspace, static_cast<hipStream_t>(stream)));

@@ -78,6 +78,7 @@ struct AttnArgs {
   int32_t Hq, group;            // group = Hq / Hk
   int32_t window;               // 0: none
   int32_t max_len;              // no request attends more positions, as far as the host knows
+  int64_t sum_len;              // attended positions of all requests, 0 where the host does not know
   int32_t max_tokens;           // no request has more tokens, as far as the host knows
   float scale;
   CacheArgs cache;
