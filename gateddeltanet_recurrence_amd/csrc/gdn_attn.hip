@@ -136,13 +136,18 @@ __device__ __forceinline__ Share find_share(const AttnArgs& p, const SplitArgs& 
   return w;
 }
 
+// The token of a request that a row belongs to.
+__device__ __forceinline__ int token_of(const AttnArgs& p, const Plan& s, int row) {
+  return s.T == 1 ? 0 : (int)((unsigned)row / (unsigned)p.group);
+}
+
 // The next segment of a share: units [c0, c1) of (request, rows from seg_row on, key
 // head h); the share's u moves past it.
 struct Segment {
   Plan s;
   int h, seg_row, rows, c0, c1;
   int t0, end;                                             // positions [t0, end)
-  int note, parts;                                         // its place among the notes, the shares that hold it
+  int note, last_unit;                                     // its place among the notes, its last unit
 };
 
 __device__ __forceinline__ Segment next_segment(const AttnArgs& p, const SplitArgs& sp, Share& w) {
@@ -155,15 +160,14 @@ __device__ __forceinline__ Segment next_segment(const AttnArgs& p, const SplitAr
   const unsigned local = w.u - w.r_first, seg = local / (unsigned)x.s.chunks;
   x.c0 = local - seg * x.s.chunks;
   x.c1 = min(x.s.chunks, x.c0 + (w.u_end - w.u));
-  x.h = seg / (unsigned)x.s.segs;
+  x.h = x.s.segs == 1 ? seg : seg / (unsigned)x.s.segs;
   x.seg_row = (int)(seg - x.h * x.s.segs) * sp.seg_rows;
   x.note = sp.max_segs > 0 ? (w.r * p.cache.Hk + x.h) * sp.max_segs + (int)(seg - x.h * x.s.segs) : (int)blockIdx.x;
-  // the shares from this one on that hold the segment, which begins in this one if c0 = 0
-  x.parts = (int)((unsigned)(w.u - x.c0 + x.s.chunks - 1) / (unsigned)w.size) - (int)blockIdx.x + 1;
+  x.last_unit = w.u - x.c0 + x.s.chunks - 1;
   w.u += x.c1 - x.c0;
   x.rows = min(sp.seg_rows, x.s.T * p.group - x.seg_row);
   const int cap = p.cache.max_pages << p.cache.page_shift;
-  const int64_t past_last = x.s.len - x.s.T + (int)((unsigned)(x.seg_row + x.rows - 1) / (unsigned)p.group) + 1;
+  const int64_t past_last = x.s.len - x.s.T + token_of(p, x.s, x.seg_row + x.rows - 1) + 1;
   x.t0 = x.s.base + (int)((int64_t)x.c0 << sp.chunk_shift);
   x.end = (int)min((int64_t)x.s.base + ((int64_t)x.c1 << sp.chunk_shift), (int64_t)clamp_pos(past_last, cap));
   return x;
@@ -172,8 +176,9 @@ __device__ __forceinline__ Segment next_segment(const AttnArgs& p, const SplitAr
 // The workgroup that begins a segment notes what the join has to know of it: the
 // parts, the first of them, where the rows belong. In the order of workgroups there
 // is one note each, of the last segment that it begins and leaves to others.
-__device__ __forceinline__ void note_segment(const SplitArgs& sp, const Segment& x) {
-  const int parts = x.c0 == 0 && x.c1 == x.s.chunks ? 0 : x.parts;
+__device__ __forceinline__ void note_segment(const SplitArgs& sp, const Segment& x, int share) {
+  // the shares from this one on that hold the segment
+  const int parts = x.c1 == x.s.chunks ? 0 : (int)((unsigned)x.last_unit / (unsigned)share) - (int)blockIdx.x + 1;
   sp.notes[2 * x.note] = int4{parts, (int)blockIdx.x, x.rows, x.seg_row};
   sp.notes[2 * x.note + 1] = int4{x.s.start, x.h, 0, 0};
 }
@@ -190,11 +195,10 @@ __device__ __forceinline__ Rows rows_of(const AttnArgs& p, const Plan& s, int ro
   Rows x;
   const int cap = p.cache.max_pages << p.cache.page_shift;
   const int last = row0 + max(rows, 1) - 1, row = min(row0 + n, last);
-  x.j = (int)((unsigned)row / (unsigned)p.group);
+  x.j = token_of(p, s, row);
   x.head = row - x.j * p.group;
   const int64_t before = s.len - s.T + 1;                  // one past the first token's newest position
-  const int64_t past = before + x.j, past0 = before + (int)((unsigned)row0 / (unsigned)p.group),
-                past1 = before + (int)((unsigned)last / (unsigned)p.group);
+  const int64_t past = before + x.j, past0 = before + token_of(p, s, row0), past1 = before + token_of(p, s, last);
   x.hi = n < rows ? clamp_pos(past, cap) : 0;
   x.hi_min = clamp_pos(past0, cap);
   x.hi_max = clamp_pos(past1, cap);
@@ -251,7 +255,7 @@ __device__ __forceinline__ void store_row(const AttnArgs& p, const SplitArgs& sp
                                           int d, float M, float l, float4_t o) {
   if (complete) {
     typedef typename std::conditional<FMT == kF32, float, _Float16>::type IO;
-    const int row = sg.seg_row + rr, j = (int)((unsigned)row / (unsigned)p.group);
+    const int row = sg.seg_row + rr, j = token_of(p, sg.s, row);
     IO* out = static_cast<IO*>(p.output) + ((int64_t)(sg.s.start + j) * p.Hq + sg.h * p.group + row - j * p.group) * D + d;
     const float norm = l == 0.f ? 0.f : 1.f / l;
     if constexpr (FMT == kF32)
@@ -348,12 +352,12 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_attn_k(AttnArgs p, SplitArgs 
   const float to_log2 = p.scale * 1.4426950408889634f;
   const IO* __restrict__ qs = static_cast<const IO*>(p.q);
   if (tid == 0 && sp.notes != nullptr && sp.max_segs == 0) sp.notes[2 * blockIdx.x] = int4{0, 0, 0, 0};
+  bool again = false;
   // byte offsets of this lane in a block: 16 bytes of k in row n; its columns of v in rows 4 g + (0 .. 3)
   const int k_at = n * S::kRow + 16 * g, v_at = 4 * g * S::kRow + S::kCols * S::kBytes * n;
 
   while (sh.u < sh.u_end) {
     const Segment sg = next_segment(p, sp, sh);
-    if (tid == 0 && sp.notes != nullptr && sg.c0 == 0 && (sp.max_segs > 0 || sg.c1 < sg.s.chunks)) note_segment(sp, sg);
     const Plan& s = sg.s;
     const int rows = sg.rows, end = sg.end;
     const bool complete = sg.c0 == 0 && sg.c1 == s.chunks;
@@ -620,9 +624,12 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_attn_k(AttnArgs p, SplitArgs 
       }
     }
 
+    if (tid == 0 && sp.notes != nullptr && sg.c0 == 0 && (sp.max_segs > 0 || !complete)) note_segment(sp, sg, sh.size);
+
     // ---- join the waves
     l = row_sum(l);
-    __syncthreads();                                       // the last segment's sums have been read
+    if (again) __syncthreads();                            // the last segment's sums have been read
+    again = true;
     if (g == 0) {
       stats[wave][n][0] = M;
       stats[wave][n][1] = l;
@@ -813,7 +820,6 @@ __global__ void __launch_bounds__(kRingBlock, 3) gdn_attn_rows_k(AttnArgs p, Spl
 
   while (w.u < w.u_end) {
     const Segment sg = next_segment(p, sp, w);
-    if (tid == 0 && sp.notes != nullptr && sg.c0 == 0 && (sp.max_segs > 0 || sg.c1 < sg.s.chunks)) note_segment(sp, sg);
     const Plan& s = sg.s;
     const int h = sg.h, seg_row = sg.seg_row, seg_rows = sg.rows, t0 = sg.t0, end = sg.end;
     const int stages = end > t0 ? (end - t0 + S::kStage - 1) / S::kStage : 0;
@@ -1077,6 +1083,8 @@ __global__ void __launch_bounds__(kRingBlock, 3) gdn_attn_rows_k(AttnArgs p, Spl
     }
     stage0 += stages;
     if (lane == 0) *(volatile int*)&finished[wave] = stage0;
+
+    if (tid == 0 && sp.notes != nullptr && sg.c0 == 0 && (sp.max_segs > 0 || !complete)) note_segment(sp, sg, w.size);
 
     // ---- join the waves
     l = row_sum(l);
