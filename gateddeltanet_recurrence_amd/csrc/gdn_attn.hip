@@ -317,8 +317,12 @@ struct Pages {
   table_t table;
   int h, end;
 
-  __device__ __forceinline__ Pages(const AttnArgs& args, int r, int head, int past)
-      : p(args), table((table_t)(args.cache.table + (int64_t)r * args.cache.max_pages)), h(head), end(past) {}
+  __device__ __forceinline__ explicit Pages(const AttnArgs& args) : p(args), table(nullptr), h(0), end(0) {}
+  __device__ __forceinline__ void of(int r, int head, int past) {
+    table = (table_t)(p.cache.table + (int64_t)r * p.cache.max_pages);
+    h = head;
+    end = past;
+  }
 
   // The table's entry for the block at pos (any entry where pos is past the table), to be checked below.
   __device__ __forceinline__ int entry(int pos) const {
@@ -356,65 +360,66 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_attn_k(AttnArgs p, SplitArgs 
   // byte offsets of this lane in a block: 16 bytes of k in row n; its columns of v in rows 4 g + (0 .. 3)
   const int k_at = n * S::kRow + 16 * g, v_at = 4 * g * S::kRow + S::kCols * S::kBytes * n;
 
-  while (sh.u < sh.u_end) {
-    const Segment sg = next_segment(p, sp, sh);
-    const Plan& s = sg.s;
-    const int rows = sg.rows, end = sg.end;
-    const bool complete = sg.c0 == 0 && sg.c1 == s.chunks;
-    const Rows rw = rows_of(p, s, sg.seg_row, rows, n);
-    const int lo = rw.lo, hi = rw.hi;
-    const Pages pages(p, sh.r, sg.h, end);
+  if (sh.u >= sh.u_end) return;
+  Segment sg;
+  Rows rw;
+  Pages pages(p);
+  int t = 0;
+  half8_t qh[FMT == kF32 ? 1 : D / 32];                    // q, the first product's second operand
+  float4_t qf[FMT == kF32 ? D / 16 : 1];
 
-    // ---- tiles: this wave's are t0 + (wave + kWaves i) kTile; U of them are in flight, tile i in buffer i % U.
-    // A load past `end` or without a page has an empty range: it costs no traffic, and the number of
-    // loads in flight stays the same, so that the wait for a tile waits for nothing younger.
-    uint32_t kw[U][S::kBlocks][S::kKLoads][4], vw[U][S::kPos][S::kSets][S::kVWords];
-    uint32_t kscale[U][S::kBlocks], vscale[U][S::kBlocks];  // exponent bytes of this lane's positions
-    int entry[U][S::kBlocks], held[U][S::kBlocks];          // table entries of the next tile, pages of this one
-    constexpr int kStep = kWaves * S::kTile;
-    auto look_up = [&](int u, int t) {
+  // ---- tiles: this wave's are t0 + (wave + kWaves i) kTile; U of them are in flight, tile i in buffer i % U.
+  // A load past `end` or without a page has an empty range: it costs no traffic, and the number of
+  // loads in flight stays the same, so that the wait for a tile waits for nothing younger.
+  uint32_t kw[U][S::kBlocks][S::kKLoads][4], vw[U][S::kPos][S::kSets][S::kVWords];
+  uint32_t kscale[U][S::kBlocks], vscale[U][S::kBlocks];  // exponent bytes of this lane's positions
+  int entry[U][S::kBlocks], held[U][S::kBlocks];          // table entries of the next tile, pages of this one
+  constexpr int kStep = kWaves * S::kTile;
+  auto look_up = [&](int u, int t) {
 #pragma unroll
-      for (int a = 0; a < S::kBlocks; ++a) entry[u][a] = pages.entry(t + 16 * a);
-    };
-    auto load_k = [&](int u, int t) {
+    for (int a = 0; a < S::kBlocks; ++a) entry[u][a] = pages.entry(t + 16 * a);
+  };
+  auto load_k = [&](int u, int t) {
 #pragma unroll
-      for (int a = 0; a < S::kBlocks; ++a) {
-        const int pos = t + 16 * a, page = pages.page(entry[u][a], pos);
-        const int64_t row = pages.row(page, pos);
-        const int count = pages.rows(page, pos);
-        held[u][a] = page;
-        const rsrc_t rs = make_rsrc(static_cast<const char*>(p.cache.k) + row * S::kRow, count * S::kRow);
+    for (int a = 0; a < S::kBlocks; ++a) {
+      const int pos = t + 16 * a, page = pages.page(entry[u][a], pos);
+      const int64_t row = pages.row(page, pos);
+      const int count = pages.rows(page, pos);
+      held[u][a] = page;
+      const rsrc_t rs = make_rsrc(static_cast<const char*>(p.cache.k) + row * S::kRow, count * S::kRow);
 #pragma unroll
-        for (int c = 0; c < S::kKLoads; ++c) load_words<4, 0>(rs, k_at + 64 * c, kw[u][a][c]);
-        if constexpr (FMT == kE4M3)
-          kscale[u][a] = __builtin_amdgcn_raw_buffer_load_b32(make_rsrc(p.cache.k_scales + row, count > 0 ? 16 : 0), 4 * g, 0, 0);
-      }
-    };
-    auto load_v = [&](int u, int t) {
+      for (int c = 0; c < S::kKLoads; ++c) load_words<4, 0>(rs, k_at + 64 * c, kw[u][a][c]);
+      if constexpr (FMT == kE4M3)
+        kscale[u][a] = __builtin_amdgcn_raw_buffer_load_b32(make_rsrc(p.cache.k_scales + row, count > 0 ? 16 : 0), 4 * g, 0, 0);
+    }
+  };
+  auto load_v = [&](int u, int t) {
 #pragma unroll
-      for (int a = 0; a < S::kBlocks; ++a) {
-        const int pos = t + 16 * a, page = held[u][a];
-        const int64_t row = pages.row(page, pos);
-        const int count = pages.rows(page, pos);
-        const rsrc_t rs = make_rsrc(static_cast<const char*>(p.cache.v) + row * S::kRow, count * S::kRow);
+    for (int a = 0; a < S::kBlocks; ++a) {
+      const int pos = t + 16 * a, page = held[u][a];
+      const int64_t row = pages.row(page, pos);
+      const int count = pages.rows(page, pos);
+      const rsrc_t rs = make_rsrc(static_cast<const char*>(p.cache.v) + row * S::kRow, count * S::kRow);
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
+      for (int e = 0; e < 4; ++e)
 #pragma unroll
-          for (int c = 0; c < S::kSets; ++c)
-            load_words<S::kVWords, kStream>(rs, v_at + e * S::kRow + 16 * S::kCols * S::kBytes * c, vw[u][4 * a + e][c]);
-        if constexpr (FMT == kE4M3)
-          vscale[u][a] = __builtin_amdgcn_raw_buffer_load_b32(make_rsrc(p.cache.v_scales + row, count > 0 ? 16 : 0), 4 * g, 0, 0);
-      }
-    };
+        for (int c = 0; c < S::kSets; ++c)
+          load_words<S::kVWords, kStream>(rs, v_at + e * S::kRow + 16 * S::kCols * S::kBytes * c, vw[u][4 * a + e][c]);
+      if constexpr (FMT == kE4M3)
+        vscale[u][a] = __builtin_amdgcn_raw_buffer_load_b32(make_rsrc(p.cache.v_scales + row, count > 0 ? 16 : 0), 4 * g, 0, 0);
+    }
+  };
 
-    int t = sg.t0 + wave * S::kTile;
+  // The next segment: its q, then its first tiles, on their way while the last one's waves are joined.
+  auto begin = [&]() {
+    sg = next_segment(p, sp, sh);
+    pages.of(sh.r, sg.h, sg.end);
+    t = sg.t0 + wave * S::kTile;
 #pragma unroll
     for (int u = 0; u < U; ++u) look_up(u, t + u * kStep);
-
-    // q as the first product's second operand, in the order k is loaded in
-    const IO* q = qs + (int64_t)(s.start + rw.j) * p.q_stride + (int64_t)(sg.h * p.group + rw.head) * D;
-    half8_t qh[FMT == kF32 ? 1 : D / 32];
-    float4_t qf[FMT == kF32 ? D / 16 : 1];
+    rw = rows_of(p, sg.s, sg.seg_row, sg.rows, n);
+    const IO* q = qs + (int64_t)(sg.s.start + rw.j) * p.q_stride + (int64_t)(sg.h * p.group + rw.head) * D;
+    // in the order k is loaded in
     if constexpr (FMT == kF32) {
 #pragma unroll
       for (int c = 0; c < D / 16; ++c) qf[c] = *reinterpret_cast<const float4_t*>(q + 16 * c + 4 * g);
@@ -434,7 +439,11 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_attn_k(AttnArgs p, SplitArgs 
       look_up(u, t + (u + U) * kStep);
     }
     __builtin_amdgcn_sched_barrier(0);
+  };
 
+  begin();
+  for (;;) {
+    const int lo = rw.lo, hi = rw.hi, end = sg.end;
     float4_t acc[kAcc];
 #pragma unroll
     for (int i = 0; i < kAcc; ++i) acc[i] = float4_t{0.f, 0.f, 0.f, 0.f};
@@ -624,7 +633,12 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_attn_k(AttnArgs p, SplitArgs 
       }
     }
 
-    if (tid == 0 && sp.notes != nullptr && sg.c0 == 0 && (sp.max_segs > 0 || !complete)) note_segment(sp, sg, sh.size);
+    const Segment done = sg;
+    const int rows = done.rows;
+    const bool complete = done.c0 == 0 && done.c1 == done.s.chunks;
+    const bool more = sh.u < sh.u_end;
+    if (more) begin();
+    if (tid == 0 && sp.notes != nullptr && done.c0 == 0 && (sp.max_segs > 0 || !complete)) note_segment(sp, done, sh.size);
 
     // ---- join the waves
     l = row_sum(l);
@@ -665,8 +679,9 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_attn_k(AttnArgs p, SplitArgs 
       float4_t o = *reinterpret_cast<const float4_t*>(&sums[0][rr][d]);
 #pragma unroll
       for (int w = 1; w < kWaves; ++w) o += *reinterpret_cast<const float4_t*>(&sums[w][rr][d]);
-      store_row<FMT, D>(p, sp, sg, complete, rr, d, joined[rr][0], joined[rr][1], o);
+      store_row<FMT, D>(p, sp, done, complete, rr, d, joined[rr][0], joined[rr][1], o);
     }
+    if (!more) return;
   }
 }
 
@@ -818,8 +833,10 @@ __global__ void __launch_bounds__(kRingBlock, 3) gdn_attn_rows_k(AttnArgs p, Spl
   int stage0 = 0;                                          // stages of the segments before this one
   if (tid == 0 && sp.notes != nullptr && sp.max_segs == 0) sp.notes[2 * blockIdx.x] = int4{0, 0, 0, 0};
 
-  while (w.u < w.u_end) {
-    const Segment sg = next_segment(p, sp, w);
+  if (w.u >= w.u_end) return;
+  Segment sg = next_segment(p, sp, w);
+  for (;;) {
+    const bool more = w.u < w.u_end;
     const Plan& s = sg.s;
     const int h = sg.h, seg_row = sg.seg_row, seg_rows = sg.rows, t0 = sg.t0, end = sg.end;
     const int stages = end > t0 ? (end - t0 + S::kStage - 1) / S::kStage : 0;
@@ -853,9 +870,11 @@ __global__ void __launch_bounds__(kRingBlock, 3) gdn_attn_rows_k(AttnArgs p, Spl
         lds_store(landed_at, stage0 + ++i);
       }
       stage0 += stages;
+      if (more) sg = next_segment(p, sp, w);
       __syncthreads();                                     // A
       __syncthreads();                                     // B
       __syncthreads();                                     // C
+      if (!more) return;
       continue;
     }
 
@@ -1130,6 +1149,8 @@ __global__ void __launch_bounds__(kRingBlock, 3) gdn_attn_rows_k(AttnArgs p, Spl
       store_row<FMT, D>(p, sp, sg, complete, rr, 4 * unit, joined[rr / kRows][rn][0], joined[rr / kRows][rn][1], o);
     }
     __syncthreads();                                       // C: the ring is the loaders' again
+    if (!more) return;
+    sg = next_segment(p, sp, w);
   }
 }
 
