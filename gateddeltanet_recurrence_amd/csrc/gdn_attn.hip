@@ -88,6 +88,7 @@ __device__ __forceinline__ Plan plan_of(const AttnArgs& p, const SplitArgs& sp, 
   s.hi = clamp_pos(s.len, cap);
   s.base = p.window > 0 ? clamp_pos(s.len - s.T + 1 - p.window, s.hi) & ~31 : 0;
   s.segs = (int)(((unsigned)(s.T * p.group) + sp.seg_rows - 1) / (unsigned)sp.seg_rows);
+  if (sp.max_segs > 0) s.segs = min(s.segs, sp.max_segs);  // no note past the request's, whatever cu_seqlens holds
   s.chunks = s.T > 0 ? max((int)(((int64_t)s.hi - s.base + (1ll << sp.chunk_shift) - 1) >> sp.chunk_shift), 1) : 0;
   return s;
 }
@@ -642,6 +643,7 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_attn_k(AttnArgs p, SplitArgs 
 
     // ---- join the waves
     l = row_sum(l);
+    if (l != l) M = INFINITY;                              // a NaN score is no maximum, but has to show
     if (again) __syncthreads();                            // the last segment's sums have been read
     again = true;
     if (g == 0) {
@@ -1107,6 +1109,7 @@ __global__ void __launch_bounds__(kRingBlock, 3) gdn_attn_rows_k(AttnArgs p, Spl
 
     // ---- join the waves
     l = row_sum(l);
+    if (l != l) M = INFINITY;                              // a NaN score is no maximum, but has to show
     if (g == 0) {
       stats[wave][n][0] = M;
       stats[wave][n][1] = l;

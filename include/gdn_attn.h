@@ -174,12 +174,17 @@ typedef struct gdn_kv_tensors {
                                     k_stride apart; gdn_kv_read writes dense rows    */
   void* v;                       /* likewise                                        */
   const int32_t* cu_seqlens;     /* device, i32 [R + 1], or NULL                    */
-  const int32_t* cu_seqlens_host;/* host mirror or NULL, as in gdn.h                */
+  const int32_t* cu_seqlens_host;/* host mirror or NULL, as in gdn.h: what it says
+                                    must be what cu_seqlens holds when the work runs,
+                                    so a captured call whose cu_seqlens changes
+                                    between replays gives none                      */
   const int32_t* seq_lens;       /* device, i32 [R]                                 */
   const int32_t* seq_lens_host;  /* host mirror or NULL; every value must lie in
                                     [T_r, max_pages * page_size], else
                                     GDN_ERR_CAPACITY (T_r is checked where the host
-                                    knows it)                                       */
+                                    knows it). Besides the checks it only guides how
+                                    the work is split: a captured call may be replayed
+                                    with other lengths                              */
   const void* q;                 /* with rotary_dim > 0 and Hq > 0: rotated into q_out */
   void* q_out;                   /* io [N, Hq, D] dense, or q itself (in place)      */
   const int32_t* positions;      /* device, i32 [N]: rotary positions, or NULL for
@@ -227,11 +232,13 @@ typedef struct gdn_attn_tensors {
  * scale * q[n, h] . k_p. Token j of request r (position P = seq_lens[r] - T_r + j)
  * attends positions max(0, P - window + 1) .. P that have a page; a token that
  * attends none gives zeros. What the cache holds at other positions has no
- * influence, whatever it is. Scores, weights, sums and the output accumulate in FP32;
- * FP16 io rounds the weights (at most 1, relative to the row's largest) to FP16 for
- * the product with v.
- * Any number of tokens per request is taken; the kernel is made for decode and
- * verify, where the cache is read once for up to 16 rows (tokens x Hq / Hk).
+ * influence, whatever it is. A row whose scores are all -inf gives zeros, too, and one
+ * with a NaN score NaN. Scores, weights, sums and the output accumulate in FP32; FP16 io
+ * rounds the weights (at most 1, relative to the row's largest) to FP16 for the product
+ * with v.
+ * Any number of tokens per request is taken; the kernels are made for decode and
+ * verify, where the cache is read once for up to 64 rows (tokens x Hq / Hk).
+ * (N + R) Hq D / 64 is at most 2^30, else GDN_ERR_SHAPE.
  * The workspace (gdn_attn_workspace_bytes() bytes, disjoint from every tensor, 16-byte
  * aligned) needs no initial value; calls that overlap in time, and captured graphs
  * that may run at once, need one each.
