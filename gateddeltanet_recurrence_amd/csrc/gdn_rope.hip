@@ -108,6 +108,32 @@ __device__ __forceinline__ int64_t position_of(const RowArgs& p, int n, int& r) 
   return (int64_t)p.seq_lens[r] - row_start(p, r + 1) + n;
 }
 
+// factor cos t and factor sin t, rounded once to float wherever the position lies: t is
+// reduced to y, at most an eighth of a turn, in turns and in double precision, and
+// the power series' terms up to y^13 and y^12 leave less than 2^-40.
+__device__ __forceinline__ float2 turn_of(double t, double factor) {
+  constexpr double kInvTwoPi = 0.15915494309189533577, kTwoPi = 6.283185307179586477;
+  const double turn = t * kInvTwoPi, quarter = rint(4.0 * turn);
+  const double y = fma(-0.25, quarter, turn) * kTwoPi, z = y * y;
+  double s = 1.0 / 6227020800.0, c = 1.0 / 479001600.0;    // 1 / 13!, 1 / 12!
+  s = fma(s, z, -1.0 / 39916800.0);
+  c = fma(c, z, -1.0 / 3628800.0);
+  s = fma(s, z, 1.0 / 362880.0);
+  c = fma(c, z, 1.0 / 40320.0);
+  s = fma(s, z, -1.0 / 5040.0);
+  c = fma(c, z, -1.0 / 720.0);
+  s = fma(s, z, 1.0 / 120.0);
+  c = fma(c, z, 1.0 / 24.0);
+  s = fma(s, z, -1.0 / 6.0);
+  c = fma(c, z, -0.5);
+  s = fma(s * z, y, y) * factor;
+  c = fma(c, z, 1.0) * factor;
+  const int q = (int)(quarter - 4.0 * floor(0.25 * quarter));
+  const float fs = (float)s, fc = (float)c;
+  const float a = q & 1 ? fs : fc, b = q & 1 ? fc : fs;    // cos, sin after q quarter turns
+  return float2{q == 1 || q == 2 ? -a : a, q >= 2 ? -b : b};
+}
+
 template <typename IO, int D, bool CACHE, bool E4M3>
 __global__ void __launch_bounds__(kThreads) gdn_rope_k(RopeArgs p) {
   constexpr int V = Vec<IO>::n;            // elements of a vector
@@ -134,15 +160,9 @@ __global__ void __launch_bounds__(kThreads) gdn_rope_k(RopeArgs p) {
     if ((int)threadIdx.x < tokens) pos_of[threadIdx.x] = (double)p.positions[n0 + threadIdx.x];
   }
   __syncthreads();
-  // The angle in turns, reduced to [-1/2, 1/2] in double precision: what is left
-  // is exact to 2^-25 of a turn in float, wherever the position lies.
-  constexpr double kInvTwoPi = 0.15915494309189533577;
   for (int i = threadIdx.x; i < tokens * pairs; i += kThreads) {
     const int t = i / pairs;
-    const double turn = pos_of[t] * (p.inv_freq[i - t * pairs] * kInvTwoPi);
-    float s, c;
-    sincospif(2.f * (float)(turn - rint(turn)), &s, &c);
-    turns[i] = float2{c * p.factor, s * p.factor};
+    turns[i] = turn_of(pos_of[t] * p.inv_freq[i - t * pairs], (double)p.factor);
   }
   __syncthreads();
 
