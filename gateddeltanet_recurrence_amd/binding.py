@@ -260,11 +260,12 @@ def _need(x, name, shape, dtype=None):
         raise ValueError(f"{name} must be a GPU tensor")
 
 
-def _stream_handle(stream) -> Optional[int]:
+def _stream_handle(stream, index: Optional[int] = None) -> Optional[int]:
+    """The handle of `stream`; of None, the current stream's on GPU `index` (default: the current one)."""
     if stream is None:
         # the raw handle: making the Stream object of torch.cuda.current_stream() takes 2.7 us
         c = _torch()._C
-        return c._cuda_getCurrentRawStream(c._cuda_getDevice())
+        return c._cuda_getCurrentRawStream(c._cuda_getDevice() if index is None else index)
     if isinstance(stream, int):
         return stream
     return int(stream.cuda_stream)
@@ -276,6 +277,8 @@ def _host_i32(arr):
         return None, None
     import numpy as np
     if type(arr) is np.ndarray and arr.dtype == np.int32 and arr.flags.c_contiguous:
+        if arr.flags.writeable and arr.size > 0:             # through the buffer: 0.3 us instead of 0.7
+            return arr, ctypes.addressof(ctypes.c_char.from_buffer(arr))
         return arr, arr.ctypes.data
     if hasattr(arr, "numpy") and hasattr(arr, "is_cuda"):
         if arr.is_cuda:
@@ -820,8 +823,7 @@ def _out_rows(out, of, name):
 
 
 def _int_vector(x, name, n, index):
-    if x.dtype is not _torch().int32 or x.dim() != 1 or x.shape[0] != n or x.get_device() != index or \
-            not x.is_contiguous():
+    if x.shape != (n,) or x.dtype is not _torch().int32 or x.get_device() != index or not x.is_contiguous():
         raise ValueError(f"{name} must be a contiguous int32 [{n}] on GPU {index}")
     return x.data_ptr()
 
@@ -906,7 +908,7 @@ def gdn_rope_forward(q, k, positions, inv_freq, q_out, k_out, *, rope_layout: in
     _on_current_device(index)
     st = lib().gdn_rope_forward(
         GdnRopeParams(N, Hq, Hk, D, _io_code(io), 2 * inv_freq.shape[0], rope_layout, rope_factor, qs, ks),
-        GdnRopeTensors(qp, kp, pos, freq, qop, kop), _stream_handle(stream))
+        GdnRopeTensors(qp, kp, pos, freq, qop, kop), _stream_handle(stream, index))
     if check and st != GDN_OK:
         raise GDNError(st, "gdn_rope_forward")
     return st
@@ -949,7 +951,7 @@ def gdn_kv_write(k, v, cache: KVCache, seq_lens, cu_seqlens=None, *, q=None, q_o
                                                  seq_lens_host)
     st = lib().gdn_kv_write(GdnKvParams(N, R, Hq, rot, rope_layout, rope_factor, qs, ks, vs),
                             GdnKvTensors(k.data_ptr(), v.data_ptr(), cu, cu_h, lens, len_h, qp, qop, pos, freq),
-                            cache.struct, _stream_handle(stream))
+                            cache.struct, _stream_handle(stream, index))
     del keep
     if check and st != GDN_OK:
         raise GDNError(st, "gdn_kv_write")
@@ -968,7 +970,7 @@ def gdn_kv_read(k, v, cache: KVCache, seq_lens, cu_seqlens=None, *, num_reqs: Op
     R, lens, cu, len_h, cu_h, keep = _cache_rows(cache, seq_lens, cu_seqlens, num_reqs, cu_seqlens_host,
                                                  seq_lens_host)
     st = lib().gdn_kv_read(GdnKvParams(N, R), GdnKvTensors(k.data_ptr(), v.data_ptr(), cu, cu_h, lens, len_h),
-                           cache.struct, _stream_handle(stream))
+                           cache.struct, _stream_handle(stream, index))
     del keep
     if check and st != GDN_OK:
         raise GDNError(st, "gdn_kv_read")
@@ -1009,7 +1011,7 @@ def gdn_attn_forward(q, cache: KVCache, seq_lens, cu_seqlens, output, *, scale: 
                                                  seq_lens_host)
     st = lib().gdn_attn_forward(GdnAttnParams(N, R, Hq, scale, window, qs),
                                 GdnAttnTensors(q.data_ptr(), cu, cu_h, lens, len_h, output.data_ptr()), cache.struct,
-                                ws, ws_bytes, _stream_handle(stream))
+                                ws, ws_bytes, _stream_handle(stream, index))
     del keep
     if check and st != GDN_OK:
         raise GDNError(st, "gdn_attn_forward")
