@@ -44,8 +44,7 @@ namespace gdn {
 
 namespace {
 
-constexpr int kWaves = 4;                 // of gdn_attn_k
-constexpr int kThreads = 64 * kWaves;
+constexpr int kThreads = 256;             // of gdn_attn_join_k
 constexpr int kRingWaves = 8;             // computing waves of gdn_attn_rows_k
 constexpr int kRingThreads = 64 * kRingWaves;
 constexpr int kRingBlock = kRingThreads + 128;   // with a loader wave each for k and v
@@ -79,11 +78,11 @@ struct Plan {
 
 __device__ __forceinline__ int clamp_pos(int64_t x, int hi) { return (int)(x < 0 ? 0 : x > hi ? hi : x); }
 
-__device__ __forceinline__ Plan plan_of(const AttnArgs& p, const SplitArgs& sp, int r) {
+__device__ __forceinline__ Plan plan_of(const AttnArgs& p, const SplitArgs& sp, int start, int T, int len) {
   Plan s;
-  s.start = row_start(p.rows, r);
-  s.T = max(row_start(p.rows, r + 1) - s.start, 0);
-  s.len = p.rows.seq_lens[r];
+  s.start = start;
+  s.T = T;
+  s.len = len;
   const int cap = p.cache.max_pages << p.cache.page_shift;
   s.hi = clamp_pos(s.len, cap);
   s.base = p.window > 0 ? clamp_pos(s.len - s.T + 1 - p.window, s.hi) & ~31 : 0;
@@ -91,6 +90,11 @@ __device__ __forceinline__ Plan plan_of(const AttnArgs& p, const SplitArgs& sp, 
   if (sp.max_segs > 0) s.segs = min(s.segs, sp.max_segs);  // no note past the request's, whatever cu_seqlens holds
   s.chunks = s.T > 0 ? max((int)(((int64_t)s.hi - s.base + (1ll << sp.chunk_shift) - 1) >> sp.chunk_shift), 1) : 0;
   return s;
+}
+
+__device__ __forceinline__ Plan plan_of(const AttnArgs& p, const SplitArgs& sp, int r) {
+  const int start = row_start(p.rows, r);
+  return plan_of(p, sp, start, max(row_start(p.rows, r + 1) - start, 0), p.rows.seq_lens[r]);
 }
 
 // The launch bounds the units of all requests by 2^30.
@@ -115,17 +119,29 @@ __device__ __forceinline__ int wave_scan(int x) {
 // whose units begin at r_first. Every wave finds it by itself.
 struct Share {
   int u, u_end, r, r_first, size;
+  int start, T, len;                                       // of request `lane`, where there are at most 64
 };
 
 __device__ __forceinline__ Share find_share(const AttnArgs& p, const SplitArgs& sp, int lane) {
   const int R = p.rows.R, per = (R + 63) >> 6;             // requests a lane sums
   const int r0 = min(lane * per, R), r1 = min(r0 + per, R);
   int mine = 0;
+  Share w;
+  w.start = w.T = w.len = 0;
+  if (R <= 64) {
+    if (r0 < r1) {
+      const Plan s = plan_of(p, sp, r0);
+      mine = units_of(s, p.cache.Hk);
+      w.start = s.start;
+      w.T = s.T;
+      w.len = (int)s.len;
+    }
+  } else {
 #pragma unroll 4
-  for (int r = r0; r < r1; ++r) mine += units_of(plan_of(p, sp, r), p.cache.Hk);
+    for (int r = r0; r < r1; ++r) mine += units_of(plan_of(p, sp, r), p.cache.Hk);
+  }
   const int after = wave_scan(mine), before = after - mine;
   const int total = __builtin_amdgcn_readlane(after, 63);
-  Share w;
   const int share = w.size = share_of(total, (int)gridDim.x);
   w.u = (int)min((int64_t)blockIdx.x * share, (int64_t)total);
   w.u_end = min(w.u + share, total);
@@ -153,10 +169,16 @@ struct Segment {
 
 __device__ __forceinline__ Segment next_segment(const AttnArgs& p, const SplitArgs& sp, Share& w) {
   Segment x;
-  x.s = plan_of(p, sp, w.r);
+  // of at most 64 requests each lane holds one: no load in the way of the table's
+  const auto plan_at = [&](int r) {
+    return p.rows.R <= 64 ? plan_of(p, sp, __builtin_amdgcn_readlane(w.start, r), __builtin_amdgcn_readlane(w.T, r),
+                                    __builtin_amdgcn_readlane(w.len, r))
+                          : plan_of(p, sp, r);
+  };
+  x.s = plan_at(w.r);
   while (w.u - w.r_first >= units_of(x.s, p.cache.Hk)) {   // requests without tokens have no units
     w.r_first += units_of(x.s, p.cache.Hk);
-    x.s = plan_of(p, sp, ++w.r);
+    x.s = plan_at(++w.r);
   }
   const unsigned local = w.u - w.r_first, seg = local / (unsigned)x.s.chunks;
   x.c0 = local - seg * x.s.chunks;
@@ -274,7 +296,7 @@ __device__ __forceinline__ void store_row(const AttnArgs& p, const SplitArgs& sp
   }
 }
 
-template <int FMT, int D>
+template <int FMT, int D, int WAVES>
 struct Shape {
   static constexpr int kBytes = FMT == kF32 ? 4 : FMT == kF16 ? 2 : 1;   // of a cache element
   static constexpr int kRow = D * kBytes;                                // bytes of a position's k or v
@@ -286,11 +308,11 @@ struct Shape {
   static constexpr int kCols = FMT == kF32 ? 4 : FMT == kF16 ? (D / 16 < 8 ? D / 16 : 8) : D / 16;
   static constexpr int kSets = D / (16 * kCols);
   static constexpr int kVWords = kCols * kBytes / 4;                     // dwords of a set in one position
-  // tiles a wave has in flight: 32 KiB, at most 4
-  static constexpr int kAhead = 32768 / (2 * kTile * kRow) < 4 ? 32768 / (2 * kTile * kRow) : 4;
+  static constexpr int kTileBytes = 2 * kTile * kRow;                    // of k and v
+  // tiles a wave has in flight: 128 KiB a workgroup, at most 4
+  static constexpr int kAhead = 131072 / WAVES / kTileBytes < 4 ? 131072 / WAVES / kTileBytes : 4;
   static constexpr int kPitch = D + 4;                                   // floats between rows in LDS
 };
-static_assert(Shape<kE4M3, 128>::kAhead * 64 * 128 == 32768 && Shape<kE4M3, 64>::kAhead == 4, "see split_groups");
 
 constexpr int kStream = 2;                // cache policy of a buffer access: nontemporal
 
@@ -341,14 +363,14 @@ struct Pages {
   }
 };
 
-template <int FMT, int D>
-__global__ void __launch_bounds__(kThreads, 1) gdn_attn_k(AttnArgs p, SplitArgs sp) {
-  typedef Shape<FMT, D> S;
+template <int FMT, int D, int WAVES>
+__global__ void __launch_bounds__(64 * WAVES, 1) gdn_attn_k(AttnArgs p, SplitArgs sp) {
+  typedef Shape<FMT, D, WAVES> S;
   typedef typename std::conditional<FMT == kF32, float, _Float16>::type IO;
   constexpr int kAcc = S::kSets * S::kCols;                // 16 x 16 blocks of the output
   constexpr int U = S::kAhead;
-  __shared__ alignas(16) float sums[kWaves][kRows][S::kPitch];
-  __shared__ float stats[kWaves][kRows][2];
+  __shared__ alignas(16) float sums[WAVES][kRows][S::kPitch];
+  __shared__ float stats[WAVES][kRows][2];
   __shared__ float joined[kRows][2];
 
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -369,13 +391,13 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_attn_k(AttnArgs p, SplitArgs 
   half8_t qh[FMT == kF32 ? 1 : D / 32];                    // q, the first product's second operand
   float4_t qf[FMT == kF32 ? D / 16 : 1];
 
-  // ---- tiles: this wave's are t0 + (wave + kWaves i) kTile; U of them are in flight, tile i in buffer i % U.
+  // ---- tiles: this wave's are t0 + (wave + WAVES i) kTile; U of them are in flight, tile i in buffer i % U.
   // A load past `end` or without a page has an empty range: it costs no traffic, and the number of
   // loads in flight stays the same, so that the wait for a tile waits for nothing younger.
   uint32_t kw[U][S::kBlocks][S::kKLoads][4], vw[U][S::kPos][S::kSets][S::kVWords];
   uint32_t kscale[U][S::kBlocks], vscale[U][S::kBlocks];  // exponent bytes of this lane's positions
   int entry[U][S::kBlocks], held[U][S::kBlocks];          // table entries of the next tile, pages of this one
-  constexpr int kStep = kWaves * S::kTile;
+  constexpr int kStep = WAVES * S::kTile;
   auto look_up = [&](int u, int t) {
 #pragma unroll
     for (int a = 0; a < S::kBlocks; ++a) entry[u][a] = pages.entry(t + 16 * a);
@@ -653,12 +675,12 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_attn_k(AttnArgs p, SplitArgs 
     __syncthreads();
     float top = stats[0][n][0];
 #pragma unroll
-    for (int w = 1; w < kWaves; ++w) top = fmaxf(top, stats[w][n][0]);
+    for (int w = 1; w < WAVES; ++w) top = fmaxf(top, stats[w][n][0]);
     const float f = M == -INFINITY ? 0.f : exp2_fast(M - top);
     if (tid < kRows) {
       float total = 0.f;
 #pragma unroll
-      for (int w = 0; w < kWaves; ++w)
+      for (int w = 0; w < WAVES; ++w)
         total += stats[w][n][0] == -INFINITY ? 0.f : stats[w][n][1] * exp2_fast(stats[w][n][0] - top);
       joined[n][0] = top;
       joined[n][1] = total;
@@ -676,11 +698,11 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_attn_k(AttnArgs p, SplitArgs 
                          acc[S::kCols * c + e + 2][i] * f, acc[S::kCols * c + e + 3][i] * f};
     }
     __syncthreads();
-    for (int i = tid; i < rows * (D / 4); i += kThreads) {
+    for (int i = tid; i < rows * (D / 4); i += 64 * WAVES) {
       const int rr = i / (D / 4), d = 4 * (i - rr * (D / 4));
       float4_t o = *reinterpret_cast<const float4_t*>(&sums[0][rr][d]);
 #pragma unroll
-      for (int w = 1; w < kWaves; ++w) o += *reinterpret_cast<const float4_t*>(&sums[w][rr][d]);
+      for (int w = 1; w < WAVES; ++w) o += *reinterpret_cast<const float4_t*>(&sums[w][rr][d]);
       store_row<FMT, D>(p, sp, done, complete, rr, d, joined[rr][0], joined[rr][1], o);
     }
     if (!more) return;
@@ -1239,14 +1261,22 @@ __global__ void __launch_bounds__(kThreads) gdn_attn_join_k(AttnArgs p, SplitArg
         half4_t{(_Float16)(o[0] * norm), (_Float16)(o[1] * norm), (_Float16)(o[2] * norm), (_Float16)(o[3] * norm)};
 }
 
+// Waves of gdn_attn_k's workgroups in a launch of at most one a CU: 8 where a wave's 16 KiB
+// in flight are two to four tiles or one, and not (a wave of) more.
+template <int FMT, int D>
+constexpr int many_waves() {
+  typedef Shape<FMT, D, 8> S;
+  return S::kAhead > 0 && 8 * S::kAhead * S::kTileBytes == 131072 && S::kTileBytes > 4096 ? 8 : 4;
+}
+
 // Workgroups of a split launch: one per CU keeps the waves' shares equal in time (of two
 // on a CU the older one's loads go first: 64 requests of 8,192 positions, D = 128, the
 // first 256 workgroups were done after 230 us and the others after 313), two where a
 // wave's tiles in flight are small (8-bit heads of 64: 222 -> 195 us).
 template <int FMT, int D>
 constexpr int split_groups() {
-  typedef Shape<FMT, D> S;
-  return S::kAhead * 2 * S::kTile * S::kRow < 32768 ? 2 * kGroups : kGroups;
+  typedef Shape<FMT, D, 4> S;
+  return 4 * S::kAhead * S::kTileBytes < 131072 ? 2 * kGroups : kGroups;
 }
 constexpr int kMostGroups = 2 * kGroups;
 
@@ -1279,9 +1309,9 @@ hipError_t launch_attn_d(const AttnArgs& p, void* workspace, hipStream_t stream)
   const int64_t most = (int64_t)p.max_tokens * p.group;    // rows of a request and key head
   const bool few = most <= kRows;
   sp.seg_rows = few ? kRows : kTiles * kRows;
-  const int64_t segments = ((int64_t)p.rows.N * p.group / sp.seg_rows + p.rows.R) * p.cache.Hk;
+  const int64_t segments = ((few ? 0 : (int64_t)p.rows.N * p.group / sp.seg_rows) + p.rows.R) * p.cache.Hk;
   int64_t groups = segments < kWholeGroups ? segments : kWholeGroups;
-  const bool whole = one_group_each(p.max_len, p.sum_len, p.cache.Hk, 2 * Shape<FMT, D>::kRow);
+  const bool whole = one_group_each(p.max_len, p.sum_len, p.cache.Hk, 2 * Shape<FMT, D, 4>::kRow);
   int64_t notes = 0;
   if (whole) {
     sp.chunk_shift = kWholeShift;
@@ -1298,8 +1328,11 @@ hipError_t launch_attn_d(const AttnArgs& p, void* workspace, hipStream_t stream)
     notes = segs * p.rows.R * p.cache.Hk;
     if (notes <= groups) sp.max_segs = (int)segs; else notes = groups;
   }
-  if (few)
-    hipLaunchKernelGGL((gdn_attn_k<FMT, D>), dim3((unsigned)groups), dim3(kThreads), 0, stream, p, sp);
+  if (few && groups <= kGroups)
+    hipLaunchKernelGGL((gdn_attn_k<FMT, D, many_waves<FMT, D>()>), dim3((unsigned)groups), dim3(64 * many_waves<FMT, D>()), 0,
+                       stream, p, sp);
+  else if (few)
+    hipLaunchKernelGGL((gdn_attn_k<FMT, D, 4>), dim3((unsigned)groups), dim3(256), 0, stream, p, sp);
   else
     hipLaunchKernelGGL((gdn_attn_rows_k<FMT, D>), dim3((unsigned)groups), dim3(kRingBlock), 0, stream, p, sp);
   if (!whole) {
