@@ -363,15 +363,16 @@ struct Pages {
   }
 };
 
-template <int FMT, int D, int WAVES>
+template <int FMT, int D, int WAVES, int TILES>
 __global__ void __launch_bounds__(64 * WAVES, 1) gdn_attn_k(AttnArgs p, SplitArgs sp) {
   typedef Shape<FMT, D, WAVES> S;
   typedef typename std::conditional<FMT == kF32, float, _Float16>::type IO;
-  constexpr int kAcc = S::kSets * S::kCols;                // 16 x 16 blocks of the output
+  constexpr int kAcc = S::kSets * S::kCols;                // 16 x 16 blocks of a row tile's output
+  constexpr int kMost = TILES * kRows;                     // rows of a segment
   constexpr int U = S::kAhead;
-  __shared__ alignas(16) float sums[WAVES][kRows][S::kPitch];
-  __shared__ float stats[WAVES][kRows][2];
-  __shared__ float joined[kRows][2];
+  __shared__ alignas(16) float sums[WAVES][kMost][S::kPitch];
+  __shared__ float stats[WAVES][kMost][2];
+  __shared__ float joined[kMost][2];
 
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int n = lane & 15, g = lane >> 4;
@@ -385,11 +386,11 @@ __global__ void __launch_bounds__(64 * WAVES, 1) gdn_attn_k(AttnArgs p, SplitArg
 
   if (sh.u >= sh.u_end) return;
   Segment sg;
-  Rows rw;
+  Rows rw[TILES];                                          // of row 16 i + n
   Pages pages(p);
   int t = 0;
-  half8_t qh[FMT == kF32 ? 1 : D / 32];                    // q, the first product's second operand
-  float4_t qf[FMT == kF32 ? D / 16 : 1];
+  half8_t qh[TILES][FMT == kF32 ? 1 : D / 32];             // q, the first product's second operand
+  float4_t qf[TILES][FMT == kF32 ? D / 16 : 1];
 
   // ---- tiles: this wave's are t0 + (wave + WAVES i) kTile; U of them are in flight, tile i in buffer i % U.
   // A load past `end` or without a page has an empty range: it costs no traffic, and the number of
@@ -440,17 +441,20 @@ __global__ void __launch_bounds__(64 * WAVES, 1) gdn_attn_k(AttnArgs p, SplitArg
     t = sg.t0 + wave * S::kTile;
 #pragma unroll
     for (int u = 0; u < U; ++u) look_up(u, t + u * kStep);
-    rw = rows_of(p, sg.s, sg.seg_row, sg.rows, n);
-    const IO* q = qs + (int64_t)(sg.s.start + rw.j) * p.q_stride + (int64_t)(sg.h * p.group + rw.head) * D;
-    // in the order k is loaded in
-    if constexpr (FMT == kF32) {
 #pragma unroll
-      for (int c = 0; c < D / 16; ++c) qf[c] = *reinterpret_cast<const float4_t*>(q + 16 * c + 4 * g);
-    } else {
+    for (int i = 0; i < TILES; ++i) {
+      rw[i] = rows_of(p, sg.s, sg.seg_row, sg.rows, 16 * i + n);
+      const IO* q = qs + (int64_t)(sg.s.start + rw[i].j) * p.q_stride + (int64_t)(sg.h * p.group + rw[i].head) * D;
+      // in the order k is loaded in
+      if constexpr (FMT == kF32) {
 #pragma unroll
-      for (int c = 0; c < D / 32; ++c)
-        qh[c] = *reinterpret_cast<const half8_t*>(
-            q + (FMT == kF16 ? 32 * c + 8 * g : 64 * (c >> 1) + 16 * g + 8 * (c & 1)));
+        for (int c = 0; c < D / 16; ++c) qf[i][c] = *reinterpret_cast<const float4_t*>(q + 16 * c + 4 * g);
+      } else {
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c)
+          qh[i][c] = *reinterpret_cast<const half8_t*>(
+              q + (FMT == kF16 ? 32 * c + 8 * g : 64 * (c >> 1) + 16 * g + 8 * (c & 1)));
+      }
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -466,38 +470,54 @@ __global__ void __launch_bounds__(64 * WAVES, 1) gdn_attn_k(AttnArgs p, SplitArg
 
   begin();
   for (;;) {
-    const int lo = rw.lo, hi = rw.hi, end = sg.end;
-    float4_t acc[kAcc];
+    const int end = sg.end;
+    int lo[TILES], hi[TILES];
+    float4_t acc[TILES][kAcc];
+    float M[TILES], l[TILES];                              // l: this lane's positions only
 #pragma unroll
-    for (int i = 0; i < kAcc; ++i) acc[i] = float4_t{0.f, 0.f, 0.f, 0.f};
-    float M = -INFINITY, l = 0.f;                          // l: this lane's positions only
+    for (int i = 0; i < TILES; ++i) {
+      lo[i] = rw[i].lo;
+      hi[i] = rw[i].hi;
+      M[i] = -INFINITY;
+      l[i] = 0.f;
+#pragma unroll
+      for (int k = 0; k < kAcc; ++k) acc[i][k] = float4_t{0.f, 0.f, 0.f, 0.f};
+    }
 
     while (t < end) {
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const bool some = t < end;
         // ---- scores: block a of lane group g holds positions t + 16 a + 4 g + (0 .. 3)
-        float4_t x[S::kBlocks];
+        float4_t x[TILES][S::kBlocks];
         if (some) {
 #pragma unroll
           for (int a = 0; a < S::kBlocks; ++a) {
-            x[a] = float4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int r = 0; r < TILES; ++r) x[r][a] = float4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int c = 0; c < S::kKLoads; ++c) {
               const uint32_t(&w)[4] = kw[u][a][c];
               if constexpr (FMT == kF32) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                  x[a] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(w[e]), qf[c][e], x[a], 0, 0, 0);
+#pragma unroll
+                  for (int r = 0; r < TILES; ++r)
+                    x[r][a] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(w[e]), qf[r][c][e], x[r][a], 0, 0, 0);
               } else if constexpr (FMT == kF16) {
-                x[a] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8_t, uint4_t{w[0], w[1], w[2], w[3]}),
-                                                              qh[c], x[a], 0, 0, 0);
+#pragma unroll
+                for (int r = 0; r < TILES; ++r)
+                  x[r][a] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
+                      __builtin_bit_cast(half8_t, uint4_t{w[0], w[1], w[2], w[3]}), qh[r][c], x[r][a], 0, 0, 0);
               } else {
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                   const uint4_t v = uint4_t{codes_to_half2<false>(w[2 * e]), codes_to_half2<true>(w[2 * e]),
                                             codes_to_half2<false>(w[2 * e + 1]), codes_to_half2<true>(w[2 * e + 1])};
-                  x[a] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8_t, v), qh[2 * c + e], x[a], 0, 0, 0);
+#pragma unroll
+                  for (int r = 0; r < TILES; ++r)
+                    x[r][a] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8_t, v), qh[r][2 * c + e], x[r][a],
+                                                                     0, 0, 0);
                 }
               }
             }
@@ -520,21 +540,24 @@ __global__ void __launch_bounds__(64 * WAVES, 1) gdn_attn_k(AttnArgs p, SplitArg
           // to base-2 exponents. With 8-bit values the weight carries the value's scale, so xs is the
           // exponent of the product and `inv` takes the scale out of the weights' sum again; a zero row's
           // scale counts as 2^-33, below that of every other fp16 row.
-          float xs[S::kPos], inv[S::kPos];
+          float xs[TILES][S::kPos], inv[S::kPos];
 #pragma unroll
           for (int i = 0; i < S::kPos; ++i) {
             if constexpr (FMT == kE4M3) {
               const uint32_t kb = (ks[i >> 2] >> (8 * (i & 3))) & 255u;
               const uint32_t vb = max((vscale[u][i >> 2] >> (8 * (i & 3))) & 255u, 94u);
-              xs[i] = fmaf(x[i >> 2][i & 3], to_log2 * __uint_as_float(kb << 23), (float)((int)vb - 127));
+#pragma unroll
+              for (int r = 0; r < TILES; ++r)
+                xs[r][i] = fmaf(x[r][i >> 2][i & 3], to_log2 * __uint_as_float(kb << 23), (float)((int)vb - 127));
               inv[i] = __uint_as_float((254u - min(vb, 253u)) << 23);
             } else {
-              xs[i] = x[i >> 2][i & 3] * to_log2;
+#pragma unroll
+              for (int r = 0; r < TILES; ++r) xs[r][i] = x[r][i >> 2][i & 3] * to_log2;
             }
           }
 
           // ---- masks, where some row does not attend all of the tile, or part of it has no page
-          bool whole = t >= rw.lo_max && t + S::kTile <= rw.hi_min && t + S::kTile <= end;
+          bool whole = t >= rw[0].lo_max && t + S::kTile <= rw[0].hi_min && t + S::kTile <= end;
 #pragma unroll
           for (int a = 0; a < S::kBlocks; ++a) whole = whole && page[a] >= 0;
           bool mixed = false;                              // a non-finite value that only some rows attend
@@ -543,10 +566,12 @@ __global__ void __launch_bounds__(64 * WAVES, 1) gdn_attn_k(AttnArgs p, SplitArg
             for (int i = 0; i < S::kPos; ++i) {
               const int pos = t + 16 * (i >> 2) + 4 * g + (i & 3);
               const bool there = page[i >> 2] >= 0 && pos < end;
-              if (!(there && pos >= lo && pos < hi)) xs[i] = -INFINITY;
+#pragma unroll
+              for (int r = 0; r < TILES; ++r)
+                if (!(there && pos >= lo[r] && pos < hi[r])) xs[r][i] = -INFINITY;
               // a value that not every row attends may have to count for some: 0 times it has to be 0
               // for the others, whatever it is
-              if (!(there && pos >= rw.lo_max && pos < rw.hi_min)) {
+              if (!(there && pos >= rw[0].lo_max && pos < rw[0].hi_min)) {
 #pragma unroll
                 for (int c = 0; c < S::kSets; ++c)
 #pragma unroll
@@ -561,26 +586,29 @@ __global__ void __launch_bounds__(64 * WAVES, 1) gdn_attn_k(AttnArgs p, SplitArg
           }
 
           // ---- weights
-          float m = xs[0];
+          float wgt[TILES][S::kPos];
 #pragma unroll
-          for (int i = 1; i < S::kPos; ++i) m = fmaxf(m, xs[i]);
-          m = fmaxf(row_max(m), M);
-          if (__any(m > M)) {
-            const float f = M == m ? 1.f : exp2_fast(M - m);   // -inf - -inf is not asked for
-            l *= f;
+          for (int r = 0; r < TILES; ++r) {
+            float m = xs[r][0];
 #pragma unroll
-            for (int i = 0; i < kAcc; ++i) acc[i] *= f;
-            M = m;
-          }
-          const float ref = M == -INFINITY ? 0.f : M;
-          float wgt[S::kPos];
+            for (int i = 1; i < S::kPos; ++i) m = fmaxf(m, xs[r][i]);
+            m = fmaxf(row_max(m), M[r]);
+            if (__any(m > M[r])) {
+              const float f = M[r] == m ? 1.f : exp2_fast(M[r] - m);   // -inf - -inf is not asked for
+              l[r] *= f;
 #pragma unroll
-          for (int i = 0; i < S::kPos; ++i) {
-            wgt[i] = exp2_fast(xs[i] - ref);
-            if constexpr (FMT == kE4M3)
-              l = fmaf(wgt[i], inv[i], l);
-            else
-              l += wgt[i];
+              for (int i = 0; i < kAcc; ++i) acc[r][i] *= f;
+              M[r] = m;
+            }
+            const float ref = M[r] == -INFINITY ? 0.f : M[r];
+#pragma unroll
+            for (int i = 0; i < S::kPos; ++i) {
+              wgt[r][i] = exp2_fast(xs[r][i] - ref);
+              if constexpr (FMT == kE4M3)
+                l[r] = fmaf(wgt[r][i], inv[i], l[r]);
+              else
+                l[r] += wgt[r][i];
+            }
           }
 
           // ---- O^T += V^T P^T. A lane holds the same few columns of its 4 or 8 positions and turns them into
@@ -592,11 +620,16 @@ __global__ void __launch_bounds__(64 * WAVES, 1) gdn_attn_k(AttnArgs p, SplitArg
               for (int e = 0; e < 4; ++e)
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                  acc[4 * c + e] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(vw[u][i][c][e]), wgt[i], acc[4 * c + e], 0, 0, 0);
-          } else {
-            half8_t pw;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) pw[i] = (_Float16)wgt[i];
+                  for (int r = 0; r < TILES; ++r)
+                    acc[r][4 * c + e] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(vw[u][i][c][e]), wgt[r][i],
+                                                                             acc[r][4 * c + e], 0, 0, 0);
+          } else {
+            half8_t pw[TILES];
+#pragma unroll
+            for (int r = 0; r < TILES; ++r)
+#pragma unroll
+              for (int i = 0; i < 8; ++i) pw[r][i] = (_Float16)wgt[r][i];
 #pragma unroll
             for (int c = 0; c < S::kSets; ++c)
 #pragma unroll
@@ -616,8 +649,11 @@ __global__ void __launch_bounds__(64 * WAVES, 1) gdn_attn_k(AttnArgs p, SplitArg
                   a1[i] = __builtin_amdgcn_perm(pair[2 * i + 1], pair[2 * i], 0x07060302u);
                 }
                 const int o = S::kCols * c + 2 * k;
-                acc[o] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8_t, a0), pw, acc[o], 0, 0, 0);
-                acc[o + 1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8_t, a1), pw, acc[o + 1], 0, 0, 0);
+#pragma unroll
+                for (int r = 0; r < TILES; ++r) {
+                  acc[r][o] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8_t, a0), pw[r], acc[r][o], 0, 0, 0);
+                  acc[r][o + 1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8_t, a1), pw[r], acc[r][o + 1], 0, 0, 0);
+                }
               }
           }
           if (mixed) {
@@ -627,11 +663,16 @@ __global__ void __launch_bounds__(64 * WAVES, 1) gdn_attn_k(AttnArgs p, SplitArg
             for (int at = 0; at < S::kTile; ++at) {
               const int pos = t + at, pg = pages.page(pages.entry(pos & ~15), pos & ~15);
               if (pg < 0 || pos >= end) continue;
-              float own = wgt[0];
+              float w[TILES];
+              bool sees[TILES];
 #pragma unroll
-              for (int i = 1; i < S::kPos; ++i) own = 4 * (at >> 4) + (at & 3) == i ? wgt[i] : own;
-              const float w = __shfl(own, n + 16 * ((at >> 2) & 3));
-              const bool sees = pos >= lo && pos < hi && !(pos >= rw.lo_max && pos < rw.hi_min);
+              for (int r = 0; r < TILES; ++r) {
+                float own = wgt[r][0];
+#pragma unroll
+                for (int i = 1; i < S::kPos; ++i) own = 4 * (at >> 4) + (at & 3) == i ? wgt[r][i] : own;
+                w[r] = __shfl(own, n + 16 * ((at >> 2) & 3));
+                sees[r] = pos >= lo[r] && pos < hi[r] && !(pos >= rw[0].lo_max && pos < rw[0].hi_min);
+              }
               const rsrc_t rs = make_rsrc(static_cast<const char*>(p.cache.v) + pages.row(pg, pos) * S::kRow, S::kRow);
 #pragma unroll
               for (int c = 0; c < S::kSets; ++c)
@@ -643,7 +684,10 @@ __global__ void __launch_bounds__(64 * WAVES, 1) gdn_attn_k(AttnArgs p, SplitArg
 #pragma unroll
                   for (int e = 0; e < S::kCols; ++e) {
                     const float v = element<FMT>(words, e);
-                    if (sees && !(fabsf(v) < INFINITY)) acc[S::kCols * c + e][i] = fmaf(w, v, acc[S::kCols * c + e][i]);
+#pragma unroll
+                    for (int r = 0; r < TILES; ++r)
+                      if (sees[r] && !(fabsf(v) < INFINITY))
+                        acc[r][S::kCols * c + e][i] = fmaf(w[r], v, acc[r][S::kCols * c + e][i]);
                   }
                 }
             }
@@ -664,38 +708,45 @@ __global__ void __launch_bounds__(64 * WAVES, 1) gdn_attn_k(AttnArgs p, SplitArg
     if (tid == 0 && sp.notes != nullptr && done.c0 == 0 && (sp.max_segs > 0 || !complete)) note_segment(sp, done, sh.size);
 
     // ---- join the waves
-    l = row_sum(l);
-    if (l != l) M = INFINITY;                              // a NaN score is no maximum, but has to show
     if (again) __syncthreads();                            // the last segment's sums have been read
     again = true;
-    if (g == 0) {
-      stats[wave][n][0] = M;
-      stats[wave][n][1] = l;
+#pragma unroll
+    for (int r = 0; r < TILES; ++r) {
+      l[r] = row_sum(l[r]);
+      if (l[r] != l[r]) M[r] = INFINITY;                   // a NaN score is no maximum, but has to show
+      if (g == 0) {
+        stats[wave][16 * r + n][0] = M[r];
+        stats[wave][16 * r + n][1] = l[r];
+      }
     }
     __syncthreads();
-    float top = stats[0][n][0];
 #pragma unroll
-    for (int w = 1; w < WAVES; ++w) top = fmaxf(top, stats[w][n][0]);
-    const float f = M == -INFINITY ? 0.f : exp2_fast(M - top);
-    if (tid < kRows) {
-      float total = 0.f;
+    for (int r = 0; r < TILES; ++r) {
+      const int rn = 16 * r + n;
+      float top = stats[0][rn][0];
 #pragma unroll
-      for (int w = 0; w < WAVES; ++w)
-        total += stats[w][n][0] == -INFINITY ? 0.f : stats[w][n][1] * exp2_fast(stats[w][n][0] - top);
-      joined[n][0] = top;
-      joined[n][1] = total;
-    }
-    // acc[cols c + e] of row n, register i: column 16 cols c + cols (4 g + i) + e
-    if (n < rows) {
+      for (int w = 1; w < WAVES; ++w) top = fmaxf(top, stats[w][rn][0]);
+      const float f = M[r] == -INFINITY ? 0.f : exp2_fast(M[r] - top);
+      if (tid < kRows) {
+        float total = 0.f;
 #pragma unroll
-      for (int c = 0; c < S::kSets; ++c)
+        for (int w = 0; w < WAVES; ++w)
+          total += stats[w][rn][0] == -INFINITY ? 0.f : stats[w][rn][1] * exp2_fast(stats[w][rn][0] - top);
+        joined[rn][0] = top;
+        joined[rn][1] = total;
+      }
+      // acc[cols c + e] of row n, register i: column 16 cols c + cols (4 g + i) + e
+      if (rn < rows) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int c = 0; c < S::kSets; ++c)
 #pragma unroll
-          for (int e = 0; e < S::kCols; e += 4)
-            *reinterpret_cast<float4_t*>(&sums[wave][n][16 * S::kCols * c + S::kCols * (4 * g + i) + e]) =
-                float4_t{acc[S::kCols * c + e][i] * f, acc[S::kCols * c + e + 1][i] * f,
-                         acc[S::kCols * c + e + 2][i] * f, acc[S::kCols * c + e + 3][i] * f};
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int e = 0; e < S::kCols; e += 4)
+              *reinterpret_cast<float4_t*>(&sums[wave][rn][16 * S::kCols * c + S::kCols * (4 * g + i) + e]) =
+                  float4_t{acc[r][S::kCols * c + e][i] * f, acc[r][S::kCols * c + e + 1][i] * f,
+                           acc[r][S::kCols * c + e + 2][i] * f, acc[r][S::kCols * c + e + 3][i] * f};
+      }
     }
     __syncthreads();
     for (int i = tid; i < rows * (D / 4); i += 64 * WAVES) {
@@ -1263,10 +1314,11 @@ __global__ void __launch_bounds__(kThreads) gdn_attn_join_k(AttnArgs p, SplitArg
 
 // Waves of gdn_attn_k's workgroups in a launch of at most one a CU: 8 where a wave's 16 KiB
 // in flight are two to four tiles or one, and not (a wave of) more.
-template <int FMT, int D>
+template <int FMT, int D, int TILES>
 constexpr int many_waves() {
   typedef Shape<FMT, D, 8> S;
-  return S::kAhead > 0 && 8 * S::kAhead * S::kTileBytes == 131072 && S::kTileBytes > 4096 ? 8 : 4;
+  const bool fits = TILES == 1 || (FMT != kE4M3 && S::kRow <= 256);
+  return fits && S::kAhead > 0 && 8 * S::kAhead * S::kTileBytes == 131072 && S::kTileBytes > 4096 ? 8 : 4;
 }
 
 // Workgroups of a split launch: one per CU keeps the waves' shares equal in time (of two
@@ -1303,12 +1355,21 @@ bool one_group_each(int64_t longest, int64_t sum, int heads, int64_t position_by
 }
 constexpr int64_t kWholeGroups = 4096;
 
+template <int FMT, int D, int TILES>
+void launch_few(const AttnArgs& p, const SplitArgs& sp, int groups, hipStream_t stream) {
+  constexpr int kMany = many_waves<FMT, D, TILES>();
+  if (groups <= kGroups)
+    hipLaunchKernelGGL((gdn_attn_k<FMT, D, kMany, TILES>), dim3((unsigned)groups), dim3(64 * kMany), 0, stream, p, sp);
+  else
+    hipLaunchKernelGGL((gdn_attn_k<FMT, D, 4, TILES>), dim3((unsigned)groups), dim3(256), 0, stream, p, sp);
+}
+
 template <int FMT, int D>
 hipError_t launch_attn_d(const AttnArgs& p, void* workspace, hipStream_t stream) {
   SplitArgs sp{};
   const int64_t most = (int64_t)p.max_tokens * p.group;    // rows of a request and key head
-  const bool few = most <= kRows;
-  sp.seg_rows = few ? kRows : kTiles * kRows;
+  const bool few = most <= 2 * kRows;
+  sp.seg_rows = most <= kRows ? kRows : few ? 2 * kRows : kTiles * kRows;
   const int64_t segments = ((few ? 0 : (int64_t)p.rows.N * p.group / sp.seg_rows) + p.rows.R) * p.cache.Hk;
   int64_t groups = segments < kWholeGroups ? segments : kWholeGroups;
   const bool whole = one_group_each(p.max_len, p.sum_len, p.cache.Hk, 2 * Shape<FMT, D, 4>::kRow);
@@ -1319,7 +1380,7 @@ hipError_t launch_attn_d(const AttnArgs& p, void* workspace, hipStream_t stream)
     groups = few ? split_groups<FMT, D>() : kGroups;
     sp.notes = static_cast<int4*>(workspace);
     sp.parts = reinterpret_cast<float*>(static_cast<char*>(workspace) + kNoteBytes);
-    sp.part_rows = few ? kRows : part_rows(p.rows.N, p.group);
+    sp.part_rows = few ? sp.seg_rows : part_rows(p.rows.N, p.group);
     sp.chunk_shift = kChunkShift;
     const int64_t cap = (int64_t)p.cache.max_pages << p.cache.page_shift;
     while (segments * ((cap >> sp.chunk_shift) + 1) > ((int64_t)1 << 30)) ++sp.chunk_shift;
@@ -1328,11 +1389,10 @@ hipError_t launch_attn_d(const AttnArgs& p, void* workspace, hipStream_t stream)
     notes = segs * p.rows.R * p.cache.Hk;
     if (notes <= groups) sp.max_segs = (int)segs; else notes = groups;
   }
-  if (few && groups <= kGroups)
-    hipLaunchKernelGGL((gdn_attn_k<FMT, D, many_waves<FMT, D>()>), dim3((unsigned)groups), dim3(64 * many_waves<FMT, D>()), 0,
-                       stream, p, sp);
+  if (most <= kRows)
+    launch_few<FMT, D, 1>(p, sp, (int)groups, stream);
   else if (few)
-    hipLaunchKernelGGL((gdn_attn_k<FMT, D, 4>), dim3((unsigned)groups), dim3(256), 0, stream, p, sp);
+    launch_few<FMT, D, 2>(p, sp, (int)groups, stream);
   else
     hipLaunchKernelGGL((gdn_attn_rows_k<FMT, D>), dim3((unsigned)groups), dim3(kRingBlock), 0, stream, p, sp);
   if (!whole) {
