@@ -12,23 +12,20 @@
 // are the N side of both products, S^T = K Q^T and O^T = V^T P^T: a row's scores
 // lie in 4 lanes (l & 15 = row), its weights leave the first product in the order
 // the second one takes them in, and the running M, l and the rescaling factor are
-// one register each. Two kernels differ in how keys and values reach the registers:
+// one register each. Keys and values go straight from memory to registers, with no LDS
+// and no barrier in the loop. A wave's tile is 32 positions (16 for fp32), the waves of
+// a workgroup take alternate tiles, and each has 16 or 32 KiB of them in flight. Up to
+// two tiles of 16 rows share the loaded keys and values.
 //
-//  gdn_attn_k, for at most 16 rows a request and key head (decode): straight from
-//  memory, with no LDS and no barrier in the loop. A wave's tile is 32 positions
-//  (16 for fp32) and its 4 waves take alternate tiles. Each byte is used once and
-//  loaded past the caches' retention (nontemporal).
-//
-//  gdn_attn_rows_k, for up to 64 rows (drafts, prompts): through LDS, so that the
-//  8 computing waves, up to 4 tiles of 16 rows, share one copy. Two more waves do nothing but copy
-//  pages into a ring of 16 KiB stages, by buffer loads that write LDS directly; they
-//  need no registers for them and run ahead over the ring, and the loads' range check
-//  fills positions past the end and without a page with zeros. A counter of landed
-//  stages and one of finished stages per wave, both in LDS, hand the stages over,
-//  so the waves need not run in step.
+// What this replaced: 8 waves fed from an LDS ring by two loader waves were slower
+// wherever a segment has up to 32 rows (16 requests x 4 drafts x 6 heads a key head, up
+// to 8,192 positions of D = 256 fp16: 74 us against 60) and for more rows, as several
+// segments, in all but one case: 16 x 5 drafts x 8 heads over 4,096 positions, D = 256
+// fp16 66 against 69, 8 bits 67 against 47, D = 64 fp16 37 against 25, D = 128 fp32
+// 100 against 89 us.
 //
 // Work is split evenly over the workgroups whatever the lengths: the positions of
-// every segment (request, 16 or 64 rows, key head) in chunks of 128 are laid end to
+// every segment (request, 16 or 32 rows, key head) in chunks of 128 are laid end to
 // end, and workgroup b takes the b-th equal share of the chunks. A share that holds
 // all of a segment's chunks writes the output; the others leave (M, l, sum) in the
 // workspace and gdn_attn_join_k, a second launch, joins them. Every wave forms the
@@ -45,12 +42,10 @@ namespace gdn {
 namespace {
 
 constexpr int kThreads = 256;             // of gdn_attn_join_k
-constexpr int kRingWaves = 8;             // computing waves of gdn_attn_rows_k
-constexpr int kRingThreads = 64 * kRingWaves;
-constexpr int kRingBlock = kRingThreads + 128;   // with a loader wave each for k and v
 constexpr int kRows = 16;                 // rows of a tile: the N side of the MFMA
-constexpr int kTiles = 4;                 // tiles of a segment of gdn_attn_rows_k
+constexpr int kTiles = 2;                 // tiles of a segment, at most
 constexpr int kChunkShift = 7;            // positions of a unit of work: 128 or more
+constexpr int kMostLines = 8;
 constexpr int kWholeShift = 30;           // one unit per segment: nothing is split
 constexpr int kGroups = 256;              // workgroups of a split launch: one per CU
 
@@ -63,7 +58,8 @@ struct SplitArgs {
   int4* notes;                            // of the segments that may be split (see note_segment); null: none is
   float* parts;                           // [2 * groups][part_rows * (D + 2)]: M, l, sums
   int32_t part_rows;
-  int32_t seg_rows;                       // rows of a segment: 16 or 64
+  int32_t seg_rows;                       // rows of a segment: 16 or 32
+  int32_t line_shift, line_groups;        // log2 of the lines, workgroups of a line (see block_of)
   int32_t chunk_shift;
   int32_t max_segs;                       // > 0: notes by segment, this many of a request and key head; 0: by workgroup
 };
@@ -98,7 +94,9 @@ __device__ __forceinline__ Plan plan_of(const AttnArgs& p, const SplitArgs& sp, 
 }
 
 // The launch bounds the units of all requests by 2^30.
-__device__ __forceinline__ int units_of(const Plan& s, int Hk) { return s.segs * Hk * s.chunks; }
+__device__ __forceinline__ int units_of(const SplitArgs& sp, const Plan& s, int Hk) {
+  return (sp.line_shift > 0 ? 1 : s.segs) * Hk * s.chunks;
+}
 
 __device__ __forceinline__ int share_of(int total, int groups) {
   return max((int)((unsigned)(total + groups - 1) / (unsigned)groups), 1);
@@ -120,7 +118,24 @@ __device__ __forceinline__ int wave_scan(int x) {
 struct Share {
   int u, u_end, r, r_first, size;
   int start, T, len;                                       // of request `lane`, where there are at most 64
+  int id, at, line;                                        // see block_of
 };
+
+// Where requests have 2 to 8 segments each, the same positions' segments go to as many
+// workgroups (lines), which walk them at once and share an L2: workgroups are handed
+// to the 8 XCDs in turn, so the numbers of those of one position differ by 8. `at` is a
+// workgroup's place in its line, `id` its number line by line.
+__device__ __forceinline__ void block_of(const SplitArgs& sp, Share& w) {
+  const int b = (int)blockIdx.x;
+  w.id = w.at = b;
+  w.line = 0;
+  if (sp.line_shift > 0) {
+    const int slot = b >> 3;
+    w.line = slot & ((1 << sp.line_shift) - 1);
+    w.at = (slot >> sp.line_shift << 3) + (b & 7);
+    w.id = w.line * sp.line_groups + w.at;
+  }
+}
 
 __device__ __forceinline__ Share find_share(const AttnArgs& p, const SplitArgs& sp, int lane) {
   const int R = p.rows.R, per = (R + 63) >> 6;             // requests a lane sums
@@ -131,19 +146,20 @@ __device__ __forceinline__ Share find_share(const AttnArgs& p, const SplitArgs& 
   if (R <= 64) {
     if (r0 < r1) {
       const Plan s = plan_of(p, sp, r0);
-      mine = units_of(s, p.cache.Hk);
+      mine = units_of(sp, s, p.cache.Hk);
       w.start = s.start;
       w.T = s.T;
       w.len = (int)s.len;
     }
   } else {
 #pragma unroll 4
-    for (int r = r0; r < r1; ++r) mine += units_of(plan_of(p, sp, r), p.cache.Hk);
+    for (int r = r0; r < r1; ++r) mine += units_of(sp, plan_of(p, sp, r), p.cache.Hk);
   }
   const int after = wave_scan(mine), before = after - mine;
   const int total = __builtin_amdgcn_readlane(after, 63);
-  const int share = w.size = share_of(total, (int)gridDim.x);
-  w.u = (int)min((int64_t)blockIdx.x * share, (int64_t)total);
+  block_of(sp, w);
+  const int share = w.size = share_of(total, sp.line_groups);
+  w.u = (int)min((int64_t)w.at * share, (int64_t)total);
   w.u_end = min(w.u + share, total);
   w.r = w.r_first = 0;
   if (w.u >= w.u_end) return w;
@@ -164,7 +180,7 @@ struct Segment {
   Plan s;
   int h, seg_row, rows, c0, c1;
   int t0, end;                                             // positions [t0, end)
-  int note, last_unit;                                     // its place among the notes, its last unit
+  int id, note, last_unit;                                 // its workgroup, its place among the notes, its last unit
 };
 
 __device__ __forceinline__ Segment next_segment(const AttnArgs& p, const SplitArgs& sp, Share& w) {
@@ -176,21 +192,27 @@ __device__ __forceinline__ Segment next_segment(const AttnArgs& p, const SplitAr
                           : plan_of(p, sp, r);
   };
   x.s = plan_at(w.r);
-  while (w.u - w.r_first >= units_of(x.s, p.cache.Hk)) {   // requests without tokens have no units
-    w.r_first += units_of(x.s, p.cache.Hk);
+  while (w.u - w.r_first >= units_of(sp, x.s, p.cache.Hk)) {   // requests without tokens have no units
+    w.r_first += units_of(sp, x.s, p.cache.Hk);
     x.s = plan_at(++w.r);
   }
   const unsigned local = w.u - w.r_first, seg = local / (unsigned)x.s.chunks;
   x.c0 = local - seg * x.s.chunks;
   x.c1 = min(x.s.chunks, x.c0 + (w.u_end - w.u));
-  x.h = x.s.segs == 1 ? seg : seg / (unsigned)x.s.segs;
-  x.seg_row = (int)(seg - x.h * x.s.segs) * sp.seg_rows;
-  x.note = sp.max_segs > 0 ? (w.r * p.cache.Hk + x.h) * sp.max_segs + (int)(seg - x.h * x.s.segs) : (int)blockIdx.x;
+  int line = w.line;
+  x.h = seg;
+  if (sp.line_shift == 0 && x.s.segs > 1) {
+    x.h = seg / (unsigned)x.s.segs;
+    line = seg - x.h * x.s.segs;
+  }
+  x.seg_row = line * sp.seg_rows;
+  x.id = w.id;
+  x.note = sp.max_segs > 0 ? (w.r * p.cache.Hk + x.h) * sp.max_segs + line : w.id;
   x.last_unit = w.u - x.c0 + x.s.chunks - 1;
   w.u += x.c1 - x.c0;
-  x.rows = min(sp.seg_rows, x.s.T * p.group - x.seg_row);
+  x.rows = line < x.s.segs ? min(sp.seg_rows, x.s.T * p.group - x.seg_row) : 0;   // 0: fewer segments than lines
   const int cap = p.cache.max_pages << p.cache.page_shift;
-  const int64_t past_last = x.s.len - x.s.T + token_of(p, x.s, x.seg_row + x.rows - 1) + 1;
+  const int64_t past_last = x.rows == 0 ? 0 : x.s.len - x.s.T + token_of(p, x.s, x.seg_row + x.rows - 1) + 1;
   x.t0 = x.s.base + (int)((int64_t)x.c0 << sp.chunk_shift);
   x.end = (int)min((int64_t)x.s.base + ((int64_t)x.c1 << sp.chunk_shift), (int64_t)clamp_pos(past_last, cap));
   return x;
@@ -199,10 +221,10 @@ __device__ __forceinline__ Segment next_segment(const AttnArgs& p, const SplitAr
 // The workgroup that begins a segment notes what the join has to know of it: the
 // parts, the first of them, where the rows belong. In the order of workgroups there
 // is one note each, of the last segment that it begins and leaves to others.
-__device__ __forceinline__ void note_segment(const SplitArgs& sp, const Segment& x, int share) {
+__device__ __forceinline__ void note_segment(const SplitArgs& sp, const Segment& x, const Share& w) {
   // the shares from this one on that hold the segment
-  const int parts = x.c1 == x.s.chunks ? 0 : (int)((unsigned)x.last_unit / (unsigned)share) - (int)blockIdx.x + 1;
-  sp.notes[2 * x.note] = int4{parts, (int)blockIdx.x, x.rows, x.seg_row};
+  const int parts = x.c1 == x.s.chunks ? 0 : (int)((unsigned)x.last_unit / (unsigned)w.size) - w.at + 1;
+  sp.notes[2 * x.note] = int4{parts, w.id, x.rows, x.seg_row};
   sp.notes[2 * x.note + 1] = int4{x.s.start, x.h, 0, 0};
 }
 
@@ -217,7 +239,7 @@ struct Rows {
 __device__ __forceinline__ Rows rows_of(const AttnArgs& p, const Plan& s, int row0, int rows, int n) {
   Rows x;
   const int cap = p.cache.max_pages << p.cache.page_shift;
-  const int last = row0 + max(rows, 1) - 1, row = min(row0 + n, last);
+  const int last = row0 + max(rows, 1) - 1, row = min(row0 + n, min(last, s.T * p.group - 1));
   x.j = token_of(p, s, row);
   x.head = row - x.j * p.group;
   const int64_t before = s.len - s.T + 1;                  // one past the first token's newest position
@@ -287,7 +309,7 @@ __device__ __forceinline__ void store_row(const AttnArgs& p, const SplitArgs& sp
       *reinterpret_cast<half4_t*>(out) =
           half4_t{(_Float16)(o[0] * norm), (_Float16)(o[1] * norm), (_Float16)(o[2] * norm), (_Float16)(o[3] * norm)};
   } else {
-    float* part = sp.parts + (2 * (int64_t)blockIdx.x + (sg.c0 == 0 ? 1 : 0)) * (sp.part_rows * (D + 2));
+    float* part = sp.parts + (2 * (int64_t)sg.id + (sg.c0 == 0 ? 1 : 0)) * (sp.part_rows * (D + 2));
     *reinterpret_cast<float4_t*>(part + 2 * sp.part_rows + rr * D + d) = o;
     if (d == 0) {
       part[rr] = M;
@@ -379,7 +401,7 @@ __global__ void __launch_bounds__(64 * WAVES, 1) gdn_attn_k(AttnArgs p, SplitArg
   Share sh = find_share(p, sp, lane);
   const float to_log2 = p.scale * 1.4426950408889634f;
   const IO* __restrict__ qs = static_cast<const IO*>(p.q);
-  if (tid == 0 && sp.notes != nullptr && sp.max_segs == 0) sp.notes[2 * blockIdx.x] = int4{0, 0, 0, 0};
+  if (tid == 0 && sp.notes != nullptr && sp.max_segs == 0) sp.notes[2 * sh.id] = int4{0, 0, 0, 0};
   bool again = false;
   // byte offsets of this lane in a block: 16 bytes of k in row n; its columns of v in rows 4 g + (0 .. 3)
   const int k_at = n * S::kRow + 16 * g, v_at = 4 * g * S::kRow + S::kCols * S::kBytes * n;
@@ -705,7 +727,7 @@ __global__ void __launch_bounds__(64 * WAVES, 1) gdn_attn_k(AttnArgs p, SplitArg
     const bool complete = done.c0 == 0 && done.c1 == done.s.chunks;
     const bool more = sh.u < sh.u_end;
     if (more) begin();
-    if (tid == 0 && sp.notes != nullptr && done.c0 == 0 && (sp.max_segs > 0 || !complete)) note_segment(sp, done, sh.size);
+    if (tid == 0 && sp.notes != nullptr && rows > 0 && done.c0 == 0 && (sp.max_segs > 0 || !complete)) note_segment(sp, done, sh);
 
     // ---- join the waves
     if (again) __syncthreads();                            // the last segment's sums have been read
@@ -757,476 +779,6 @@ __global__ void __launch_bounds__(64 * WAVES, 1) gdn_attn_k(AttnArgs p, SplitArg
       store_row<FMT, D>(p, sp, done, complete, rr, d, joined[rr][0], joined[rr][1], o);
     }
     if (!more) return;
-  }
-}
-
-template <int FMT, int D>
-struct RingShape {
-  static constexpr int kBytes = FMT == kF32 ? 4 : FMT == kF16 ? 2 : 1;   // of a cache element
-  static constexpr int kRow = D * kBytes;                                // bytes of a position's k or v
-  static constexpr int kStage = kRow >= 512 ? 16 : 8192 / kRow;          // positions of a stage: 16 KiB of k and v
-  static constexpr int kStageBytes = 2 * kStage * kRow;                  // (32 KiB for fp32 at D = 256)
-  static constexpr int kBufs = 131072 / kStageBytes;
-  static constexpr int kTilesPerStage = kStage / 16;
-  static constexpr int kGroupLoads = 16 * kRow / 1024;                   // 1 KiB loads of 16 positions' k or v
-  static constexpr int kLoads = kTilesPerStage * kGroupLoads + (FMT == kE4M3 ? 1 : 0);       // a loader's, of a stage
-  static constexpr int kUnits = kRow / 16;                               // 16-byte units of a row
-  // columns of v a lane holds: sets of kCols neighbours, 16 * kCols apart
-  static constexpr int kCols = FMT == kF32 ? 4 : FMT == kF16 ? (D / 16 < 8 ? D / 16 : 8) : D / 16;
-  static constexpr int kSets = D / (16 * kCols);
-  static constexpr int kVWords = kCols * kBytes / 4;                     // dwords of a set in one position
-  // reads of this many 16-byte units are put in flight together where registers are scarce
-  static constexpr bool kFew = FMT == kF32 ? D >= 128 : D == 256;
-  static_assert(kLoads * (kBufs - 1) < 64, "vmcnt holds 6 bits");
-};
-
-// 16-byte unit u of row r (r = position mod 16) of a stage is stored at unit
-// u ^ swizzle(r): the 16 rows that a k fragment takes at one u, and the units of one
-// row that a v fragment takes, then fall in distinct banks.
-template <int UNITS>
-__device__ __forceinline__ int swizzle(int r) {
-  return UNITS >= 16 ? r : UNITS == 8 ? r >> 1 : r >> 2;
-}
-
-typedef __attribute__((address_space(3))) void lds_void_t;
-typedef __attribute__((address_space(1))) const void global_void_t;
-
-// The loader's view of the hand-over counters. In inline assembly, so that the
-// compiler does not make the loader wait for its direct loads (which write LDS too)
-// at every access.
-__device__ __forceinline__ void lds_store(uint32_t at, int x) {
-  asm volatile("ds_write_b32 %0, %1" ::"v"(at), "v"(x) : "memory");
-}
-__device__ __forceinline__ int lds_min8(uint32_t at) {
-  uint4_t x, y;
-  asm volatile("ds_read_b128 %0, %2\n\tds_read_b128 %1, %2 offset:16\n\ts_waitcnt lgkmcnt(0)"
-               : "=&v"(x), "=&v"(y) : "v"(at) : "memory");
-  const int a = min(min((int)x[0], (int)x[1]), min((int)x[2], (int)x[3]));
-  const int b = min(min((int)y[0], (int)y[1]), min((int)y[2], (int)y[3]));
-  return __builtin_amdgcn_readfirstlane(min(a, b));
-}
-__device__ __forceinline__ uint32_t lds_address(const void* p) {
-  return (uint32_t)(uintptr_t)(lds_void_t*)p;
-}
-
-// Waits until at most n stages of kLoads direct loads are in flight (n < kBufs).
-template <int LOADS, int N>
-__device__ __forceinline__ void wait_in_flight(int n) {
-  if constexpr (N == 0) {
-    __builtin_amdgcn_s_waitcnt((7 << 4) | (15 << 8));                     // vmcnt(0)
-  } else {
-    constexpr int k = LOADS * N;
-    if (n >= N)
-      __builtin_amdgcn_s_waitcnt((k & 15) | (7 << 4) | (15 << 8) | ((k >> 4) << 14));
-    else
-      wait_in_flight<LOADS, N - 1>(n);
-  }
-}
-
-// Copies the k or v rows of positions t .. t + kStage - 1 of one request and key head
-// into a stage, zeros from position `end` on and where there is no page.
-template <int FMT, int D>
-struct Loader {
-  typedef RingShape<FMT, D> S;
-  const AttnArgs& p;
-  const void* pool;                                                      // k or v pages
-  const uint8_t* pool_scales;
-  const __attribute__((address_space(4))) int32_t* table;                // read through the scalar cache
-  int h, end, lane;
-
-  // The pages of the positions from t on, 16 by 16; -1 where there is none. All entries are asked for
-  // before any is looked at, and a stage ahead: the scalar cache takes hundreds of cycles.
-  __device__ __forceinline__ void look_up(int t, int (&pages)[S::kTilesPerStage]) const {
-#pragma unroll
-    for (int q = 0; q < S::kTilesPerStage; ++q)
-      pages[q] = table[min((t + 16 * q) >> p.cache.page_shift, p.cache.max_pages - 1)];
-#pragma unroll
-    for (int q = 0; q < S::kTilesPerStage; ++q)
-      pages[q] = ((t + 16 * q) >> p.cache.page_shift) < p.cache.max_pages && pages[q] < p.cache.num_pages ? pages[q] : -1;
-  }
-  __device__ __forceinline__ int64_t first_row(int pg, int pos) const {
-    return (((int64_t)pg * p.cache.Hk + h) << p.cache.page_shift) + (pos & ((1 << p.cache.page_shift) - 1));
-  }
-
-  // Returns a bit per 16 positions that have a page.
-  __device__ __forceinline__ int issue(int t, const int (&pages)[S::kTilesPerStage], char* stage, uint8_t* scales) const {
-    constexpr int kRowsPerLoad = 1024 / S::kRow;
-    const int lrow = lane / S::kUnits, slot = lane % S::kUnits;
-    int held = 0;
-#pragma unroll
-    for (int q = 0; q < S::kTilesPerStage; ++q) held |= pages[q] >= 0 ? 1 << q : 0;
-#pragma unroll
-    for (int q = 0; q < S::kTilesPerStage; ++q) {
-      const int pos = t + 16 * q, pg = pages[q];
-      const int rows = __builtin_amdgcn_readfirstlane(pg >= 0 ? min(max(end - pos, 0), 16) : 0);
-      const int64_t at = first_row(max(pg, 0), pos) * S::kRow;
-      const rsrc_t rs = make_rsrc(static_cast<const char*>(pool) + at, rows * S::kRow);
-#pragma unroll
-      for (int i = 0; i < S::kGroupLoads; ++i) {
-        const int row = kRowsPerLoad * i + lrow;
-        const int off = lrow * S::kRow + 16 * (slot ^ swizzle<S::kUnits>(row));
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void_t*)(stage + 16 * q * S::kRow + 1024 * i), 16, off, 1024 * i,
-                                                 0, kStream);
-      }
-    }
-    if constexpr (FMT == kE4M3) {
-      // the exponent bytes, 4 positions a lane
-      if (lane < S::kStage / 4) {
-        int pg = pages[0];
-#pragma unroll
-        for (int q = 1; q < S::kTilesPerStage; ++q) pg = (lane >> 2) == q ? pages[q] : pg;
-        __builtin_amdgcn_global_load_lds((global_void_t*)(pool_scales + first_row(max(pg, 0), t + 4 * lane)),
-                                         (lds_void_t*)scales, 4, 0, 0);
-      }
-    }
-    return held;
-  }
-};
-
-template <int FMT, int D>
-__global__ void __launch_bounds__(kRingBlock, 3) gdn_attn_rows_k(AttnArgs p, SplitArgs sp) {
-  typedef RingShape<FMT, D> S;
-  typedef typename std::conditional<FMT == kF32, float, _Float16>::type IO;
-  constexpr int kAcc = S::kSets * S::kCols;                // 16 x 16 blocks of the output
-  __shared__ __attribute__((aligned(16))) char ring[S::kBufs][S::kStageBytes];
-  __shared__ __attribute__((aligned(16))) uint8_t scale_ring[FMT == kE4M3 ? S::kBufs : 1][FMT == kE4M3 ? 2 * S::kStage : 16];
-  __shared__ __attribute__((aligned(16))) int finished[kRingWaves];   // stages a wave is done with
-  __shared__ int landed[2];                                       // stages of k and of v in LDS
-  __shared__ int held[S::kBufs];                                  // a stage's 16-position groups that have a page
-  __shared__ float stats[kRingWaves][kRows][2];
-  __shared__ float joined[kTiles][kRows][2];
-  static_assert(sizeof(float) * kRingWaves * kRows * D <= sizeof(ring), "the waves' sums are joined in the ring");
-
-  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int n = lane & 15, g = lane >> 4;
-
-  Share w = find_share(p, sp, lane);
-  if (tid < kRingWaves) finished[tid] = 0;
-  if (tid < 2) landed[tid] = 0;
-  __syncthreads();
-  const float to_log2 = p.scale * 1.4426950408889634f;
-  int stage0 = 0;                                          // stages of the segments before this one
-  if (tid == 0 && sp.notes != nullptr && sp.max_segs == 0) sp.notes[2 * blockIdx.x] = int4{0, 0, 0, 0};
-
-  if (w.u >= w.u_end) return;
-  Segment sg = next_segment(p, sp, w);
-  for (;;) {
-    const bool more = w.u < w.u_end;
-    const Plan& s = sg.s;
-    const int h = sg.h, seg_row = sg.seg_row, seg_rows = sg.rows, t0 = sg.t0, end = sg.end;
-    const int stages = end > t0 ? (end - t0 + S::kStage - 1) / S::kStage : 0;
-    const bool complete = sg.c0 == 0 && sg.c1 == s.chunks;
-
-    if (wave >= kRingWaves) {
-      // ---- a loader: issue what the ring has room for, announce what has landed
-      const int side = wave - kRingWaves;                  // 0: k, 1: v
-      const Loader<FMT, D> load{p, side ? p.cache.v : p.cache.k, side ? p.cache.v_scales : p.cache.k_scales,
-                                (const __attribute__((address_space(4))) int32_t*)(p.cache.table + (int64_t)w.r * p.cache.max_pages),
-                                h, end, lane};
-      const uint32_t done_at = lds_address(finished), landed_at = lds_address(&landed[side]), held_at = lds_address(held);
-      int issued = 0, pages[S::kTilesPerStage];
-      load.look_up(t0, pages);
-      for (int i = 0; i < stages;) {
-        while (issued < stages) {
-          if (stage0 + issued - lds_min8(done_at) < S::kBufs) {
-            const int b = (stage0 + issued) % S::kBufs;
-            const int bits = load.issue(t0 + issued * S::kStage, pages, ring[b] + side * (S::kStageBytes / 2),
-                                        scale_ring[FMT == kE4M3 ? b : 0] + (FMT == kE4M3 ? side * S::kStage : 0));
-            if (side == 0) lds_store(held_at + 4 * b, bits);
-            ++issued;
-            load.look_up(t0 + issued * S::kStage, pages);
-          } else if (issued > i) {
-            break;
-          } else {
-            __builtin_amdgcn_s_sleep(1);
-          }
-        }
-        wait_in_flight<S::kLoads, S::kBufs - 1>(issued - 1 - i);
-        lds_store(landed_at, stage0 + ++i);
-      }
-      stage0 += stages;
-      if (more) sg = next_segment(p, sp, w);
-      __syncthreads();                                     // A
-      __syncthreads();                                     // B
-      __syncthreads();                                     // C
-      if (!more) return;
-      continue;
-    }
-
-    // ---- the wave's tile and stream of positions, this lane's row, and what the tile's rows attend
-    // the streams of a tile hold at most half of the ring's stages at a time
-    constexpr int kMost = S::kBufs / 2 * S::kTilesPerStage;
-    const int streams = min(seg_rows <= kRows ? kRingWaves : seg_rows <= 2 * kRows ? kRingWaves / 2 : kRingWaves / 4, kMost);
-    const int sub = wave / streams, stream = wave - sub * streams;
-    const int rows = max(min(kRows, seg_rows - sub * kRows), 0);       // 0: a wave without a tile
-    const int row0 = seg_row + (rows > 0 ? sub * kRows : 0);
-    const Rows rw = rows_of(p, s, row0, rows, n);
-    const int lo = rw.lo, hi = rw.hi, lo_max = rw.lo_max, hi_min = rw.hi_min;
-
-    // q as the first product's second operand, in the order k is read in
-    const IO* q = static_cast<const IO*>(p.q) + (int64_t)(s.start + rw.j) * p.q_stride +
-                  (int64_t)(h * p.group + rw.head) * D;
-    half8_t qh[FMT == kF32 ? 1 : D / 32];
-    float4_t qf[FMT == kF32 ? D / 16 : 1];
-    if constexpr (FMT == kF32) {
-#pragma unroll
-      for (int c = 0; c < D / 16; ++c) qf[c] = *reinterpret_cast<const float4_t*>(q + 16 * c + 4 * g);
-    } else {
-#pragma unroll
-      for (int c = 0; c < D / 32; ++c)
-        qh[c] = *reinterpret_cast<const half8_t*>(
-            q + (FMT == kF16 ? 32 * c + 8 * g : 64 * (c >> 1) + 16 * g + 8 * (c & 1)));
-    }
-
-    float4_t acc[kAcc];
-#pragma unroll
-    for (int i = 0; i < kAcc; ++i) acc[i] = float4_t{0.f, 0.f, 0.f, 0.f};
-    float M = -INFINITY, l = 0.f;                          // l: this lane's positions only
-    // `end` is a multiple of 128, or ends what the rows attend: a tile past it belongs to the next share
-    const int tiles = rows > 0 && end > t0 ? (end - t0 + 15) / 16 : 0;
-    if (lane == 0) *(volatile int*)&finished[wave] = stage0 + min(rows > 0 ? stream / S::kTilesPerStage : stages, stages);
-    for (int x = stream; x < tiles; x += streams) {
-      const int i = x / S::kTilesPerStage, xi = x - i * S::kTilesPerStage;
-      auto wait = [&](int side) {
-        while (__builtin_amdgcn_readfirstlane(*(volatile int*)&landed[side]) <= stage0 + i) __builtin_amdgcn_s_sleep(1);
-        asm volatile("" ::: "memory");
-      };
-      wait(0);
-      const int t = t0 + 16 * x;
-      const int b = (stage0 + i) % S::kBufs;
-      const char* kt = ring[b] + 16 * xi * S::kRow;
-      const char* vt = kt + S::kStage * S::kRow;
-      bool none = t >= rw.hi_max || t + 16 <= rw.lo_min;         // no row of the tile attends any of it
-      none = none || ((__builtin_amdgcn_readfirstlane(*(volatile int*)&held[b]) >> xi) & 1) == 0;
-      if (!none) {
-        // the lane's place, hidden from the compiler where registers are scarce: it then forms the LDS
-        // addresses here instead of keeping (and spilling) all of them across the loop
-        int n_ = n, g_ = g;
-        if (S::kFew) asm volatile("" : "+v"(n_), "+v"(g_));
-        // ---- scores: lane group g holds positions t + 4 g + (0 .. 3)
-        float4_t sc = float4_t{0.f, 0.f, 0.f, 0.f}, sd = sc;  // two chains of products
-#pragma unroll
-        for (int c = 0; c < S::kUnits / 4; ++c) {
-          const uint4_t w = *reinterpret_cast<const uint4_t*>(kt + n_ * S::kRow + 16 * ((4 * c + g_) ^ swizzle<S::kUnits>(n_)));
-          if constexpr (FMT == kF32) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              (e & 1 ? sd : sc) = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(w[e]), qf[c][e], e & 1 ? sd : sc, 0, 0, 0);
-          } else if constexpr (FMT == kF16) {
-            (c & 1 ? sd : sc) = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8_t, w), qh[c], c & 1 ? sd : sc, 0, 0, 0);
-          } else {
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const uint4_t v = uint4_t{codes_to_half2<false>(w[2 * e]), codes_to_half2<true>(w[2 * e]),
-                                        codes_to_half2<false>(w[2 * e + 1]), codes_to_half2<true>(w[2 * e + 1])};
-              (e & 1 ? sd : sc) = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8_t, v), qh[2 * c + e], e & 1 ? sd : sc, 0, 0, 0);
-            }
-          }
-          if (S::kFew && (c & 3) == 3) __builtin_amdgcn_sched_barrier(0);
-        }
-        sc += sd;
-        wait(1);
-        // to base-2 exponents. With 8-bit values the weight carries the value's scale, so xs is the
-        // exponent of the product and `inv` takes the scale out of the weights' sum again; a zero row's
-        // scale counts as 2^-33, below that of every other fp16 row.
-        float xs[4], inv[4];
-        uint32_t kscale = 0, vscale = 0;
-        if constexpr (FMT == kE4M3) {
-          kscale = *reinterpret_cast<const uint32_t*>(scale_ring[b] + 16 * xi + 4 * g);
-          vscale = *reinterpret_cast<const uint32_t*>(scale_ring[b] + S::kStage + 16 * xi + 4 * g);
-        }
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          if constexpr (FMT == kE4M3) {
-            const uint32_t kb = (kscale >> (8 * e)) & 255u;
-            const uint32_t vb = max((vscale >> (8 * e)) & 255u, 94u);
-            xs[e] = fmaf(sc[e], to_log2 * __uint_as_float(kb << 23), (float)((int)vb - 127));
-            inv[e] = __uint_as_float((254u - min(vb, 253u)) << 23);
-          } else {
-            xs[e] = sc[e] * to_log2;
-          }
-        }
-
-        // ---- masks, where some row does not attend all of the tile
-        bool mixed = false;                                // a non-finite value that not every row attends
-        if (t < lo_max || t + 16 > hi_min) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int pos = t + 4 * g + e;
-            if (!(pos >= lo && pos < hi)) xs[e] = -INFINITY;
-            if (pos < lo_max || pos >= hi_min) {
-#pragma unroll
-              for (int w = 0; w < S::kUnits / 16 + (S::kUnits < 16); ++w) {
-                // this lane's share of the row: its 16 lanes hold the whole of it
-                if (S::kUnits >= 16 || n < S::kUnits) {
-                  const uint4_t v = *reinterpret_cast<const uint4_t*>(vt + (4 * g_ + e) * S::kRow + 16 * (n_ + 16 * w));
-                  mixed = mixed || (nonfinite<FMT>(v[0]) | nonfinite<FMT>(v[1]) | nonfinite<FMT>(v[2]) | nonfinite<FMT>(v[3])) != 0;
-                }
-              }
-            }
-          }
-          mixed = __any(mixed);
-        }
-
-        // ---- weights
-        float m = fmaxf(fmaxf(xs[0], xs[1]), fmaxf(xs[2], xs[3]));
-        m = fmaxf(row_max(m), M);
-        if (__any(m > M)) {
-          const float f = M == m ? 1.f : exp2_fast(M - m); // -inf - -inf is not asked for
-          l *= f;
-#pragma unroll
-          for (int k = 0; k < kAcc; ++k) acc[k] *= f;
-          M = m;
-        }
-        const float ref = M == -INFINITY ? 0.f : M;
-        float wgt[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          wgt[e] = exp2_fast(xs[e] - ref);
-          if constexpr (FMT == kE4M3)
-            l = fmaf(wgt[e], inv[e], l);
-          else
-            l += wgt[e];
-        }
-
-        // ---- O^T += V^T P^T. A lane reads the same few columns of its group's 4 positions and turns
-        // them into columns of 4 positions with byte permutes (half an instruction an element).
-        const half4_t pw = half4_t{(_Float16)wgt[0], (_Float16)wgt[1], (_Float16)wgt[2], (_Float16)wgt[3]};
-        // this lane's words of set c in position `at` for column block k (0 .. 15)
-        auto load_columns = [&](int at, int k, int c, uint32_t (&w)[S::kVWords]) {
-          const int byte = S::kCols * S::kBytes * k;
-          const char* src = vt + at * S::kRow + 16 * ((byte >> 4) ^ swizzle<S::kUnits>(at)) + (byte & 15) +
-                            16 * S::kCols * S::kBytes * c;
-          if constexpr (S::kVWords == 4) {
-            const uint4_t v = *reinterpret_cast<const uint4_t*>(src);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) w[i] = v[i];
-          } else if constexpr (S::kVWords == 2) {
-            const uint2_t v = *reinterpret_cast<const uint2_t*>(src);
-            w[0] = v[0];
-            w[1] = v[1];
-          } else {
-            w[0] = *reinterpret_cast<const uint32_t*>(src);
-          }
-        };
-#pragma unroll
-        for (int c = 0; c < S::kSets; ++c) {
-          if (S::kFew) __builtin_amdgcn_sched_barrier(0);
-          uint32_t vw[4][S::kVWords];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) load_columns(4 * g_ + e, n_, c, vw[e]);
-          if (mixed) {                                     // 0 times a value that is not finite has to be 0
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-#pragma unroll
-              for (int w = 0; w < S::kVWords; ++w) vw[e][w] &= ~nonfinite<FMT>(vw[e][w]);
-          }
-          if constexpr (FMT == kF32) {
-#pragma unroll
-            for (int w = 0; w < 4; ++w)
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                acc[4 * c + w] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(vw[e][w]), wgt[e], acc[4 * c + w], 0, 0, 0);
-          } else {
-#pragma unroll
-            for (int w = 0; w < S::kCols / 2; ++w) {       // two columns at a time
-              uint32_t pair[4];
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                if constexpr (FMT == kF16)
-                  pair[e] = vw[e][w];
-                else
-                  pair[e] = (w & 1) ? codes_to_half2<true>(vw[e][w >> 1]) : codes_to_half2<false>(vw[e][w >> 1]);
-              }
-              const uint2_t a0 = uint2_t{__builtin_amdgcn_perm(pair[1], pair[0], 0x05040100u),
-                                         __builtin_amdgcn_perm(pair[3], pair[2], 0x05040100u)};
-              const uint2_t a1 = uint2_t{__builtin_amdgcn_perm(pair[1], pair[0], 0x07060302u),
-                                         __builtin_amdgcn_perm(pair[3], pair[2], 0x07060302u)};
-              const int o = S::kCols * c + 2 * w;
-              acc[o] = __builtin_amdgcn_mfma_f32_16x16x16f16(__builtin_bit_cast(half4_t, a0), pw, acc[o], 0, 0, 0);
-              acc[o + 1] = __builtin_amdgcn_mfma_f32_16x16x16f16(__builtin_bit_cast(half4_t, a1), pw, acc[o + 1], 0, 0, 0);
-            }
-          }
-        }
-        if (mixed) {
-          // the values left out above, for the rows that attend them: position by position, element by element
-#pragma unroll 1
-          for (int at = 0; at < 16; ++at) {
-            const float own = at & 2 ? (at & 1 ? wgt[3] : wgt[2]) : (at & 1 ? wgt[1] : wgt[0]);
-            const float w = __shfl(own, n + 16 * (at >> 2));
-            const bool sees = t + at >= lo && t + at < hi;
-#pragma unroll
-            for (int c = 0; c < S::kSets; ++c)
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                __builtin_amdgcn_sched_barrier(0);
-                uint32_t words[S::kVWords];
-                load_columns(at, 4 * g_ + i, c, words);
-#pragma unroll
-                for (int e = 0; e < S::kCols; ++e) {
-                  const float v = element<FMT>(words, e);
-                  if (sees && !(fabsf(v) < INFINITY)) acc[S::kCols * c + e][i] = fmaf(w, v, acc[S::kCols * c + e][i]);
-                }
-              }
-          }
-        }
-      }
-      asm volatile("" ::: "memory");
-      const int next = min((x + streams) / S::kTilesPerStage, stages);
-      if (lane == 0) *(volatile int*)&finished[wave] = stage0 + next;
-    }
-    stage0 += stages;
-    if (lane == 0) *(volatile int*)&finished[wave] = stage0;
-
-    if (tid == 0 && sp.notes != nullptr && sg.c0 == 0 && (sp.max_segs > 0 || !complete)) note_segment(sp, sg, w.size);
-
-    // ---- join the waves
-    l = row_sum(l);
-    if (l != l) M = INFINITY;                              // a NaN score is no maximum, but has to show
-    if (g == 0) {
-      stats[wave][n][0] = M;
-      stats[wave][n][1] = l;
-    }
-    __syncthreads();                                       // A: the ring is free
-    const int w0 = sub * streams;                          // the waves of this wave's tile
-    float top = M, total = 0.f;
-    for (int k = w0; k < w0 + streams; ++k) top = fmaxf(top, stats[k][n][0]);
-    const float f = M == -INFINITY ? 0.f : exp2_fast(M - top);
-    if (stream == 0 && rows > 0 && g == 0) {
-      for (int k = w0; k < w0 + streams; ++k)
-        total += stats[k][n][0] == -INFINITY ? 0.f : stats[k][n][1] * exp2_fast(stats[k][n][0] - top);
-      joined[sub][n][0] = top;
-      joined[sub][n][1] = total;
-    }
-    // acc[cols c + e] of row n, register i: column 16 cols c + cols (4 g + i) + e. The 16-byte units of
-    // a row are stored in the order of unit ^ row.
-    float* sums = reinterpret_cast<float*>(&ring[0][0]);
-    if (n < rows) {
-#pragma unroll
-      for (int c = 0; c < S::kSets; ++c)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int e = 0; e < S::kCols; e += 4) {
-            if (S::kFew) __builtin_amdgcn_sched_barrier(0);
-            const int unit = (16 * S::kCols * c + S::kCols * (4 * g + i) + e) / 4;
-            *reinterpret_cast<float4_t*>(sums + (wave * kRows + n) * D + 4 * (unit ^ n)) =
-                float4_t{acc[S::kCols * c + e][i] * f, acc[S::kCols * c + e + 1][i] * f,
-                         acc[S::kCols * c + e + 2][i] * f, acc[S::kCols * c + e + 3][i] * f};
-          }
-    }
-    __syncthreads();                                       // B
-    for (int i = tid; i < seg_rows * (D / 4); i += kRingThreads) {
-      const int rr = i / (D / 4), unit = i - rr * (D / 4), rn = rr % kRows;
-      const float* from = sums + (rr / kRows * streams * kRows + rn) * D + 4 * (unit ^ rn);
-      float4_t o = *reinterpret_cast<const float4_t*>(from);
-#pragma unroll 2
-      for (int k = 1; k < streams; ++k) o += *reinterpret_cast<const float4_t*>(from + k * (kRows * D));
-      store_row<FMT, D>(p, sp, sg, complete, rr, 4 * unit, joined[rr / kRows][rn][0], joined[rr / kRows][rn][1], o);
-    }
-    __syncthreads();                                       // C: the ring is the loaders' again
-    if (!more) return;
-    sg = next_segment(p, sp, w);
   }
 }
 
@@ -1368,19 +920,19 @@ template <int FMT, int D>
 hipError_t launch_attn_d(const AttnArgs& p, void* workspace, hipStream_t stream) {
   SplitArgs sp{};
   const int64_t most = (int64_t)p.max_tokens * p.group;    // rows of a request and key head
-  const bool few = most <= 2 * kRows;
-  sp.seg_rows = most <= kRows ? kRows : few ? 2 * kRows : kTiles * kRows;
-  const int64_t segments = ((few ? 0 : (int64_t)p.rows.N * p.group / sp.seg_rows) + p.rows.R) * p.cache.Hk;
+  const bool few = most <= kRows;
+  sp.seg_rows = few ? kRows : kTiles * kRows;
+  const int64_t segments = ((most <= sp.seg_rows ? 0 : (int64_t)p.rows.N * p.group / sp.seg_rows) + p.rows.R) * p.cache.Hk;
   int64_t groups = segments < kWholeGroups ? segments : kWholeGroups;
   const bool whole = one_group_each(p.max_len, p.sum_len, p.cache.Hk, 2 * Shape<FMT, D, 4>::kRow);
   int64_t notes = 0;
   if (whole) {
     sp.chunk_shift = kWholeShift;
   } else {
-    groups = few ? split_groups<FMT, D>() : kGroups;
+    groups = split_groups<FMT, D>();
     sp.notes = static_cast<int4*>(workspace);
     sp.parts = reinterpret_cast<float*>(static_cast<char*>(workspace) + kNoteBytes);
-    sp.part_rows = few ? sp.seg_rows : part_rows(p.rows.N, p.group);
+    sp.part_rows = few ? kRows : part_rows(p.rows.N, p.group);
     sp.chunk_shift = kChunkShift;
     const int64_t cap = (int64_t)p.cache.max_pages << p.cache.page_shift;
     while (segments * ((cap >> sp.chunk_shift) + 1) > ((int64_t)1 << 30)) ++sp.chunk_shift;
@@ -1388,13 +940,14 @@ hipError_t launch_attn_d(const AttnArgs& p, void* workspace, hipStream_t stream)
     const int64_t segs = (most + sp.seg_rows - 1) / sp.seg_rows;
     notes = segs * p.rows.R * p.cache.Hk;
     if (notes <= groups) sp.max_segs = (int)segs; else notes = groups;
+    if (segs > 1 && segs <= kMostLines && ((int64_t)p.rows.N * p.group / p.rows.R + sp.seg_rows - 1) / sp.seg_rows == segs)
+      while (1 << sp.line_shift < segs) ++sp.line_shift;
   }
-  if (most <= kRows)
+  sp.line_groups = (int)groups >> sp.line_shift;
+  if (few)
     launch_few<FMT, D, 1>(p, sp, (int)groups, stream);
-  else if (few)
-    launch_few<FMT, D, 2>(p, sp, (int)groups, stream);
   else
-    hipLaunchKernelGGL((gdn_attn_rows_k<FMT, D>), dim3((unsigned)groups), dim3(kRingBlock), 0, stream, p, sp);
+    launch_few<FMT, D, kTiles>(p, sp, (int)groups, stream);
   if (!whole) {
     // 16 slices where a segment has more than 16 parts on average, else 2
     const unsigned rows = (unsigned)(most < sp.seg_rows ? most : sp.seg_rows);

@@ -237,7 +237,8 @@ typedef struct gdn_attn_tensors {
  * rounds the weights (at most 1, relative to the row's largest) to FP16 for the product
  * with v.
  * Any number of tokens per request is taken; the kernels are made for decode and
- * verify, where the cache is read once for up to 64 rows (tokens x Hq / Hk).
+ * verify, where the cache is read once for up to 32 rows (tokens x Hq / Hk) and, where
+ * most requests have the same number of up to 256, mostly from the L2 for the rest.
  * (N + R) Hq D / 64 is at most 2^30, else GDN_ERR_SHAPE.
  * The workspace (gdn_attn_workspace_bytes() bytes, disjoint from every tensor, 16-byte
  * aligned) needs no initial value; calls that overlap in time, and captured graphs

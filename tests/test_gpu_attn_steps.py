@@ -276,10 +276,32 @@ def _check(lens, new, *, Hk, G, D, fmt, page, seed=0, **kw):
 @pytest.mark.parametrize("fmt", FORMATS)
 @pytest.mark.parametrize("D", [64, 128, 256])
 def test_rows_past_a_segment(fmt, D):
-    """Prompts of more than 64 rows, in segments of 64, 65 and 1 rows; rows of one token in two segments."""
+    """Prompts of more than 64 rows, the last segment full or of one or two rows; rows of one token in two segments."""
     _check([300, 130], [33, 65], Hk=1, G=2, D=D, fmt=fmt, page=16, seed=70)
     _check([200, 77], [7, 1], Hk=1, G=24, D=D, fmt=fmt, page=32, seed=71)
     _check([2000], [40], Hk=1, G=3, D=D, fmt=fmt, page=64, seed=72, mirrors=False)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("lens,new,G", [([3000, 2000], [8, 8], 8), ([2500, 999, 4000], [24, 23, 25], 4), ([1500], [100], 2),
+                                        ([5000, 700], [40, 41], 6), ([1500], [70], 5), ([4000, 130, 2], [16, 16, 2], 4),
+                                        ([3000, 2500, 60, 500], [9, 0, 9, 10], 4)])
+def test_segments_side_by_side(fmt, D, lens, new, G):
+    """Requests of 2, 3, 7, 8 and more segments over long caches, equally many or not, one without tokens."""
+    _check(lens, new, Hk=2, G=G, D=D, fmt=fmt, page=64, seed=80)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("window", [0, 40, 1500])
+@pytest.mark.parametrize("mirrors", [True, False])
+def test_many_requests_side_by_side(fmt, window, mirrors):
+    """Two segments each: notes by segment with few requests, by workgroup with many."""
+    rng = np.random.default_rng(81)
+    for R in (5, 90):
+        lens = [int(x) for x in rng.integers(40, 900, R)]
+        lens[1] = 5000
+        _check(lens, [10] * R, Hk=2, G=5, D=64, fmt=fmt, page=32, seed=82, window=window, mirrors=mirrors, dense=not mirrors)
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
