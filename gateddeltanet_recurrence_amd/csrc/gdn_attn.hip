@@ -46,6 +46,15 @@ constexpr int kRows = 16;                 // rows of a tile: the N side of the M
 constexpr int kTiles = 2;                 // tiles of a segment, at most
 constexpr int kChunkShift = 7;            // positions of a unit of work: 128 or more
 constexpr int kMostLines = 8;
+// Of segments that are not split, up to this many get a workgroup each. More are shared
+// out over two a CU, which load a segment's first tiles before the last one is joined,
+// evenly by length; a segment's fixed part counts as so many bytes of keys and values.
+// One each against shared: 256 requests of 100 positions, 8 key heads of 128 fp16 43 and
+// 34 us, of 300 70 and 62, of 90 .. 700 75 and 73; with 1,024 segments the uneven ones
+// lose (128 requests of 1 .. 4 drafts, 64 columns in 8 bits, 28 and 32 us).
+constexpr int kOneEach = 1024;
+constexpr int kSegmentBytes = 200000;
+constexpr int64_t kMostShared = 1 << 22;
 constexpr int kWholeShift = 30;           // one unit per segment: nothing is split
 constexpr int kGroups = 256;              // workgroups of a split launch: one per CU
 
@@ -60,7 +69,9 @@ struct SplitArgs {
   int32_t part_rows;
   int32_t seg_rows;                       // rows of a segment: 16 or 32
   int32_t line_shift, line_groups;        // log2 of the lines, workgroups of a line (see block_of)
-  int32_t chunk_shift;
+  int32_t chunk_shift;                    // log2 of a unit's positions
+  int32_t whole;                          // > 0: a share is the segments that begin in it, each as long as this many
+                                          // units more
   int32_t max_segs;                       // > 0: notes by segment, this many of a request and key head; 0: by workgroup
 };
 
@@ -84,7 +95,7 @@ __device__ __forceinline__ Plan plan_of(const AttnArgs& p, const SplitArgs& sp, 
   s.base = p.window > 0 ? clamp_pos(s.len - s.T + 1 - p.window, s.hi) & ~31 : 0;
   s.segs = (int)(((unsigned)(s.T * p.group) + sp.seg_rows - 1) / (unsigned)sp.seg_rows);
   if (sp.max_segs > 0) s.segs = min(s.segs, sp.max_segs);  // no note past the request's, whatever cu_seqlens holds
-  s.chunks = s.T > 0 ? max((int)(((int64_t)s.hi - s.base + (1ll << sp.chunk_shift) - 1) >> sp.chunk_shift), 1) : 0;
+  s.chunks = s.T > 0 ? max((int)(((int64_t)s.hi - s.base + (1ll << sp.chunk_shift) - 1) >> sp.chunk_shift) + sp.whole, 1) : 0;
   return s;
 }
 
@@ -113,11 +124,9 @@ __device__ __forceinline__ int wave_scan(int x) {
   return x;
 }
 
-// This workgroup's share [u, u_end) of the units, and the request r that holds u,
-// whose units begin at r_first. Every wave finds it by itself.
 struct Share {
   int u, u_end, r, r_first, size;
-  int start, T, len;                                       // of request `lane`, where there are at most 64
+  int first, start, T, len;                                // of request first + lane
   int id, at, line;                                        // see block_of
 };
 
@@ -137,20 +146,31 @@ __device__ __forceinline__ void block_of(const SplitArgs& sp, Share& w) {
   }
 }
 
+// A request's plan: the lanes hold 64 of them, so that no load is in the way of the table's.
+__device__ __forceinline__ Plan plan_at(const AttnArgs& p, const SplitArgs& sp, const Share& w, int r) {
+  const int k = r - w.first;
+  return k < 64 ? plan_of(p, sp, __builtin_amdgcn_readlane(w.start, k), __builtin_amdgcn_readlane(w.T, k),
+                          __builtin_amdgcn_readlane(w.len, k))
+                : plan_of(p, sp, r);
+}
+
+// This workgroup's share [u, u_end) of the units, and the request r that holds u,
+// whose units begin at r_first. Every wave finds it by itself.
 __device__ __forceinline__ Share find_share(const AttnArgs& p, const SplitArgs& sp, int lane) {
   const int R = p.rows.R, per = (R + 63) >> 6;             // requests a lane sums
   const int r0 = min(lane * per, R), r1 = min(r0 + per, R);
   int mine = 0;
   Share w;
-  w.start = w.T = w.len = 0;
+  const auto hold = [&](int first) {
+    const int r = min(first + lane, R - 1);
+    w.first = first;
+    w.start = row_start(p.rows, r);
+    w.T = max(row_start(p.rows, r + 1) - w.start, 0);
+    w.len = p.rows.seq_lens[r];
+  };
+  hold(0);
   if (R <= 64) {
-    if (r0 < r1) {
-      const Plan s = plan_of(p, sp, r0);
-      mine = units_of(sp, s, p.cache.Hk);
-      w.start = s.start;
-      w.T = s.T;
-      w.len = (int)s.len;
-    }
+    if (r0 < r1) mine = units_of(sp, plan_of(p, sp, w.start, w.T, w.len), p.cache.Hk);
   } else {
 #pragma unroll 4
     for (int r = r0; r < r1; ++r) mine += units_of(sp, plan_of(p, sp, r), p.cache.Hk);
@@ -166,6 +186,17 @@ __device__ __forceinline__ Share find_share(const AttnArgs& p, const SplitArgs& 
   const int holder = __builtin_ctzll(__ballot(w.u >= before && w.u < after));
   w.r = holder * per;
   w.r_first = __builtin_amdgcn_readlane(before, holder);
+  if (R > 64) hold(w.r);
+  if (sp.whole > 0) {
+    // on to the first segment that begins here
+    Plan s = plan_at(p, sp, w, w.r);
+    while (w.u - w.r_first >= units_of(sp, s, p.cache.Hk)) {
+      w.r_first += units_of(sp, s, p.cache.Hk);
+      s = plan_at(p, sp, w, ++w.r);
+    }
+    const unsigned past = (unsigned)(w.u - w.r_first) % (unsigned)s.chunks;
+    if (past > 0) w.u += s.chunks - (int)past;
+  }
   return w;
 }
 
@@ -185,20 +216,14 @@ struct Segment {
 
 __device__ __forceinline__ Segment next_segment(const AttnArgs& p, const SplitArgs& sp, Share& w) {
   Segment x;
-  // of at most 64 requests each lane holds one: no load in the way of the table's
-  const auto plan_at = [&](int r) {
-    return p.rows.R <= 64 ? plan_of(p, sp, __builtin_amdgcn_readlane(w.start, r), __builtin_amdgcn_readlane(w.T, r),
-                                    __builtin_amdgcn_readlane(w.len, r))
-                          : plan_of(p, sp, r);
-  };
-  x.s = plan_at(w.r);
+  x.s = plan_at(p, sp, w, w.r);
   while (w.u - w.r_first >= units_of(sp, x.s, p.cache.Hk)) {   // requests without tokens have no units
     w.r_first += units_of(sp, x.s, p.cache.Hk);
-    x.s = plan_at(++w.r);
+    x.s = plan_at(p, sp, w, ++w.r);
   }
   const unsigned local = w.u - w.r_first, seg = local / (unsigned)x.s.chunks;
   x.c0 = local - seg * x.s.chunks;
-  x.c1 = min(x.s.chunks, x.c0 + (w.u_end - w.u));
+  x.c1 = sp.whole > 0 ? x.s.chunks : min(x.s.chunks, x.c0 + (w.u_end - w.u));
   int line = w.line;
   x.h = seg;
   if (sp.line_shift == 0 && x.s.segs > 1) {
@@ -864,8 +889,12 @@ __global__ void __launch_bounds__(kThreads) gdn_attn_join_k(AttnArgs p, SplitArg
         half4_t{(_Float16)(o[0] * norm), (_Float16)(o[1] * norm), (_Float16)(o[2] * norm), (_Float16)(o[3] * norm)};
 }
 
-// Waves of gdn_attn_k's workgroups in a launch of at most one a CU: 8 where a wave's 16 KiB
-// in flight are two to four tiles or one, and not (a wave of) more.
+// Waves of gdn_attn_k's workgroups in a launch of at most one a CU: 8 with 16 KiB in
+// flight each instead of 4 with 32, where a tile is 8 or 16 KiB and the registers suffice
+// (a windowed FP32 step of 15 tokens 16.8 -> 15.5 us, 4 requests of 1,000 positions in 8
+// bits 15.8 -> 14.4, one short request 9.3 -> 8.7; large ones within 1 %). With more
+// workgroups than CUs two of 4 waves share one: 64 requests of 300 positions 17.6 us
+// against 20.7, 256 of 1,000 172 against 198.
 template <int FMT, int D, int TILES>
 constexpr int many_waves() {
   typedef Shape<FMT, D, 8> S;
@@ -895,17 +924,18 @@ int part_rows(int64_t N, int group) {
 
 // Whether every segment passes through one workgroup of its own, which spares the
 // second launch (about 5 us with what it waits for). A workgroup alone takes in about
-// 47 KB a us; split evenly, the whole call runs at about 6.4 GB a ms. Half of that time
-// is what the longest segment may take before the others wait for it. Measured, whole
-// against split: 64 requests of 1,000 positions, 8 key heads of 128 fp16 47 and 51 us,
-// 16 of 600 14 and 17; 16 of 2,048 with 4 heads 28 and 18 us, of 64 columns 18 and 15.
-// Without the host's lengths the sum is not known and counts as nothing.
-bool one_group_each(int64_t longest, int64_t sum, int heads, int64_t position_bytes) {
-  const double alone = (double)longest * position_bytes / 47e3;
+// 47 KB a us (of 8-bit pages 29, which it has to turn into halves); split evenly, the
+// whole call runs at about 6.4 GB a ms. Half of that time is what the longest segment
+// may take before the others wait for it. Measured, whole against split: 64 requests of
+// 1,000 positions, 8 key heads of 128 fp16 47 and 49 us, 16 of 600 13 and 18, one of 333
+// 8.5 and 9.8, of 700 12.7 and 9.7, 4 of 1,000 in 8 bits 14.3 and 10.8; 16 of 2,048 with
+// 4 heads 28 and 18 us. Without the host's lengths the sum is not known and counts as
+// nothing.
+bool one_group_each(int64_t longest, int64_t sum, int heads, int64_t position_bytes, bool eight_bits) {
+  const double alone = (double)longest * position_bytes / (eight_bits ? 29e3 : 47e3);
   const double together = (double)sum * heads * position_bytes / 6.4e6;
   return alone <= together / 2 + 5.0;
 }
-constexpr int64_t kWholeGroups = 4096;
 
 template <int FMT, int D, int TILES>
 void launch_few(const AttnArgs& p, const SplitArgs& sp, int groups, hipStream_t stream) {
@@ -923,18 +953,24 @@ hipError_t launch_attn_d(const AttnArgs& p, void* workspace, hipStream_t stream)
   const bool few = most <= kRows;
   sp.seg_rows = few ? kRows : kTiles * kRows;
   const int64_t segments = ((most <= sp.seg_rows ? 0 : (int64_t)p.rows.N * p.group / sp.seg_rows) + p.rows.R) * p.cache.Hk;
-  int64_t groups = segments < kWholeGroups ? segments : kWholeGroups;
-  const bool whole = one_group_each(p.max_len, p.sum_len, p.cache.Hk, 2 * Shape<FMT, D, 4>::kRow);
+  int64_t groups = segments;
+  const bool whole = one_group_each(p.max_len, p.sum_len, p.cache.Hk, 2 * Shape<FMT, D, 4>::kRow, FMT == kE4M3);
   int64_t notes = 0;
-  if (whole) {
+  const int64_t cap = (int64_t)p.cache.max_pages << p.cache.page_shift;
+  if (whole && (segments <= kOneEach || segments > kMostShared)) {
     sp.chunk_shift = kWholeShift;
+    if (segments > kMostShared) groups = 2 * kGroups;      // evenly by their number: units are counted in 32 bits
+  } else if (whole) {
+    groups = 2 * kGroups;
+    sp.chunk_shift = 5;
+    sp.whole = kSegmentBytes / (32 * 2 * Shape<FMT, D, 4>::kRow);
+    while (segments * ((cap >> sp.chunk_shift) + 1 + sp.whole) > ((int64_t)1 << 30)) ++sp.chunk_shift;
   } else {
     groups = split_groups<FMT, D>();
     sp.notes = static_cast<int4*>(workspace);
     sp.parts = reinterpret_cast<float*>(static_cast<char*>(workspace) + kNoteBytes);
     sp.part_rows = few ? kRows : part_rows(p.rows.N, p.group);
     sp.chunk_shift = kChunkShift;
-    const int64_t cap = (int64_t)p.cache.max_pages << p.cache.page_shift;
     while (segments * ((cap >> sp.chunk_shift) + 1) > ((int64_t)1 << 30)) ++sp.chunk_shift;
     // notes by segment where there are fewer segments than workgroups
     const int64_t segs = (most + sp.seg_rows - 1) / sp.seg_rows;

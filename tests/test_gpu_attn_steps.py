@@ -319,6 +319,25 @@ def test_segments_and_workgroups(fmt, mirrors, R):
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("G", [2, 20])
+def test_many_short_requests(fmt, G):
+    """More unsplit segments than get a workgroup each: shared out by length, some requests without tokens,
+    some without a cached position, one far longer than the rest."""
+    rng = np.random.default_rng(83)
+    R = 700
+    lens = [int(x) for x in rng.integers(0, 60, R)]
+    new = [int(min(x, n)) for x, n in zip(rng.integers(0, 3, R), lens)]
+    lens[130] = 700
+    lens[131:200] = [5] * 69
+    new[131:200] = [0] * 69                                # a run of requests with nothing to do
+    lens[R - 1], new[R - 1] = 33, 1
+    c = make_cache(lens, Hk=2, D=64, fmt=fmt, page=16, seed=84)
+    q = (np.random.default_rng(85).standard_normal((sum(new), 2 * G, 64))).astype(io_np(fmt))
+    want, tol = oracle_attention(c, q, _cu(new))
+    assert_within(run_attention(c, q, _cu(new), torch, gdn), want, tol, f"{fmt} {G}")
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
 @pytest.mark.parametrize("window", [1, 100, 128, 1000])
 def test_windows_of_long_caches(fmt, window):
     _check([5000, 4097, 127], [1, 1, 1], Hk=2, G=4, D=128, fmt=fmt, page=128, window=window, seed=75)
