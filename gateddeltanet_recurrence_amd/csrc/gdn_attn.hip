@@ -24,14 +24,19 @@
 // fp16 66 against 69, 8 bits 67 against 47, D = 64 fp16 37 against 25, D = 128 fp32
 // 100 against 89 us.
 //
-// Work is split evenly over the workgroups whatever the lengths: the positions of
-// every segment (request, 16 or 32 rows, key head) in chunks of 128 are laid end to
-// end, and workgroup b takes the b-th equal share of the chunks. A share that holds
-// all of a segment's chunks writes the output; the others leave (M, l, sum) in the
-// workspace and gdn_attn_join_k, a second launch, joins them. Every wave forms the
-// prefix sums of the requests' chunks by itself: R loads and one scan instead of a
-// launch. The order of every sum is fixed by the lengths, so results repeat bit for
-// bit; no atomics are used.
+// Work is split evenly over the workgroups whatever the lengths (short requests are not
+// split at all, see one_group_each): the positions of every segment (request, 16 or 32
+// rows, key head) in chunks of 128 are laid end to end, and workgroup b takes the b-th
+// equal share of the chunks. A share that holds all of a segment's chunks writes the
+// output; the others leave (M, l, sum) in the workspace and gdn_attn_join_k, a second
+// launch, joins them. Every wave forms the prefix sums of the requests' chunks by
+// itself: R loads and one scan instead of a launch. The order of every sum is fixed by
+// the lengths, so results repeat bit for bit; no atomics are used.
+//
+// Measured: 64 requests of up to 16,384 positions, 8 key heads of 128 fp16, 1.85 GB, 294 us
+// (6.3 TB/s; counted HBM reads equal the bytes of the attended keys and values); 16 x up
+// to 4 drafts over up to 8,192 positions of 4 x 256 fp16, 279 MB, 60 us; one request of
+// 131,072 positions in 8 bits, 270 MB, 52 us.
 #include <type_traits>
 
 #include "gdn_attn_kernels.h"
@@ -45,7 +50,7 @@ constexpr int kThreads = 256;             // of gdn_attn_join_k
 constexpr int kRows = 16;                 // rows of a tile: the N side of the MFMA
 constexpr int kTiles = 2;                 // tiles of a segment, at most
 constexpr int kChunkShift = 7;            // positions of a unit of work: 128 or more
-constexpr int kMostLines = 8;
+constexpr int kMostLines = 8;             // see block_of
 // Of segments that are not split, up to this many get a workgroup each. More are shared
 // out over two a CU, which load a segment's first tiles before the last one is joined,
 // evenly by length; a segment's fixed part counts as so many bytes of keys and values.
@@ -966,6 +971,7 @@ hipError_t launch_attn_d(const AttnArgs& p, void* workspace, hipStream_t stream)
     sp.whole = kSegmentBytes / (32 * 2 * Shape<FMT, D, 4>::kRow);
     while (segments * ((cap >> sp.chunk_shift) + 1 + sp.whole) > ((int64_t)1 << 30)) ++sp.chunk_shift;
   } else {
+    static_assert(D == 64 || split_groups<FMT, D>() == kGroups, "see attn_workspace_bytes");
     groups = split_groups<FMT, D>();
     sp.notes = static_cast<int4*>(workspace);
     sp.parts = reinterpret_cast<float*>(static_cast<char*>(workspace) + kNoteBytes);

@@ -63,7 +63,9 @@ extern "C" {
  * 4: gdn_forward_no_alloc and GDN_ERR_SCRATCH.
  * 5: the update rules GDN_RULE_DELTA, GDN_RULE_GATED and GDN_RULE_LINEAR.
  * 6: gdn_replay_forward (replay and verify in one pass over the committed state)
- *    and its pooled form gdn_replay_forward_pooled (gdn_pool.h). */
+ *    and its pooled form gdn_replay_forward_pooled (gdn_pool.h).
+ * 7: gdn_conv_decode_forward (gdn_conv.h). The attention layer's calls (gdn_attn.h)
+ *    were added to it and change none of the others. */
 #define GDN_ABI_VERSION 7
 
 typedef enum gdn_status {
