@@ -72,7 +72,7 @@ struct SplitArgs {
   int4* notes;                            // of the segments that may be split (see note_segment); null: none is
   float* parts;                           // [2 * groups][part_rows * (D + 2)]: M, l, sums
   int32_t part_rows;
-  int32_t seg_rows;                       // rows of a segment: 16 or 32
+  int32_t seg_shift;                      // log2 of a segment's rows: 4 or 5
   int32_t line_shift, line_groups;        // log2 of the lines, workgroups of a line (see block_of)
   int32_t chunk_shift;                    // log2 of a unit's positions
   int32_t whole;                          // > 0: a share is the segments that begin in it, each as long as this many
@@ -83,24 +83,25 @@ struct SplitArgs {
 // What a request brings: its rows, the positions any of them attends and its units.
 struct Plan {
   int start, T;                           // first token, tokens
-  int64_t len;                            // seq_lens[r] as given
+  int len;                                // seq_lens[r], 0 for less
   int base, hi;                           // positions [base, hi), base a multiple of 32
   int segs, chunks;                       // segments of a key head, units of each
 };
 
-__device__ __forceinline__ int clamp_pos(int64_t x, int hi) { return (int)(x < 0 ? 0 : x > hi ? hi : x); }
+// Tokens, positions and the window are at most 2^30, so that differences of two fit 32 bits.
+__device__ __forceinline__ int clamp_pos(int x, int hi) { return min(max(x, 0), hi); }
 
 __device__ __forceinline__ Plan plan_of(const AttnArgs& p, const SplitArgs& sp, int start, int T, int len) {
   Plan s;
   s.start = start;
   s.T = T;
-  s.len = len;
+  s.len = max(len, 0);
   const int cap = p.cache.max_pages << p.cache.page_shift;
-  s.hi = clamp_pos(s.len, cap);
+  s.hi = min(s.len, cap);
   s.base = p.window > 0 ? clamp_pos(s.len - s.T + 1 - p.window, s.hi) & ~31 : 0;
-  s.segs = (int)(((unsigned)(s.T * p.group) + sp.seg_rows - 1) / (unsigned)sp.seg_rows);
+  s.segs = (s.T * p.group + (1 << sp.seg_shift) - 1) >> sp.seg_shift;
   if (sp.max_segs > 0) s.segs = min(s.segs, sp.max_segs);  // no note past the request's, whatever cu_seqlens holds
-  s.chunks = s.T > 0 ? max((int)(((int64_t)s.hi - s.base + (1ll << sp.chunk_shift) - 1) >> sp.chunk_shift) + sp.whole, 1) : 0;
+  s.chunks = s.T > 0 ? max((int)(((unsigned)(s.hi - s.base) + (1u << sp.chunk_shift) - 1) >> sp.chunk_shift) + sp.whole, 1) : 0;
   return s;
 }
 
@@ -115,7 +116,7 @@ __device__ __forceinline__ int units_of(const SplitArgs& sp, const Plan& s, int 
 }
 
 __device__ __forceinline__ int share_of(int total, int groups) {
-  return max((int)((unsigned)(total + groups - 1) / (unsigned)groups), 1);
+  return total <= groups ? 1 : (int)((unsigned)(total + groups - 1) / (unsigned)groups);
 }
 
 // Inclusive sum over the lanes of a wave.
@@ -184,7 +185,7 @@ __device__ __forceinline__ Share find_share(const AttnArgs& p, const SplitArgs& 
   const int total = __builtin_amdgcn_readlane(after, 63);
   block_of(sp, w);
   const int share = w.size = share_of(total, sp.line_groups);
-  w.u = (int)min((int64_t)w.at * share, (int64_t)total);
+  w.u = min(w.at * share, total);
   w.u_end = min(w.u + share, total);
   w.r = w.r_first = 0;
   if (w.u >= w.u_end) return w;
@@ -207,7 +208,7 @@ __device__ __forceinline__ Share find_share(const AttnArgs& p, const SplitArgs& 
 
 // The token of a request that a row belongs to.
 __device__ __forceinline__ int token_of(const AttnArgs& p, const Plan& s, int row) {
-  return s.T == 1 ? 0 : (int)((unsigned)row / (unsigned)p.group);
+  return s.T == 1 ? 0 : p.group == 1 ? row : (int)((unsigned)row / (unsigned)p.group);
 }
 
 // The next segment of a share: units [c0, c1) of (request, rows from seg_row on, key
@@ -226,7 +227,7 @@ __device__ __forceinline__ Segment next_segment(const AttnArgs& p, const SplitAr
     w.r_first += units_of(sp, x.s, p.cache.Hk);
     x.s = plan_at(p, sp, w, ++w.r);
   }
-  const unsigned local = w.u - w.r_first, seg = local / (unsigned)x.s.chunks;
+  const unsigned local = w.u - w.r_first, seg = x.s.chunks == 1 ? local : local / (unsigned)x.s.chunks;
   x.c0 = local - seg * x.s.chunks;
   x.c1 = sp.whole > 0 ? x.s.chunks : min(x.s.chunks, x.c0 + (w.u_end - w.u));
   int line = w.line;
@@ -235,16 +236,16 @@ __device__ __forceinline__ Segment next_segment(const AttnArgs& p, const SplitAr
     x.h = seg / (unsigned)x.s.segs;
     line = seg - x.h * x.s.segs;
   }
-  x.seg_row = line * sp.seg_rows;
+  x.seg_row = line << sp.seg_shift;
   x.id = w.id;
   x.note = sp.max_segs > 0 ? (w.r * p.cache.Hk + x.h) * sp.max_segs + line : w.id;
   x.last_unit = w.u - x.c0 + x.s.chunks - 1;
   w.u += x.c1 - x.c0;
-  x.rows = line < x.s.segs ? min(sp.seg_rows, x.s.T * p.group - x.seg_row) : 0;   // 0: fewer segments than lines
+  x.rows = line < x.s.segs ? min(1 << sp.seg_shift, x.s.T * p.group - x.seg_row) : 0;   // 0: fewer segments than lines
   const int cap = p.cache.max_pages << p.cache.page_shift;
-  const int64_t past_last = x.rows == 0 ? 0 : x.s.len - x.s.T + token_of(p, x.s, x.seg_row + x.rows - 1) + 1;
-  x.t0 = x.s.base + (int)((int64_t)x.c0 << sp.chunk_shift);
-  x.end = (int)min((int64_t)x.s.base + ((int64_t)x.c1 << sp.chunk_shift), (int64_t)clamp_pos(past_last, cap));
+  const int past_last = x.rows == 0 ? 0 : x.s.len - x.s.T + token_of(p, x.s, x.seg_row + x.rows - 1) + 1;
+  x.t0 = x.s.base + (x.c0 << sp.chunk_shift);
+  x.end = (int)min((unsigned)x.s.base + ((unsigned)x.c1 << sp.chunk_shift), (unsigned)clamp_pos(past_last, cap));
   return x;
 }
 
@@ -272,8 +273,8 @@ __device__ __forceinline__ Rows rows_of(const AttnArgs& p, const Plan& s, int ro
   const int last = row0 + max(rows, 1) - 1, row = min(row0 + n, min(last, s.T * p.group - 1));
   x.j = token_of(p, s, row);
   x.head = row - x.j * p.group;
-  const int64_t before = s.len - s.T + 1;                  // one past the first token's newest position
-  const int64_t past = before + x.j, past0 = before + token_of(p, s, row0), past1 = before + token_of(p, s, last);
+  const int before = s.len - s.T + 1;                      // one past the first token's newest position
+  const int past = before + x.j, past0 = before + token_of(p, s, row0), past1 = before + token_of(p, s, last);
   x.hi = n < rows ? clamp_pos(past, cap) : 0;
   x.hi_min = clamp_pos(past0, cap);
   x.hi_max = clamp_pos(past1, cap);
@@ -828,7 +829,7 @@ __global__ void __launch_bounds__(kThreads) gdn_attn_join_k(AttnArgs p, SplitArg
     // notes by segment: those of requests without that many rows are not written
     const int r = id / (p.cache.Hk * sp.max_segs), seg = id % sp.max_segs;
     const int T = row_start(p.rows, r + 1) - row_start(p.rows, r);
-    if ((int64_t)T * p.group <= (int64_t)seg * sp.seg_rows) return;
+    if ((int64_t)T * p.group <= (int64_t)seg << sp.seg_shift) return;
   }
   const int4 a = sp.notes[2 * id], b = sp.notes[2 * id + 1];
   const int count = a.x, b0 = a.y, rows = a.z, seg_row = a.w, start = b.x, h = b.y;
@@ -956,8 +957,10 @@ hipError_t launch_attn_d(const AttnArgs& p, void* workspace, hipStream_t stream)
   SplitArgs sp{};
   const int64_t most = (int64_t)p.max_tokens * p.group;    // rows of a request and key head
   const bool few = most <= kRows;
-  sp.seg_rows = few ? kRows : kTiles * kRows;
-  const int64_t segments = ((most <= sp.seg_rows ? 0 : (int64_t)p.rows.N * p.group / sp.seg_rows) + p.rows.R) * p.cache.Hk;
+  const int seg_rows = few ? kRows : kTiles * kRows;
+  sp.seg_shift = few ? 4 : 5;
+  static_assert(kRows == 16 && kTiles == 2, "see seg_shift");
+  const int64_t segments = ((most <= seg_rows ? 0 : (int64_t)p.rows.N * p.group / seg_rows) + p.rows.R) * p.cache.Hk;
   int64_t groups = segments;
   const bool whole = one_group_each(p.max_len, p.sum_len, p.cache.Hk, 2 * Shape<FMT, D, 4>::kRow, FMT == kE4M3);
   int64_t notes = 0;
@@ -979,10 +982,10 @@ hipError_t launch_attn_d(const AttnArgs& p, void* workspace, hipStream_t stream)
     sp.chunk_shift = kChunkShift;
     while (segments * ((cap >> sp.chunk_shift) + 1) > ((int64_t)1 << 30)) ++sp.chunk_shift;
     // notes by segment where there are fewer segments than workgroups
-    const int64_t segs = (most + sp.seg_rows - 1) / sp.seg_rows;
+    const int64_t segs = (most + seg_rows - 1) / seg_rows;
     notes = segs * p.rows.R * p.cache.Hk;
     if (notes <= groups) sp.max_segs = (int)segs; else notes = groups;
-    if (segs > 1 && segs <= kMostLines && ((int64_t)p.rows.N * p.group / p.rows.R + sp.seg_rows - 1) / sp.seg_rows == segs)
+    if (segs > 1 && segs <= kMostLines && ((int64_t)p.rows.N * p.group / p.rows.R + seg_rows - 1) / seg_rows == segs)
       while (1 << sp.line_shift < segs) ++sp.line_shift;
   }
   sp.line_groups = (int)groups >> sp.line_shift;
@@ -992,7 +995,7 @@ hipError_t launch_attn_d(const AttnArgs& p, void* workspace, hipStream_t stream)
     launch_few<FMT, D, kTiles>(p, sp, (int)groups, stream);
   if (!whole) {
     // 16 slices where a segment has more than 16 parts on average, else 2
-    const unsigned rows = (unsigned)(most < sp.seg_rows ? most : sp.seg_rows);
+    const unsigned rows = (unsigned)(most < seg_rows ? most : seg_rows);
     if (notes * 16 < groups)
       hipLaunchKernelGGL((gdn_attn_join_k<FMT, D, 16>), dim3((unsigned)notes, rows, D / 64), dim3(kThreads), 0, stream, p, sp);
     else
