@@ -256,7 +256,7 @@ __device__ __forceinline__ void note_segment(const SplitArgs& sp, const Segment&
   // the shares from this one on that hold the segment
   const int parts = x.c1 == x.s.chunks ? 0 : (int)((unsigned)x.last_unit / (unsigned)w.size) - w.at + 1;
   sp.notes[2 * x.note] = int4{parts, w.id, x.rows, x.seg_row};
-  sp.notes[2 * x.note + 1] = int4{x.s.start, x.h, 0, 0};
+  sp.notes[2 * x.note + 1] = int4{x.s.start, x.h, x.s.T, 0};
 }
 
 // A lane's row of a tile of `rows` rows from row0 on, and the positions that the
@@ -825,13 +825,13 @@ __global__ void __launch_bounds__(kThreads) gdn_attn_join_k(AttnArgs p, SplitArg
   __shared__ float4_t sums[kThreads];
   __shared__ float stats[kThreads / kLanes][2];
   const int tid = threadIdx.x, id = (int)blockIdx.x;
-  if (sp.max_segs > 0) {
+  const int4 a = sp.notes[2 * id], b = sp.notes[2 * id + 1];
+  if (sp.max_segs > 0 && p.rows.cu_seqlens != nullptr) {
     // notes by segment: those of requests without that many rows are not written
-    const int r = id / (p.cache.Hk * sp.max_segs), seg = id % sp.max_segs;
+    const int heads = sp.max_segs > 1 ? id / sp.max_segs : id, seg = id - heads * sp.max_segs, r = heads / p.cache.Hk;
     const int T = row_start(p.rows, r + 1) - row_start(p.rows, r);
     if ((int64_t)T * p.group <= (int64_t)seg << sp.seg_shift) return;
   }
-  const int4 a = sp.notes[2 * id], b = sp.notes[2 * id + 1];
   const int count = a.x, b0 = a.y, rows = a.z, seg_row = a.w, start = b.x, h = b.y;
   const int slot = tid / kLanes, slice = slot % SLICES;
   const int row0 = (int)blockIdx.y * kRowsHere, rr = row0 + slot / SLICES;
@@ -886,7 +886,7 @@ __global__ void __launch_bounds__(kThreads) gdn_attn_join_k(AttnArgs p, SplitArg
     l = fmaf(stats[slot + i][1], f, l);
   }
   const float norm = l == 0.f ? 0.f : 1.f / l;
-  const int row = seg_row + rr, j = (int)((unsigned)row / (unsigned)p.group);
+  const int row = seg_row + rr, j = b.z == 1 ? 0 : (int)((unsigned)row / (unsigned)p.group);
   IO* out = static_cast<IO*>(p.output) + ((int64_t)(start + j) * p.Hq + h * p.group + row - j * p.group) * D + d;
   if constexpr (FMT == kF32)
     *reinterpret_cast<float4_t*>(out) = o * norm;
