@@ -36,7 +36,7 @@
 // Measured: 64 requests of up to 16,384 positions, 8 key heads of 128 fp16, 1.85 GB, 294 us
 // (6.3 TB/s; counted HBM reads equal the bytes of the attended keys and values); 16 x up
 // to 4 drafts over up to 8,192 positions of 4 x 256 fp16, 279 MB, 60 us; one request of
-// 131,072 positions in 8 bits, 270 MB, 52 us.
+// 131,072 positions in 8 bits, 270 MB, 51 us; one of 333 positions 8 us.
 #include <type_traits>
 
 #include "gdn_attn_kernels.h"
@@ -934,7 +934,7 @@ int part_rows(int64_t N, int group) {
 // whole call runs at about 6.4 GB a ms. Half of that time is what the longest segment
 // may take before the others wait for it. Measured, whole against split: 64 requests of
 // 1,000 positions, 8 key heads of 128 fp16 47 and 49 us, 16 of 600 13 and 18, one of 333
-// 8.5 and 9.8, of 700 12.7 and 9.7, 4 of 1,000 in 8 bits 14.3 and 10.8; 16 of 2,048 with
+// 8.3 and 9.4, of 700 12.7 and 9.3, 4 of 1,000 in 8 bits 14.3 and 10.8; 16 of 2,048 with
 // 4 heads 28 and 18 us. Without the host's lengths the sum is not known and counts as
 // nothing.
 bool one_group_each(int64_t longest, int64_t sum, int heads, int64_t position_bytes, bool eight_bits) {
