@@ -343,3 +343,16 @@ def test_frequency_refusals(kw, code):
     with pytest.raises(gdn.GDNError) as e:
         gdn.gdn_rope_frequencies(kw.pop("rotary_dim"), **kw)
     assert e.value.status == code
+
+
+@pytest.mark.parametrize("cls,pack,values", [
+    (gdn.GdnRopeParams, "_rope_params", (7, 4, 2, 64, 1, 32, 1, 1.25, 256, 128)),
+    (gdn.GdnRopeTensors, "_rope_tensors", (FAKE, FAKE + 16, 3 << 33, 0, 5, 6)),
+    (gdn.GdnKvParams, "_kv_params", (7, 3, 4, 64, 1, 0.5, 8, 16, 24)),
+    (gdn.GdnKvTensors, "_kv_tensors", tuple(FAKE + 64 * i for i in range(10))),
+    (gdn.GdnAttnParams, "_attn_params", (9, 2, 8, 0.125, 100, 4096)),
+    (gdn.GdnAttnTensors, "_attn_tensors", (FAKE, 0, 0, FAKE + 32, 0, FAKE + 64)),
+])
+def test_packed_structs_are_the_ctypes_ones(cls, pack, values):
+    from gateddeltanet_recurrence_amd import binding
+    assert getattr(binding, pack)(*values) == bytes(cls(*values))
