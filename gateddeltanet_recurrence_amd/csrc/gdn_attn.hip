@@ -88,8 +88,13 @@ struct Plan {
   int segs, chunks;                       // segments of a key head, units of each
 };
 
-// Tokens, positions and the window are at most 2^30, so that differences of two fit 32 bits.
+// Tokens are at most 2^30 and lengths not negative here, so that their differences fit 32 bits.
 __device__ __forceinline__ int clamp_pos(int x, int hi) { return min(max(x, 0), hi); }
+
+// The first position that the token before `past` attends, at most hi.
+__device__ __forceinline__ int window_start(const AttnArgs& p, int past, int hi) {
+  return clamp_pos(__builtin_elementwise_sub_sat(past, p.window), hi);
+}
 
 __device__ __forceinline__ Plan plan_of(const AttnArgs& p, const SplitArgs& sp, int start, int T, int len) {
   Plan s;
@@ -98,7 +103,7 @@ __device__ __forceinline__ Plan plan_of(const AttnArgs& p, const SplitArgs& sp, 
   s.len = max(len, 0);
   const int cap = p.cache.max_pages << p.cache.page_shift;
   s.hi = min(s.len, cap);
-  s.base = p.window > 0 ? clamp_pos(s.len - s.T + 1 - p.window, s.hi) & ~31 : 0;
+  s.base = p.window > 0 ? window_start(p, s.len - s.T + 1, s.hi) & ~31 : 0;
   s.segs = (s.T * p.group + (1 << sp.seg_shift) - 1) >> sp.seg_shift;
   if (sp.max_segs > 0) s.segs = min(s.segs, sp.max_segs);  // no note past the request's, whatever cu_seqlens holds
   s.chunks = s.T > 0 ? max((int)(((unsigned)(s.hi - s.base) + (1u << sp.chunk_shift) - 1) >> sp.chunk_shift) + sp.whole, 1) : 0;
@@ -280,9 +285,9 @@ __device__ __forceinline__ Rows rows_of(const AttnArgs& p, const Plan& s, int ro
   x.hi_max = clamp_pos(past1, cap);
   x.lo = x.lo_min = x.lo_max = 0;
   if (p.window > 0) {
-    x.lo = clamp_pos(past - p.window, cap);
-    x.lo_min = clamp_pos(past0 - p.window, cap);
-    x.lo_max = clamp_pos(past1 - p.window, cap);
+    x.lo = window_start(p, past, cap);
+    x.lo_min = window_start(p, past0, cap);
+    x.lo_max = window_start(p, past1, cap);
   }
   return x;
 }

@@ -406,7 +406,7 @@ int gdn_attn_forward(const gdn_attn_params* p, const gdn_attn_tensors* t, const 
   if (out.overlaps(ws)) return GDN_ERR_ALIAS;
   gdn::AttnArgs a{};
   a.q = t->q; a.output = t->output; a.q_stride = qs;
-  a.Hq = (int32_t)Hq; a.group = (int32_t)(Hq / Hk); a.window = (int32_t)std::min<int64_t>(p->window, kMaxPositions);
+  a.Hq = (int32_t)Hq; a.group = (int32_t)(Hq / Hk); a.window = p->window;
   a.scale = p->scale > 0.f ? p->scale : 1.0f / std::sqrt((float)D);
   // the most tokens of a request, and the most positions one attends, as far as they are known here: a
   // mirror's, else what the call and the table hold

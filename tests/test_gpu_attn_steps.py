@@ -389,3 +389,30 @@ def test_minus_infinity_everywhere_is_an_empty_row():
     q[..., 3] = 1.0
     c["k"][..., 4:], c["k"][..., :3] = np.nan_to_num(c["k"][..., 4:]), np.nan_to_num(c["k"][..., :3])
     assert np.all(run_attention(c, q, _cu([1]), torch, gdn) == 0)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("G", [2, 20])
+def test_lengths_and_windows_at_the_ends_of_int32(fmt, G):
+    """Any int32 in seq_lens (no host mirror), and the largest window: positions past the table count as far as
+    the table goes, those before 0 not at all."""
+    D, page = 64, 16
+    c = make_cache([64, 64, 64, 64], Hk=2, D=D, fmt=fmt, page=page, seed=90)
+    c["table"] = np.ascontiguousarray(c["table"][:, :4])       # 64 positions are all there is
+    new = [2, 1, 2, 1]
+    q = np.random.default_rng(91).standard_normal((6, 2 * G, D)).astype(io_np(fmt))
+    rows = [q[0:1], q[1:2], q[2:3], q[3:4], q[4:5], q[5:6]]
+    of = [0, 0, 1, 2, 2, 3]                                    # request of each row
+    odd = {**c, "lens": np.asarray([2 ** 31 - 1, -2 ** 31, -1, 2 ** 31 - 1], np.int32)}
+    for window in (0, 2 ** 31 - 1, 1000):
+        got = run_attention(odd, q, _cu(new), torch, gdn, mirrors=False, window=window)
+        for i, (row, r) in enumerate(zip(rows, of)):
+            if r in (1, 2) or window == 1000:
+                assert np.all(got[i] == 0), (window, i)
+                continue
+            one = {**c, "table": c["table"][r:r + 1], "lens": np.asarray([64], np.int32)}
+            want, tol = oracle_attention(one, row, _cu([1]))
+            assert_within(got[i:i + 1], want, tol, f"{fmt} {i}")
+    # the largest window on ordinary lengths is no window
+    plain = run_attention(c, q, _cu(new), torch, gdn)
+    assert np.array_equal(run_attention(c, q, _cu(new), torch, gdn, window=2 ** 31 - 1), plain)
