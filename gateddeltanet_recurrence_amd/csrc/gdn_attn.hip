@@ -542,41 +542,39 @@ __global__ void __launch_bounds__(64 * WAVES, 1) gdn_attn_k(AttnArgs p, SplitArg
       for (int k = 0; k < kAcc; ++k) acc[i][k] = float4_t{0.f, 0.f, 0.f, 0.f};
     }
 
-    while (t < end) {
+    bool some = t < end;
+    while (some) {
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const bool some = t < end;
         // ---- scores: block a of lane group g holds positions t + 16 a + 4 g + (0 .. 3)
         float4_t x[TILES][S::kBlocks];
-        if (some) {
 #pragma unroll
-          for (int a = 0; a < S::kBlocks; ++a) {
+        for (int a = 0; a < S::kBlocks; ++a) {
 #pragma unroll
-            for (int r = 0; r < TILES; ++r) x[r][a] = float4_t{0.f, 0.f, 0.f, 0.f};
+          for (int r = 0; r < TILES; ++r) x[r][a] = float4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int c = 0; c < S::kKLoads; ++c) {
-              const uint32_t(&w)[4] = kw[u][a][c];
-              if constexpr (FMT == kF32) {
+          for (int c = 0; c < S::kKLoads; ++c) {
+            const uint32_t(&w)[4] = kw[u][a][c];
+            if constexpr (FMT == kF32) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-#pragma unroll
-                  for (int r = 0; r < TILES; ++r)
-                    x[r][a] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(w[e]), qf[r][c][e], x[r][a], 0, 0, 0);
-              } else if constexpr (FMT == kF16) {
+              for (int e = 0; e < 4; ++e)
 #pragma unroll
                 for (int r = 0; r < TILES; ++r)
-                  x[r][a] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
-                      __builtin_bit_cast(half8_t, uint4_t{w[0], w[1], w[2], w[3]}), qh[r][c], x[r][a], 0, 0, 0);
-              } else {
+                  x[r][a] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(w[e]), qf[r][c][e], x[r][a], 0, 0, 0);
+            } else if constexpr (FMT == kF16) {
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                  const uint4_t v = uint4_t{codes_to_half2<false>(w[2 * e]), codes_to_half2<true>(w[2 * e]),
-                                            codes_to_half2<false>(w[2 * e + 1]), codes_to_half2<true>(w[2 * e + 1])};
+              for (int r = 0; r < TILES; ++r)
+                x[r][a] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
+                    __builtin_bit_cast(half8_t, uint4_t{w[0], w[1], w[2], w[3]}), qh[r][c], x[r][a], 0, 0, 0);
+            } else {
 #pragma unroll
-                  for (int r = 0; r < TILES; ++r)
-                    x[r][a] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8_t, v), qh[r][2 * c + e], x[r][a],
-                                                                     0, 0, 0);
-                }
+              for (int e = 0; e < 2; ++e) {
+                const uint4_t v = uint4_t{codes_to_half2<false>(w[2 * e]), codes_to_half2<true>(w[2 * e]),
+                                          codes_to_half2<false>(w[2 * e + 1]), codes_to_half2<true>(w[2 * e + 1])};
+#pragma unroll
+                for (int r = 0; r < TILES; ++r)
+                  x[r][a] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8_t, v), qh[r][2 * c + e], x[r][a],
+                                                                   0, 0, 0);
               }
             }
           }
@@ -594,167 +592,167 @@ __global__ void __launch_bounds__(64 * WAVES, 1) gdn_attn_k(AttnArgs p, SplitArg
         load_k(u, t + U * kStep);
         look_up(u, t + 2 * U * kStep);
         __builtin_amdgcn_sched_barrier(0);
-        if (some) {
-          // to base-2 exponents. With 8-bit values the weight carries the value's scale, so xs is the
-          // exponent of the product and `inv` takes the scale out of the weights' sum again; a zero row's
-          // scale counts as 2^-33, below that of every other fp16 row.
-          float xs[TILES][S::kPos], inv[S::kPos];
+        // to base-2 exponents. With 8-bit values the weight carries the value's scale, so xs is the
+        // exponent of the product and `inv` takes the scale out of the weights' sum again; a zero row's
+        // scale counts as 2^-33, below that of every other fp16 row.
+        float xs[TILES][S::kPos], inv[S::kPos];
 #pragma unroll
-          for (int i = 0; i < S::kPos; ++i) {
-            if constexpr (FMT == kE4M3) {
-              const uint32_t kb = (ks[i >> 2] >> (8 * (i & 3))) & 255u;
-              const uint32_t vb = max((vscale[u][i >> 2] >> (8 * (i & 3))) & 255u, 94u);
-#pragma unroll
-              for (int r = 0; r < TILES; ++r)
-                xs[r][i] = fmaf(x[r][i >> 2][i & 3], to_log2 * __uint_as_float(kb << 23), (float)((int)vb - 127));
-              inv[i] = __uint_as_float((254u - min(vb, 253u)) << 23);
-            } else {
-#pragma unroll
-              for (int r = 0; r < TILES; ++r) xs[r][i] = x[r][i >> 2][i & 3] * to_log2;
-            }
-          }
-
-          // ---- masks, where some row does not attend all of the tile, or part of it has no page
-          bool whole = t >= rw[0].lo_max && t + S::kTile <= rw[0].hi_min && t + S::kTile <= end;
-#pragma unroll
-          for (int a = 0; a < S::kBlocks; ++a) whole = whole && page[a] >= 0;
-          bool mixed = false;                              // a non-finite value that only some rows attend
-          if (!whole) {
-#pragma unroll
-            for (int i = 0; i < S::kPos; ++i) {
-              const int pos = t + 16 * (i >> 2) + 4 * g + (i & 3);
-              const bool there = page[i >> 2] >= 0 && pos < end;
-#pragma unroll
-              for (int r = 0; r < TILES; ++r)
-                if (!(there && pos >= lo[r] && pos < hi[r])) xs[r][i] = -INFINITY;
-              // a value that not every row attends may have to count for some: 0 times it has to be 0
-              // for the others, whatever it is
-              if (!(there && pos >= rw[0].lo_max && pos < rw[0].hi_min)) {
-#pragma unroll
-                for (int c = 0; c < S::kSets; ++c)
-#pragma unroll
-                  for (int w = 0; w < S::kVWords; ++w) {
-                    const uint32_t bad = nonfinite<FMT>(vw[u][i][c][w]);
-                    mixed = mixed || bad != 0;
-                    vw[u][i][c][w] &= ~bad;
-                  }
-              }
-            }
-            mixed = __any(mixed);
-          }
-
-          // ---- weights
-          float wgt[TILES][S::kPos];
-#pragma unroll
-          for (int r = 0; r < TILES; ++r) {
-            float m = xs[r][0];
-#pragma unroll
-            for (int i = 1; i < S::kPos; ++i) m = fmaxf(m, xs[r][i]);
-            m = fmaxf(row_max(m), M[r]);
-            if (__any(m > M[r])) {
-              const float f = M[r] == m ? 1.f : exp2_fast(M[r] - m);   // -inf - -inf is not asked for
-              l[r] *= f;
-#pragma unroll
-              for (int i = 0; i < kAcc; ++i) acc[r][i] *= f;
-              M[r] = m;
-            }
-            const float ref = M[r] == -INFINITY ? 0.f : M[r];
-#pragma unroll
-            for (int i = 0; i < S::kPos; ++i) {
-              wgt[r][i] = exp2_fast(xs[r][i] - ref);
-              if constexpr (FMT == kE4M3)
-                l[r] = fmaf(wgt[r][i], inv[i], l[r]);
-              else
-                l[r] += wgt[r][i];
-            }
-          }
-
-          // ---- O^T += V^T P^T. A lane holds the same few columns of its 4 or 8 positions and turns them into
-          // columns of positions with byte permutes (half an instruction an element).
-          if constexpr (FMT == kF32) {
-#pragma unroll
-            for (int c = 0; c < S::kSets; ++c)
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-#pragma unroll
-                  for (int r = 0; r < TILES; ++r)
-                    acc[r][4 * c + e] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(vw[u][i][c][e]), wgt[r][i],
-                                                                             acc[r][4 * c + e], 0, 0, 0);
-          } else {
-            half8_t pw[TILES];
+        for (int i = 0; i < S::kPos; ++i) {
+          if constexpr (FMT == kE4M3) {
+            const uint32_t kb = (ks[i >> 2] >> (8 * (i & 3))) & 255u;
+            const uint32_t vb = max((vscale[u][i >> 2] >> (8 * (i & 3))) & 255u, 94u);
 #pragma unroll
             for (int r = 0; r < TILES; ++r)
+              xs[r][i] = fmaf(x[r][i >> 2][i & 3], to_log2 * __uint_as_float(kb << 23), (float)((int)vb - 127));
+            inv[i] = __uint_as_float((254u - min(vb, 253u)) << 23);
+          } else {
 #pragma unroll
-              for (int i = 0; i < 8; ++i) pw[r][i] = (_Float16)wgt[r][i];
-#pragma unroll
-            for (int c = 0; c < S::kSets; ++c)
-#pragma unroll
-              for (int k = 0; k < S::kCols / 2; ++k) {     // two columns at a time
-                uint32_t pair[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                  if constexpr (FMT == kF16)
-                    pair[i] = vw[u][i][c][k];
-                  else
-                    pair[i] = (k & 1) ? codes_to_half2<true>(vw[u][i][c][k >> 1]) : codes_to_half2<false>(vw[u][i][c][k >> 1]);
-                }
-                uint4_t a0, a1;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                  a0[i] = __builtin_amdgcn_perm(pair[2 * i + 1], pair[2 * i], 0x05040100u);
-                  a1[i] = __builtin_amdgcn_perm(pair[2 * i + 1], pair[2 * i], 0x07060302u);
-                }
-                const int o = S::kCols * c + 2 * k;
-#pragma unroll
-                for (int r = 0; r < TILES; ++r) {
-                  acc[r][o] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8_t, a0), pw[r], acc[r][o], 0, 0, 0);
-                  acc[r][o + 1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8_t, a1), pw[r], acc[r][o + 1], 0, 0, 0);
-                }
-              }
+            for (int r = 0; r < TILES; ++r) xs[r][i] = x[r][i >> 2][i & 3] * to_log2;
           }
-          if (mixed) {
-            // the values left out above, for the rows that attend them: position by position, element by
-            // element, from memory
-#pragma unroll 1
-            for (int at = 0; at < S::kTile; ++at) {
-              const int pos = t + at, pg = pages.page(pages.entry(pos & ~15), pos & ~15);
-              if (pg < 0 || pos >= end) continue;
-              float w[TILES];
-              bool sees[TILES];
+        }
+
+        // ---- masks, where some row does not attend all of the tile, or part of it has no page
+        bool whole = t >= rw[0].lo_max && t + S::kTile <= rw[0].hi_min && t + S::kTile <= end;
 #pragma unroll
-              for (int r = 0; r < TILES; ++r) {
-                float own = wgt[r][0];
+        for (int a = 0; a < S::kBlocks; ++a) whole = whole && page[a] >= 0;
+        bool mixed = false;                                // a non-finite value that only some rows attend
+        if (__builtin_expect(!whole, 0)) {
 #pragma unroll
-                for (int i = 1; i < S::kPos; ++i) own = 4 * (at >> 4) + (at & 3) == i ? wgt[r][i] : own;
-                w[r] = __shfl(own, n + 16 * ((at >> 2) & 3));
-                sees[r] = pos >= lo[r] && pos < hi[r] && !(pos >= rw[0].lo_max && pos < rw[0].hi_min);
-              }
-              const rsrc_t rs = make_rsrc(static_cast<const char*>(p.cache.v) + pages.row(pg, pos) * S::kRow, S::kRow);
+          for (int i = 0; i < S::kPos; ++i) {
+            const int pos = t + 16 * (i >> 2) + 4 * g + (i & 3);
+            const bool there = page[i >> 2] >= 0 && pos < end;
+#pragma unroll
+            for (int r = 0; r < TILES; ++r)
+              if (!(there && pos >= lo[r] && pos < hi[r])) xs[r][i] = -INFINITY;
+            // a value that not every row attends may have to count for some: 0 times it has to be 0
+            // for the others, whatever it is
+            if (!(there && pos >= rw[0].lo_max && pos < rw[0].hi_min)) {
 #pragma unroll
               for (int c = 0; c < S::kSets; ++c)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                  __builtin_amdgcn_sched_barrier(0);
-                  uint32_t words[S::kVWords];
-                  load_words<S::kVWords, 0>(rs, S::kCols * S::kBytes * (16 * c + 4 * g + i), words);
-#pragma unroll
-                  for (int e = 0; e < S::kCols; ++e) {
-                    const float v = element<FMT>(words, e);
-#pragma unroll
-                    for (int r = 0; r < TILES; ++r)
-                      if (sees[r] && !(fabsf(v) < INFINITY))
-                        acc[r][S::kCols * c + e][i] = fmaf(w[r], v, acc[r][S::kCols * c + e][i]);
-                  }
+                for (int w = 0; w < S::kVWords; ++w) {
+                  const uint32_t bad = nonfinite<FMT>(vw[u][i][c][w]);
+                  mixed = mixed || bad != 0;
+                  vw[u][i][c][w] &= ~bad;
                 }
             }
+          }
+          mixed = __any(mixed);
+        }
+
+        // ---- weights
+        float wgt[TILES][S::kPos];
+#pragma unroll
+        for (int r = 0; r < TILES; ++r) {
+          float m = xs[r][0];
+#pragma unroll
+          for (int i = 1; i < S::kPos; ++i) m = fmaxf(m, xs[r][i]);
+          m = fmaxf(row_max(m), M[r]);
+          if (__any(m > M[r])) {
+            const float f = M[r] == m ? 1.f : exp2_fast(M[r] - m);   // -inf - -inf is not asked for
+            l[r] *= f;
+#pragma unroll
+            for (int i = 0; i < kAcc; ++i) acc[r][i] *= f;
+            M[r] = m;
+          }
+          const float ref = M[r] == -INFINITY ? 0.f : M[r];
+#pragma unroll
+          for (int i = 0; i < S::kPos; ++i) {
+            wgt[r][i] = exp2_fast(xs[r][i] - ref);
+            if constexpr (FMT == kE4M3)
+              l[r] = fmaf(wgt[r][i], inv[i], l[r]);
+            else
+              l[r] += wgt[r][i];
+          }
+        }
+
+        // ---- O^T += V^T P^T. A lane holds the same few columns of its 4 or 8 positions and turns them into
+        // columns of positions with byte permutes (half an instruction an element).
+        if constexpr (FMT == kF32) {
+#pragma unroll
+          for (int c = 0; c < S::kSets; ++c)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int r = 0; r < TILES; ++r)
+                  acc[r][4 * c + e] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(vw[u][i][c][e]), wgt[r][i],
+                                                                           acc[r][4 * c + e], 0, 0, 0);
+        } else {
+          half8_t pw[TILES];
+#pragma unroll
+          for (int r = 0; r < TILES; ++r)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) pw[r][i] = (_Float16)wgt[r][i];
+#pragma unroll
+          for (int c = 0; c < S::kSets; ++c)
+#pragma unroll
+            for (int k = 0; k < S::kCols / 2; ++k) {     // two columns at a time
+              uint32_t pair[8];
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                if constexpr (FMT == kF16)
+                  pair[i] = vw[u][i][c][k];
+                else
+                  pair[i] = (k & 1) ? codes_to_half2<true>(vw[u][i][c][k >> 1]) : codes_to_half2<false>(vw[u][i][c][k >> 1]);
+              }
+              uint4_t a0, a1;
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                a0[i] = __builtin_amdgcn_perm(pair[2 * i + 1], pair[2 * i], 0x05040100u);
+                a1[i] = __builtin_amdgcn_perm(pair[2 * i + 1], pair[2 * i], 0x07060302u);
+              }
+              const int o = S::kCols * c + 2 * k;
+#pragma unroll
+              for (int r = 0; r < TILES; ++r) {
+                acc[r][o] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8_t, a0), pw[r], acc[r][o], 0, 0, 0);
+                acc[r][o + 1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8_t, a1), pw[r], acc[r][o + 1], 0, 0, 0);
+              }
+            }
+        }
+        if (__builtin_expect(mixed, 0)) {
+          // the values left out above, for the rows that attend them: position by position, element by
+          // element, from memory
+#pragma unroll 1
+          for (int at = 0; at < S::kTile; ++at) {
+            const int pos = t + at, pg = pages.page(pages.entry(pos & ~15), pos & ~15);
+            if (pg < 0 || pos >= end) continue;
+            float w[TILES];
+            bool sees[TILES];
+#pragma unroll
+            for (int r = 0; r < TILES; ++r) {
+              float own = wgt[r][0];
+#pragma unroll
+              for (int i = 1; i < S::kPos; ++i) own = 4 * (at >> 4) + (at & 3) == i ? wgt[r][i] : own;
+              w[r] = __shfl(own, n + 16 * ((at >> 2) & 3));
+              sees[r] = pos >= lo[r] && pos < hi[r] && !(pos >= rw[0].lo_max && pos < rw[0].hi_min);
+            }
+            const rsrc_t rs = make_rsrc(static_cast<const char*>(p.cache.v) + pages.row(pg, pos) * S::kRow, S::kRow);
+#pragma unroll
+            for (int c = 0; c < S::kSets; ++c)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                __builtin_amdgcn_sched_barrier(0);
+                uint32_t words[S::kVWords];
+                load_words<S::kVWords, 0>(rs, S::kCols * S::kBytes * (16 * c + 4 * g + i), words);
+#pragma unroll
+                for (int e = 0; e < S::kCols; ++e) {
+                  const float v = element<FMT>(words, e);
+#pragma unroll
+                  for (int r = 0; r < TILES; ++r)
+                    if (sees[r] && !(fabsf(v) < INFINITY))
+                      acc[r][S::kCols * c + e][i] = fmaf(w[r], v, acc[r][S::kCols * c + e][i]);
+                }
+              }
           }
         }
         __builtin_amdgcn_sched_barrier(0);
         load_v(u, t + U * kStep);
         __builtin_amdgcn_sched_barrier(0);
         t += kStep;
+        some = t < end;
+        if (!some) break;                                  // short segments end here, past few of the steps
       }
     }
 
