@@ -234,8 +234,8 @@ typedef struct gdn_attn_tensors {
  * attends none gives zeros. What the cache holds at other positions has no
  * influence, whatever it is. A row whose scores are all -inf gives zeros, too, and one
  * with a NaN score NaN. Scores, weights, sums and the output accumulate in FP32; FP16 io
- * rounds the weights (at most 1, relative to the row's largest) to FP16 for the product
- * with v.
+ * takes the weights into the product with v to 2^-19 of each, or 2^-38 of the row's
+ * largest (of weight times the value's scale with GDN_CACHE_E4M3).
  * Any number of tokens per request is taken; the kernels are made for decode and
  * verify, where the cache is read once for up to 32 rows (tokens x Hq / Hk) and, where
  * most requests have the same number of up to 256, mostly from the L2 for the rest.
