@@ -896,8 +896,9 @@ __global__ void __launch_bounds__(kThreads) gdn_attn_join_k(AttnArgs p, SplitArg
     l *= f;
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) {
-      const float w = i + k * SLICES < count && m[k] != -INFINITY ? exp2_fast(m[k] - top) : 0.f;
-      o += x[k] * w;
+      const bool there = i + k * SLICES < count;
+      const float w = there && m[k] != -INFINITY ? exp2_fast(m[k] - top) : 0.f;
+      o += (there ? x[k] : float4_t{0.f, 0.f, 0.f, 0.f}) * w;   // 0 times a repeated part's infinity is NaN
       l = fmaf(li[k], w, l);
     }
     M = top;

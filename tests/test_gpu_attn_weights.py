@@ -15,7 +15,6 @@ import numpy as np
 import pytest
 
 from attn_helpers import assert_within, make_cache, run_attention
-from gpu_helpers import dev
 
 pytestmark = pytest.mark.gpu
 
