@@ -353,6 +353,18 @@ template <int FMT> __device__ __forceinline__ float element(const uint32_t* w, i
   return (float)__builtin_bit_cast(_Float16, (uint16_t)(e & 1 ? pair >> 16 : pair));
 }
 
+// Four columns of the output: a row without weights gives zeros, whatever the values that it gave none.
+template <int FMT, typename IO>
+__device__ __forceinline__ void store_output(IO* out, float4_t o, float l) {
+  const float norm = l == 0.f ? 0.f : 1.f / l;
+  if (l == 0.f) o = float4_t{0.f, 0.f, 0.f, 0.f};
+  if constexpr (FMT == kF32)
+    *reinterpret_cast<float4_t*>(out) = o * norm;
+  else
+    *reinterpret_cast<half4_t*>(out) =
+        half4_t{(_Float16)(o[0] * norm), (_Float16)(o[1] * norm), (_Float16)(o[2] * norm), (_Float16)(o[3] * norm)};
+}
+
 // Four columns from d on of row rr of a segment, joined over the workgroup's waves:
 // the output, or this workgroup's part.
 template <int FMT, int D>
@@ -362,12 +374,7 @@ __device__ __forceinline__ void store_row(const AttnArgs& p, const SplitArgs& sp
     typedef typename std::conditional<FMT == kF32, float, _Float16>::type IO;
     const int row = sg.seg_row + rr, j = token_of(p, sg.s, row);
     IO* out = static_cast<IO*>(p.output) + ((int64_t)(sg.s.start + j) * p.Hq + sg.h * p.group + row - j * p.group) * D + d;
-    const float norm = l == 0.f ? 0.f : 1.f / l;
-    if constexpr (FMT == kF32)
-      *reinterpret_cast<float4_t*>(out) = o * norm;
-    else
-      *reinterpret_cast<half4_t*>(out) =
-          half4_t{(_Float16)(o[0] * norm), (_Float16)(o[1] * norm), (_Float16)(o[2] * norm), (_Float16)(o[3] * norm)};
+    store_output<FMT>(out, o, l);
   } else {
     float* part = sp.parts + (2 * (int64_t)sg.id + (sg.c0 == 0 ? 1 : 0)) * (sp.part_rows * (D + 2));
     *reinterpret_cast<float4_t*>(part + 2 * sp.part_rows + rr * D + d) = o;
@@ -921,14 +928,9 @@ __global__ void __launch_bounds__(kThreads) gdn_attn_join_k(AttnArgs p, SplitArg
     o += sums[tid + i * kLanes] * f;
     l = fmaf(stats[slot + i][1], f, l);
   }
-  const float norm = l == 0.f ? 0.f : 1.f / l;
   const int row = seg_row + rr, j = b.z == 1 ? 0 : (int)((unsigned)row / (unsigned)p.group);
   IO* out = static_cast<IO*>(p.output) + ((int64_t)(start + j) * p.Hq + h * p.group + row - j * p.group) * D + d;
-  if constexpr (FMT == kF32)
-    *reinterpret_cast<float4_t*>(out) = o * norm;
-  else
-    *reinterpret_cast<half4_t*>(out) =
-        half4_t{(_Float16)(o[0] * norm), (_Float16)(o[1] * norm), (_Float16)(o[2] * norm), (_Float16)(o[3] * norm)};
+  store_output<FMT>(out, o, l);
 }
 
 // Waves of gdn_attn_k's workgroups in a launch of at most one a CU: 8 with 16 KiB in

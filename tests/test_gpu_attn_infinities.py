@@ -50,3 +50,22 @@ def test_an_infinite_value_that_is_attended_is_infinite(fmt, length, new):
                 sees = np.arange(new) >= new - (length - pos)
                 assert np.all(got[sees][..., 9] == sign * np.inf), (pos, got[..., 9])
                 assert np.all(np.isfinite(got[~sees])) and np.all(np.isfinite(np.delete(got, 9, -1)))
+
+
+@pytest.mark.parametrize("fmt", ["f16", "f32"])
+@pytest.mark.parametrize("value", [np.nan, np.inf])
+@pytest.mark.parametrize("length,new", [(1, 1), (50, 1), (50, 4), (700, 3), (6000, 2)])
+def test_a_row_without_a_finite_score_is_zero_whatever_its_values(fmt, value, length, new):
+    """Scores that are all -inf give zeros."""
+    D, G = 64, 4
+    c = make_cache([length], Hk=1, D=D, fmt=fmt, page=16, seed=140, wide=False)
+    for p, s in (_place(c, 0, pos) for pos in range(length)):
+        c["k"][p, 0, s, 3] = -np.inf
+    p, s = _place(c, 0, 0)
+    c["v"][p, 0, s, 9] = value
+    q = np.random.default_rng(141).standard_normal((new, G, D)).astype(c["k"].dtype)
+    q[:, :, 3] = 1.0
+    for mirrors in (True, False):
+        _case(f"{fmt} {value} length={length} new={new} mirrors={mirrors}")
+        got = run_attention(c, q, _cu([new]), torch, gdn, mirrors=mirrors)
+        assert np.all(got == 0)
