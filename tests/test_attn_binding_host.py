@@ -1,0 +1,47 @@
+"""Host-side checks that the Python binding makes before the attention layer's C calls: no GPU, no
+library call."""
+from __future__ import annotations
+
+import pytest
+
+torch = pytest.importorskip("torch")
+from gateddeltanet_recurrence_amd import binding          # noqa: E402
+
+
+def _strided(N=6, H=2, D=64, gap=128):
+    """q as a slice of a projection's output, and dense rows that begin at the same address."""
+    wide = torch.zeros(N, H * D + gap)
+    return wide[:, :H * D].view(N, H, D), wide.flatten()[:N * H * D].view(N, H, D)
+
+
+def test_an_output_at_its_inputs_address_has_its_strides():
+    """Equal addresses mean in place, with the input's stride: dense rows there would not be what is written."""
+    q, dense = _strided()
+    assert q.data_ptr() == dense.data_ptr() and not q.is_contiguous() and dense.is_contiguous()
+    with pytest.raises(ValueError, match="q_out"):
+        binding._out_rows(dense, q, "q_out")
+    with pytest.raises(ValueError, match="q_out"):
+        binding._out_rows(q, dense, "q_out")
+    square = torch.zeros(3, 64, 64)
+    with pytest.raises(ValueError, match="q_out"):
+        binding._out_rows(square.transpose(1, 2), square, "q_out")
+
+
+def test_outputs_that_are_taken():
+    q, dense = _strided()
+    binding._out_rows(q, q, "q_out")
+    binding._out_rows(q.view(q.shape), q, "q_out")              # the same rows as another tensor
+    binding._out_rows(dense.view(dense.shape), dense, "q_out")
+    binding._out_rows(torch.zeros(q.shape), q, "q_out")
+    one, dense_one = _strided(N=1)
+    binding._out_rows(dense_one, one, "q_out")                  # one token has no stride
+    q0, _ = _strided(N=0)
+    binding._out_rows(torch.zeros(q0.shape), q0, "q_out")
+
+
+@pytest.mark.parametrize("bad", [lambda q: None, lambda q: torch.zeros(q.shape[0] + 1, *q.shape[1:]),
+                                 lambda q: torch.zeros(q.shape, dtype=torch.float16), lambda q: _strided()[0]])
+def test_outputs_that_are_refused(bad):
+    q = torch.zeros(6, 2, 64)
+    with pytest.raises(ValueError):
+        binding._out_rows(bad(q), q, "q_out")
