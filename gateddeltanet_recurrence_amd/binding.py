@@ -144,8 +144,73 @@ def library_path() -> str:
     return os.environ.get("GDN_LIBRARY") or os.path.join(PKG, _LIB_NAME)
 
 
+def _declare(L):
+    """Argument and result types of L's functions; the attention layer's calls on packed structs."""
+    vp, i32 = ctypes.c_void_p, ctypes.c_int32
+    L.gdn_forward.argtypes = [ctypes.POINTER(GdnParams), ctypes.POINTER(GdnTensors), vp,
+                              ctypes.c_size_t, vp]
+    L.gdn_forward.restype = ctypes.c_int
+    L.gdn_forward_no_alloc.argtypes = [ctypes.POINTER(GdnParams), ctypes.POINTER(GdnTensors), vp]
+    L.gdn_forward_no_alloc.restype = ctypes.c_int
+    L.gdn_forward_workspace_bytes.argtypes = [ctypes.POINTER(GdnParams), vp,
+                                              ctypes.POINTER(ctypes.c_size_t)]
+    L.gdn_forward_workspace_bytes.restype = ctypes.c_int
+    L.gdn_resolve_plan.argtypes = [ctypes.POINTER(GdnParams), vp, ctypes.POINTER(i32)]
+    L.gdn_resolve_plan.restype = ctypes.c_int
+    L.gdn_replay.argtypes = [i32, i32, i32, i32, i32, i32, vp, vp, vp, vp, vp, vp]
+    L.gdn_replay.restype = ctypes.c_int
+    L.gdn_replay_forward.argtypes = [ctypes.POINTER(GdnParams), ctypes.POINTER(GdnTensors), vp, vp, vp,
+                                     vp, vp]
+    L.gdn_replay_forward.restype = ctypes.c_int
+    L.gdn_conv_forward.argtypes = [ctypes.POINTER(GdnConvParams),
+                                   ctypes.POINTER(GdnConvTensors), vp]
+    L.gdn_conv_forward.restype = ctypes.c_int
+    L.gdn_conv_replay.argtypes = [i32, i32, i32, i32, vp, vp, vp, vp, vp, vp]
+    L.gdn_conv_replay.restype = ctypes.c_int
+    sp = ctypes.POINTER(GdnSlots)
+    L.gdn_forward_pooled.argtypes = [ctypes.POINTER(GdnParams), ctypes.POINTER(GdnTensors), sp, vp,
+                                     ctypes.c_size_t, vp]
+    L.gdn_forward_pooled.restype = ctypes.c_int
+    L.gdn_replay_pooled.argtypes = [ctypes.POINTER(GdnParams), vp, vp, vp, vp, vp, sp, vp]
+    L.gdn_replay_pooled.restype = ctypes.c_int
+    L.gdn_replay_forward_pooled.argtypes = [ctypes.POINTER(GdnParams), ctypes.POINTER(GdnTensors), sp, vp,
+                                            vp, vp, vp, vp]
+    L.gdn_replay_forward_pooled.restype = ctypes.c_int
+    L.gdn_conv_forward_pooled.argtypes = [ctypes.POINTER(GdnConvParams),
+                                          ctypes.POINTER(GdnConvTensors), sp, vp]
+    L.gdn_conv_forward_pooled.restype = ctypes.c_int
+    L.gdn_conv_replay_pooled.argtypes = [i32, i32, i32, i32, vp, vp, vp, vp, vp, sp, vp]
+    L.gdn_conv_replay_pooled.restype = ctypes.c_int
+    L.gdn_conv_decode_forward.argtypes = [ctypes.POINTER(GdnParams), ctypes.POINTER(GdnTensors),
+                                          ctypes.POINTER(GdnConvFused), vp]
+    L.gdn_conv_decode_forward.restype = ctypes.c_int
+    L.gdn_publish_slots.argtypes = [i32, vp, vp, vp]
+    L.gdn_publish_slots.restype = ctypes.c_int
+    dbl, cp = ctypes.c_double, ctypes.POINTER(GdnKvCache)
+    L.gdn_rope_frequencies.argtypes = [i32, dbl, i32, dbl, dbl, dbl, dbl, vp, ctypes.POINTER(ctypes.c_float)]
+    L.gdn_rope_forward.argtypes = [ctypes.POINTER(GdnRopeParams), ctypes.POINTER(GdnRopeTensors), vp]
+    for fn in (L.gdn_kv_write, L.gdn_kv_read):
+        fn.argtypes = [ctypes.POINTER(GdnKvParams), ctypes.POINTER(GdnKvTensors), cp, vp]
+    L.gdn_attn_forward.argtypes = [ctypes.POINTER(GdnAttnParams), ctypes.POINTER(GdnAttnTensors), cp, vp,
+                                   ctypes.c_size_t, vp]
+    L.gdn_attn_workspace_bytes.argtypes = [ctypes.POINTER(GdnAttnParams), cp, ctypes.POINTER(ctypes.c_size_t)]
+    for fn in (L.gdn_rope_frequencies, L.gdn_rope_forward, L.gdn_kv_write, L.gdn_kv_read, L.gdn_attn_forward,
+               L.gdn_attn_workspace_bytes):
+        fn.restype = ctypes.c_int
+    chars = ctypes.c_char_p
+    calls = {n: L[n] for n in ("gdn_rope_forward", "gdn_kv_write", "gdn_kv_read", "gdn_attn_forward")}
+    calls["gdn_rope_forward"].argtypes = [chars, chars, vp]
+    calls["gdn_kv_write"].argtypes = calls["gdn_kv_read"].argtypes = [chars, chars, vp, vp]
+    calls["gdn_attn_forward"].argtypes = [chars, chars, vp, vp, ctypes.c_size_t, vp]
+    for fn in calls.values():
+        fn.restype = ctypes.c_int
+    L.gdn_strerror.argtypes = [ctypes.c_int]
+    L.gdn_strerror.restype = ctypes.c_char_p
+    return calls
+
+
 def lib() -> ctypes.CDLL:
-    """The loaded libgdn.so; raises LibraryNotBuilt when it has not been built."""
+    """The loaded libgdn.so; raises LibraryNotBuilt when it has not been built, or is not of this version."""
     global _lib, _calls
     if _lib is None:
         path = library_path()
@@ -153,71 +218,15 @@ def lib() -> ctypes.CDLL:
             raise LibraryNotBuilt(f"{path} is missing: build it with "
                                   "`python -m gateddeltanet_recurrence_amd.build`")
         L = ctypes.CDLL(path)
-        vp, i32 = ctypes.c_void_p, ctypes.c_int32
-        L.gdn_forward.argtypes = [ctypes.POINTER(GdnParams), ctypes.POINTER(GdnTensors), vp,
-                                  ctypes.c_size_t, vp]
-        L.gdn_forward.restype = ctypes.c_int
-        L.gdn_forward_no_alloc.argtypes = [ctypes.POINTER(GdnParams), ctypes.POINTER(GdnTensors), vp]
-        L.gdn_forward_no_alloc.restype = ctypes.c_int
-        L.gdn_forward_workspace_bytes.argtypes = [ctypes.POINTER(GdnParams), vp,
-                                                  ctypes.POINTER(ctypes.c_size_t)]
-        L.gdn_forward_workspace_bytes.restype = ctypes.c_int
-        L.gdn_resolve_plan.argtypes = [ctypes.POINTER(GdnParams), vp, ctypes.POINTER(i32)]
-        L.gdn_resolve_plan.restype = ctypes.c_int
-        L.gdn_replay.argtypes = [i32, i32, i32, i32, i32, i32, vp, vp, vp, vp, vp, vp]
-        L.gdn_replay.restype = ctypes.c_int
-        L.gdn_replay_forward.argtypes = [ctypes.POINTER(GdnParams), ctypes.POINTER(GdnTensors), vp, vp, vp,
-                                         vp, vp]
-        L.gdn_replay_forward.restype = ctypes.c_int
-        L.gdn_conv_forward.argtypes = [ctypes.POINTER(GdnConvParams),
-                                       ctypes.POINTER(GdnConvTensors), vp]
-        L.gdn_conv_forward.restype = ctypes.c_int
-        L.gdn_conv_replay.argtypes = [i32, i32, i32, i32, vp, vp, vp, vp, vp, vp]
-        L.gdn_conv_replay.restype = ctypes.c_int
-        sp = ctypes.POINTER(GdnSlots)
-        L.gdn_forward_pooled.argtypes = [ctypes.POINTER(GdnParams), ctypes.POINTER(GdnTensors), sp, vp,
-                                         ctypes.c_size_t, vp]
-        L.gdn_forward_pooled.restype = ctypes.c_int
-        L.gdn_replay_pooled.argtypes = [ctypes.POINTER(GdnParams), vp, vp, vp, vp, vp, sp, vp]
-        L.gdn_replay_pooled.restype = ctypes.c_int
-        L.gdn_replay_forward_pooled.argtypes = [ctypes.POINTER(GdnParams), ctypes.POINTER(GdnTensors), sp, vp,
-                                                vp, vp, vp, vp]
-        L.gdn_replay_forward_pooled.restype = ctypes.c_int
-        L.gdn_conv_forward_pooled.argtypes = [ctypes.POINTER(GdnConvParams),
-                                              ctypes.POINTER(GdnConvTensors), sp, vp]
-        L.gdn_conv_forward_pooled.restype = ctypes.c_int
-        L.gdn_conv_replay_pooled.argtypes = [i32, i32, i32, i32, vp, vp, vp, vp, vp, sp, vp]
-        L.gdn_conv_replay_pooled.restype = ctypes.c_int
-        L.gdn_conv_decode_forward.argtypes = [ctypes.POINTER(GdnParams), ctypes.POINTER(GdnTensors),
-                                              ctypes.POINTER(GdnConvFused), vp]
-        L.gdn_conv_decode_forward.restype = ctypes.c_int
-        L.gdn_publish_slots.argtypes = [i32, vp, vp, vp]
-        L.gdn_publish_slots.restype = ctypes.c_int
-        dbl, cp = ctypes.c_double, ctypes.POINTER(GdnKvCache)
-        L.gdn_rope_frequencies.argtypes = [i32, dbl, i32, dbl, dbl, dbl, dbl, vp, ctypes.POINTER(ctypes.c_float)]
-        L.gdn_rope_forward.argtypes = [ctypes.POINTER(GdnRopeParams), ctypes.POINTER(GdnRopeTensors), vp]
-        for fn in (L.gdn_kv_write, L.gdn_kv_read):
-            fn.argtypes = [ctypes.POINTER(GdnKvParams), ctypes.POINTER(GdnKvTensors), cp, vp]
-        L.gdn_attn_forward.argtypes = [ctypes.POINTER(GdnAttnParams), ctypes.POINTER(GdnAttnTensors), cp, vp,
-                                       ctypes.c_size_t, vp]
-        L.gdn_attn_workspace_bytes.argtypes = [ctypes.POINTER(GdnAttnParams), cp, ctypes.POINTER(ctypes.c_size_t)]
-        for fn in (L.gdn_rope_frequencies, L.gdn_rope_forward, L.gdn_kv_write, L.gdn_kv_read, L.gdn_attn_forward,
-                   L.gdn_attn_workspace_bytes):
-            fn.restype = ctypes.c_int
-        chars = ctypes.c_char_p
-        calls = {n: L[n] for n in ("gdn_rope_forward", "gdn_kv_write", "gdn_kv_read", "gdn_attn_forward")}
-        calls["gdn_rope_forward"].argtypes = [chars, chars, vp]
-        calls["gdn_kv_write"].argtypes = calls["gdn_kv_read"].argtypes = [chars, chars, vp, vp]
-        calls["gdn_attn_forward"].argtypes = [chars, chars, vp, vp, ctypes.c_size_t, vp]
-        for fn in calls.values():
-            fn.restype = ctypes.c_int
-        L.gdn_strerror.argtypes = [ctypes.c_int]
-        L.gdn_strerror.restype = ctypes.c_char_p
-        L.gdn_abi_version.argtypes = []
-        L.gdn_abi_version.restype = ctypes.c_int
-        if L.gdn_abi_version() != ABI_VERSION:
-            raise LibraryNotBuilt(f"{path} has ABI version {L.gdn_abi_version()}, this binding "
-                                  f"needs {ABI_VERSION}: rebuild it")
+        try:
+            L.gdn_abi_version.argtypes = []
+            L.gdn_abi_version.restype = ctypes.c_int
+            if L.gdn_abi_version() != ABI_VERSION:
+                raise LibraryNotBuilt(f"{path} has ABI version {L.gdn_abi_version()}, this binding "
+                                      f"needs {ABI_VERSION}: rebuild it")
+            calls = _declare(L)
+        except AttributeError as e:                          # a function that a library of this version may lack
+            raise LibraryNotBuilt(f"{path} is older than this binding ({e}): rebuild it") from e
         _lib, _calls = L, calls
     return _lib
 

@@ -65,7 +65,8 @@ extern "C" {
  * 6: gdn_replay_forward (replay and verify in one pass over the committed state)
  *    and its pooled form gdn_replay_forward_pooled (gdn_pool.h).
  * 7: gdn_conv_decode_forward (gdn_conv.h). The attention layer's calls (gdn_attn.h)
- *    were added to it and change none of the others. */
+ *    were added to it and change none of the others: a library of version 7 may lack
+ *    them, which a caller that loads it at run time sees by their symbols. */
 #define GDN_ABI_VERSION 7
 
 typedef enum gdn_status {

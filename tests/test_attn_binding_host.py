@@ -2,6 +2,8 @@
 library call."""
 from __future__ import annotations
 
+import ctypes
+
 import pytest
 
 torch = pytest.importorskip("torch")
@@ -45,3 +47,47 @@ def test_outputs_that_are_refused(bad):
     q = torch.zeros(6, 2, 64)
     with pytest.raises(ValueError):
         binding._out_rows(bad(q), q, "q_out")
+
+
+class _Function:
+    def __init__(self, value):
+        self.value = value
+
+    def __call__(self):
+        return self.value
+
+
+class _Older:
+    """A library with the version's number and a few of its functions."""
+
+    def __init__(self, version, names):
+        self.gdn_abi_version = _Function(version)
+        for n in names:
+            setattr(self, n, _Function(0))
+
+
+@pytest.mark.parametrize("version,names", [
+    (binding.ABI_VERSION, ["gdn_forward"]),                     # this number, without the newer functions
+    (binding.ABI_VERSION - 1, []), (binding.ABI_VERSION + 1, []),
+])
+def test_a_library_of_another_build_says_rebuild(monkeypatch, tmp_path, version, names):
+    path = tmp_path / "libgdn.so"
+    path.write_bytes(b"")
+    monkeypatch.setattr(binding, "_lib", None)
+    monkeypatch.setattr(binding, "_calls", None)
+    monkeypatch.setattr(binding, "library_path", lambda: str(path))
+    monkeypatch.setattr(ctypes, "CDLL", lambda p: _Older(version, names))
+    for call in (binding.lib, binding.gdn_abi_version, lambda: binding._call("gdn_kv_write")):
+        with pytest.raises(binding.LibraryNotBuilt, match="rebuild it"):
+            call()
+    assert binding._lib is None and binding._calls is None
+
+
+def test_a_library_without_a_version_says_rebuild(monkeypatch, tmp_path):
+    path = tmp_path / "libgdn.so"
+    path.write_bytes(b"")
+    monkeypatch.setattr(binding, "_lib", None)
+    monkeypatch.setattr(binding, "library_path", lambda: str(path))
+    monkeypatch.setattr(ctypes, "CDLL", lambda p: object())
+    with pytest.raises(binding.LibraryNotBuilt, match="rebuild it"):
+        binding.lib()
