@@ -108,13 +108,16 @@ __device__ __forceinline__ int64_t position_of(const RowArgs& p, int n, int& r) 
   return (int64_t)p.seq_lens[r] - row_start(p, r + 1) + n;
 }
 
-// factor cos t and factor sin t, rounded once to float wherever the position lies: t is
-// reduced to y, at most an eighth of a turn, in turns and in double precision, and
-// the power series' terms up to y^13 and y^12 leave less than 2^-40.
-__device__ __forceinline__ float2 turn_of(double t, double factor) {
-  constexpr double kInvTwoPi = 0.15915494309189533577, kTwoPi = 6.283185307179586477;
-  const double turn = t * kInvTwoPi, quarter = rint(4.0 * turn);
-  const double y = fma(-0.25, quarter, turn) * kTwoPi, z = y * y;
+// factor cos t and factor sin t of t = position * frequency, rounded once to float wherever the position lies: the
+// product and its share of a turn are kept as sums of two doubles, so that what is left of the angle, y, at most an
+// eighth of a turn, has all its digits (one double holds a far position's angle only to 2^-52 of it: 2^-21 at 2^31).
+// The power series' terms up to y^13 and y^12 leave less than 2^-40.
+__device__ __forceinline__ float2 turn_of(double position, double frequency, double factor) {
+  constexpr double kInvTwoPi = 0.15915494309189533577, kInvTwoPiLow = -9.839338337591243e-18;
+  constexpr double kTwoPi = 6.283185307179586477;
+  const double t = position * frequency, turn = t * kInvTwoPi, quarter = rint(4.0 * turn);
+  const double low = fma(t, kInvTwoPi, -turn) + fma(fma(position, frequency, -t), kInvTwoPi, t * kInvTwoPiLow);
+  const double y = (fma(-0.25, quarter, turn) + low) * kTwoPi, z = y * y;
   double s = 1.0 / 6227020800.0, c = 1.0 / 479001600.0;    // 1 / 13!, 1 / 12!
   s = fma(s, z, -1.0 / 39916800.0);
   c = fma(c, z, -1.0 / 3628800.0);
@@ -162,7 +165,7 @@ __global__ void __launch_bounds__(kThreads) gdn_rope_k(RopeArgs p) {
   __syncthreads();
   for (int i = threadIdx.x; i < tokens * pairs; i += kThreads) {
     const int t = i / pairs;
-    turns[i] = turn_of(pos_of[t] * p.inv_freq[i - t * pairs], (double)p.factor);
+    turns[i] = turn_of(pos_of[t], p.inv_freq[i - t * pairs], (double)p.factor);
   }
   __syncthreads();
 

@@ -87,8 +87,9 @@ typedef struct gdn_kv_cache {
  * the leading rotary_dim = r elements of a head are
  *   GDN_ROPE_HALF         (i, i + r / 2)
  *   GDN_ROPE_INTERLEAVED  (2 i, 2 i + 1)           i = 0 .. r / 2 - 1
- * and the elements from r on are left as they are. Frequencies are doubles and the angle is formed and
- * reduced in double precision, so far positions lose nothing; the rotation itself
+ * and the elements from r on are left as they are. Frequencies are doubles; the angle is
+ * formed and reduced without rounding it, so that far positions lose nothing, and its
+ * cos and sin times the factor are rounded once to FP32. The rotation itself
  * runs in FP32 and is rounded once to io. */
 typedef enum gdn_rope_layout { GDN_ROPE_HALF = 0, GDN_ROPE_INTERLEAVED = 1 } gdn_rope_layout;
 
