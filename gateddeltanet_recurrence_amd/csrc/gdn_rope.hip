@@ -19,6 +19,18 @@ namespace {
 
 constexpr int kThreads = 256;
 
+// A launch has fewer than 2^32 work-items in a dimension (more are dropped without an error): workgroups past 2^23
+// go to the second one. The first token of this workgroup, at most N.
+constexpr int kGridShift = 23;
+dim3 grid_of(int64_t N, int tokens_per_block) {
+  const int64_t blocks = (N + tokens_per_block - 1) / tokens_per_block, wide = (int64_t)1 << kGridShift;
+  return dim3((unsigned)(blocks < wide ? blocks : wide), (unsigned)((blocks + wide - 1) >> kGridShift));
+}
+__device__ __forceinline__ int first_token(int N, int tokens_per_block) {
+  const unsigned n0 = ((blockIdx.y << kGridShift) + blockIdx.x) * (unsigned)tokens_per_block;   // below 2^31 + 2^27
+  return (int)min(n0, (unsigned)N);
+}
+
 // A 16-byte vector of io elements.
 template <typename IO> struct Vec;
 template <> struct Vec<_Float16> {
@@ -147,7 +159,7 @@ __global__ void __launch_bounds__(kThreads) gdn_rope_k(RopeArgs p) {
   __shared__ double pos_of[kRopeMaxTokens];
   extern __shared__ float2 turns[];        // [tokens][rot / 2] cos and sin
 
-  const int n0 = (int)blockIdx.x * p.tokens_per_block;
+  const int n0 = first_token(p.N, p.tokens_per_block);
   const int tokens = min(p.tokens_per_block, (CACHE ? row_count(p.rows) : p.N) - n0);
   if (tokens <= 0) return;                 // uniform across the workgroup
   const int pairs = p.rot >> 1;
@@ -276,7 +288,7 @@ __global__ void __launch_bounds__(kThreads) gdn_kv_read_k(ReadArgs p) {
   constexpr int kHeadStep = kThreads / E;
   typedef typename Vec<IO>::type vec_t;
   __shared__ int64_t row_of[kRopeMaxTokens];
-  const int n0 = (int)blockIdx.x * p.tokens_per_block;
+  const int n0 = first_token(p.rows.N, p.tokens_per_block);
   const int tokens = min(p.tokens_per_block, row_count(p.rows) - n0);
   if (tokens <= 0) return;
   int r = request_of(p.rows, n0);
@@ -329,7 +341,7 @@ __global__ void __launch_bounds__(kThreads) gdn_kv_read_k(ReadArgs p) {
 
 template <typename IO, int D>
 hipError_t launch_rope_d(const RopeArgs& p, hipStream_t stream) {
-  const dim3 grid((unsigned)((p.N + p.tokens_per_block - 1) / p.tokens_per_block));
+  const dim3 grid = grid_of(p.N, p.tokens_per_block);
   const size_t lds = (size_t)p.tokens_per_block * (p.rot / 2) * sizeof(float2);
   if (!p.to_cache) {
     hipLaunchKernelGGL((gdn_rope_k<IO, D, false, false>), grid, dim3(kThreads), lds, stream, p);
@@ -346,7 +358,7 @@ hipError_t launch_rope_d(const RopeArgs& p, hipStream_t stream) {
 
 template <typename IO, int D>
 hipError_t launch_read_d(const ReadArgs& p, hipStream_t stream) {
-  const dim3 grid((unsigned)((p.rows.N + p.tokens_per_block - 1) / p.tokens_per_block));
+  const dim3 grid = grid_of(p.rows.N, p.tokens_per_block);
   if (!p.cache.e4m3) {
     hipLaunchKernelGGL((gdn_kv_read_k<IO, D, false>), grid, dim3(kThreads), 0, stream, p);
   } else {
