@@ -265,12 +265,11 @@ __device__ __forceinline__ void note_segment(const SplitArgs& sp, const Segment&
   sp.notes[2 * x.note + 1] = int4{x.s.start, x.h, x.s.T, 0};
 }
 
-// A lane's row of a tile of `rows` rows from row0 on, and the positions that the
-// tile's rows attend: [lo, hi) of the lane's, within [lo_min, hi_max); every row
-// attends [lo_max, hi_min).
+// Row n of a segment of `rows` rows from row0 on, and the positions that it attends:
+// [lo, hi); every row of the segment attends [lo_max, hi_min).
 struct Rows {
   int j, head;                                             // token of the request, head of the group
-  int lo, hi, lo_min, lo_max, hi_min, hi_max;
+  int lo, hi, lo_max, hi_min;
 };
 
 __device__ __forceinline__ Rows rows_of(const AttnArgs& p, const Plan& s, int row0, int rows, int n) {
@@ -283,11 +282,9 @@ __device__ __forceinline__ Rows rows_of(const AttnArgs& p, const Plan& s, int ro
   const int past = before + x.j, past0 = before + token_of(p, s, row0), past1 = before + token_of(p, s, last);
   x.hi = n < rows ? clamp_pos(past, cap) : 0;
   x.hi_min = clamp_pos(past0, cap);
-  x.hi_max = clamp_pos(past1, cap);
-  x.lo = x.lo_min = x.lo_max = 0;
+  x.lo = x.lo_max = 0;
   if (p.window > 0) {
     x.lo = window_start(p, past, cap);
-    x.lo_min = window_start(p, past0, cap);
     x.lo_max = window_start(p, past1, cap);
   }
   return x;
