@@ -800,7 +800,9 @@ class KVCache:
     k_pages, v_pages [num_pages, Hk, page_size, D] float16 or float32; for the 8-bit
     format float8_e4m3fn or uint8, with k_scales, v_scales [num_pages, Hk, page_size]
     uint8 (the exponent bytes; I/O is then float16). page_table [R, max_pages] int32;
-    page_table_host an optional host mirror, checked on every call.
+    page_table_host an optional host mirror, checked on every call: a contiguous int32
+    array or CPU tensor is read in place, so that a program can change it along with
+    page_table; anything else is copied once, here.
     """
 
     def __init__(self, k_pages, v_pages, page_table, *, k_scales=None, v_scales=None, page_table_host=None):

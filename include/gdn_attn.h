@@ -56,7 +56,9 @@ extern "C" {
  *                  power of two with a <= 448 * 2^(s - 127), and code = x / 2^(s - 127)
  *                  rounded to nearest even; s = 0 when no finite x is nonzero, and a
  *                  non-finite x is stored as NaN. A power of two makes the division and
- *                  the way back exact, so a code is the only rounding.
+ *                  the way back exact, so a code is the only rounding. Rows of FP16 have
+ *                  s = 0 or 95 .. 135, and no other byte may stand beside a position that
+ *                  is attended (attention takes a value's byte below 94 as 94).
  *
  * A page number outside [0, num_pages) (e.g. -1) names no page: nothing is
  * written there, reads give zeros, and attention leaves those positions out.
@@ -185,7 +187,13 @@ typedef struct gdn_kv_tensors {
                                     GDN_ERR_CAPACITY (T_r is checked where the host
                                     knows it). Besides the checks it only guides how
                                     the work is split: a captured call may be replayed
-                                    with other lengths                              */
+                                    with other lengths. The split stays the captured
+                                    one, so gdn_attn_forward captured with short
+                                    lengths is slow over far longer ones (one request,
+                                    300 positions at capture and 131,072 at replay, 8
+                                    key heads of 128 FP16: 1.4 ms instead of 92 us):
+                                    capture it with the longest to come, or with NULL,
+                                    which counts as the table's length               */
   const void* q;                 /* with rotary_dim > 0 and Hq > 0: rotated into q_out */
   void* q_out;                   /* io [N, Hq, D] dense, or q itself (in place)      */
   const int32_t* positions;      /* device, i32 [N]: rotary positions, or NULL for
@@ -240,6 +248,9 @@ typedef struct gdn_attn_tensors {
  * Any number of tokens per request is taken; the kernels are made for decode and
  * verify, where the cache is read once for up to 32 rows (tokens x Hq / Hk) and, where
  * most requests have the same number of up to 256, mostly from the L2 for the rest.
+ * Prompts are such segments of 32 rows, each of which walks the request's positions up
+ * to its own from the first that any token of the call attends, so a long prompt is far
+ * from the matrix cores' rate, and a window does not make it faster.
  * (N + R) Hq D / 64 is at most 2^30, else GDN_ERR_SHAPE.
  * The workspace (gdn_attn_workspace_bytes() bytes, disjoint from every tensor, 16-byte
  * aligned) needs no initial value; calls that overlap in time, and captured graphs

@@ -91,3 +91,19 @@ def test_a_library_without_a_version_says_rebuild(monkeypatch, tmp_path):
     monkeypatch.setattr(ctypes, "CDLL", lambda p: object())
     with pytest.raises(binding.LibraryNotBuilt, match="rebuild it"):
         binding.lib()
+
+
+def test_int32_mirrors_are_read_in_place():
+    """A mirror that the program changes later is the one that the next call's checks see."""
+    import numpy as np
+    a = np.arange(12, dtype=np.int32).reshape(3, 4)
+    kept, at = binding._host_i32(a)
+    assert at == a.ctypes.data and np.shares_memory(kept, a)
+    t = torch.arange(12, dtype=torch.int32).view(3, 4)
+    kept, at = binding._host_i32(t)
+    assert at == t.data_ptr()
+    t[1, 2] = 77
+    assert kept[1, 2] == 77
+    for copied in (a.astype(np.int64), a[:, :2], [[1, 2], [3, 4]]):
+        kept, at = binding._host_i32(copied)
+        assert kept.dtype == np.int32 and at == kept.ctypes.data and np.array_equal(kept, copied)
