@@ -28,7 +28,7 @@ ABI_VERSION = 7          # the struct layouts below match this version of includ
 CONV_SILU, CONV_NONE = 0, 1
 ROPE_HALF, ROPE_INTERLEAVED = 0, 1
 ROPE_SCALING_NONE, ROPE_SCALING_LINEAR, ROPE_SCALING_NTK, ROPE_SCALING_YARN = 0, 1, 2, 3
-CACHE_IO, CACHE_E4M3 = 0, 1
+CACHE_IO, CACHE_E4M3, CACHE_E2M1 = 0, 1, 4
 
 
 class LibraryNotBuilt(RuntimeError):
@@ -121,6 +121,26 @@ class GdnAttnTensors(ctypes.Structure):
                                                "output")]
 
 
+class GdnSelectParams(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("num_tokens", "num_reqs", "num_q_heads", "list_len", "first_pages",
+                                              "newest_pages", "q_stride")]
+
+
+class GdnSelectTensors(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("q", "cu_seqlens", "cu_seqlens_host", "seq_lens", "seq_lens_host",
+                                               "bounds", "pages", "counts")]
+
+
+class GdnSparseParams(ctypes.Structure):
+    _fields_ = [("num_tokens", ctypes.c_int32), ("num_reqs", ctypes.c_int32), ("num_q_heads", ctypes.c_int32),
+                ("list_len", ctypes.c_int32), ("scale", ctypes.c_float), ("q_stride", ctypes.c_int32)]
+
+
+class GdnSparseTensors(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("q", "cu_seqlens", "cu_seqlens_host", "seq_lens", "seq_lens_host",
+                                               "pages", "counts", "output")]
+
+
 def _packer(cls):
     """cls's fields in order -> the bytes of such a struct. Called for every decode step, this
     takes 0.07 us where making the ctypes object takes 0.2."""
@@ -134,6 +154,8 @@ def _packer(cls):
 _rope_params, _rope_tensors = _packer(GdnRopeParams), _packer(GdnRopeTensors)
 _kv_params, _kv_tensors = _packer(GdnKvParams), _packer(GdnKvTensors)
 _attn_params, _attn_tensors = _packer(GdnAttnParams), _packer(GdnAttnTensors)
+_select_params, _select_tensors = _packer(GdnSelectParams), _packer(GdnSelectTensors)
+_sparse_params, _sparse_tensors = _packer(GdnSparseParams), _packer(GdnSparseTensors)
 
 _lib = None
 _calls = None            # the attention layer's calls, taking packed structs
@@ -194,14 +216,25 @@ def _declare(L):
     L.gdn_attn_forward.argtypes = [ctypes.POINTER(GdnAttnParams), ctypes.POINTER(GdnAttnTensors), cp, vp,
                                    ctypes.c_size_t, vp]
     L.gdn_attn_workspace_bytes.argtypes = [ctypes.POINTER(GdnAttnParams), cp, ctypes.POINTER(ctypes.c_size_t)]
+    L.gdn_kv_bounds.argtypes = [ctypes.POINTER(GdnKvParams), ctypes.POINTER(GdnKvTensors), cp, vp, vp]
+    L.gdn_attn_select.argtypes = [ctypes.POINTER(GdnSelectParams), ctypes.POINTER(GdnSelectTensors), cp, vp,
+                                  ctypes.c_size_t, vp]
+    L.gdn_attn_sparse_forward.argtypes = [ctypes.POINTER(GdnSparseParams), ctypes.POINTER(GdnSparseTensors), cp, vp,
+                                          ctypes.c_size_t, vp]
+    L.gdn_attn_select_workspace_bytes.argtypes = [ctypes.POINTER(GdnSelectParams), cp, ctypes.POINTER(ctypes.c_size_t)]
+    L.gdn_attn_sparse_workspace_bytes.argtypes = [ctypes.POINTER(GdnSparseParams), cp, ctypes.POINTER(ctypes.c_size_t)]
     for fn in (L.gdn_rope_frequencies, L.gdn_rope_forward, L.gdn_kv_write, L.gdn_kv_read, L.gdn_attn_forward,
-               L.gdn_attn_workspace_bytes):
+               L.gdn_attn_workspace_bytes, L.gdn_kv_bounds, L.gdn_attn_select, L.gdn_attn_sparse_forward,
+               L.gdn_attn_select_workspace_bytes, L.gdn_attn_sparse_workspace_bytes):
         fn.restype = ctypes.c_int
     chars = ctypes.c_char_p
-    calls = {n: L[n] for n in ("gdn_rope_forward", "gdn_kv_write", "gdn_kv_read", "gdn_attn_forward")}
+    calls = {n: L[n] for n in ("gdn_rope_forward", "gdn_kv_write", "gdn_kv_read", "gdn_attn_forward", "gdn_kv_bounds",
+                               "gdn_attn_select", "gdn_attn_sparse_forward")}
     calls["gdn_rope_forward"].argtypes = [chars, chars, vp]
     calls["gdn_kv_write"].argtypes = calls["gdn_kv_read"].argtypes = [chars, chars, vp, vp]
-    calls["gdn_attn_forward"].argtypes = [chars, chars, vp, vp, ctypes.c_size_t, vp]
+    for n in ("gdn_attn_forward", "gdn_attn_select", "gdn_attn_sparse_forward"):
+        calls[n].argtypes = [chars, chars, vp, vp, ctypes.c_size_t, vp]
+    calls["gdn_kv_bounds"].argtypes = [chars, chars, vp, vp, vp]
     for fn in calls.values():
         fn.restype = ctypes.c_int
     L.gdn_strerror.argtypes = [ctypes.c_int]
@@ -799,7 +832,9 @@ class KVCache:
 
     k_pages, v_pages [num_pages, Hk, page_size, D] float16 or float32; for the 8-bit
     format float8_e4m3fn or uint8, with k_scales, v_scales [num_pages, Hk, page_size]
-    uint8 (the exponent bytes; I/O is then float16). page_table [R, max_pages] int32;
+    uint8 (the exponent bytes; I/O is then float16). For the 4-bit format k_pages, v_pages
+    are [num_pages, Hk, page_size, D / 2] uint8, two e2m1 codes a byte, and the scales
+    [num_pages, Hk, D / 32, page_size]. page_table [R, max_pages] int32;
     page_table_host an optional host mirror, checked on every call: a contiguous int32
     array or CPU tensor is read in place, so that a program can change it along with
     page_table; anything else is copied once, here.
@@ -810,19 +845,26 @@ class KVCache:
         if k_pages.dim() != 4 or page_table.dim() != 2:
             raise ValueError("k_pages must be [num_pages, Hk, page_size, D] and page_table [R, max_pages]")
         P, Hk, page_size, D = k_pages.shape
-        self.e4m3 = k_scales is not None or v_scales is not None
-        if self.e4m3:
+        row = D                                              # a row's columns in the pages
+        self.format, self.io_dtype = CACHE_IO, k_pages.dtype
+        if k_scales is not None or v_scales is not None:
             if k_scales is None or v_scales is None:
-                raise ValueError("the 8-bit format needs k_scales and v_scales")
-            if k_pages.dtype not in (torch.uint8, torch.float8_e4m3fn):
-                raise ValueError(f"k_pages: dtype {k_pages.dtype} is not an 8-bit cache")
-            _need(k_scales, "k_scales", (P, Hk, page_size), torch.uint8)
-            _need(v_scales, "v_scales", (P, Hk, page_size), torch.uint8)
+                raise ValueError("the 8-bit and 4-bit formats need k_scales and v_scales")
             self.io_dtype = torch.float16
-        else:
-            self.io_dtype = k_pages.dtype
-        _need(k_pages, "k_pages", (P, Hk, page_size, D))
-        _need(v_pages, "v_pages", (P, Hk, page_size, D), k_pages.dtype)
+            if k_scales.dim() == 4:
+                self.format, D = CACHE_E2M1, 2 * D
+                if k_pages.dtype is not torch.uint8:
+                    raise ValueError(f"k_pages: dtype {k_pages.dtype} is not a 4-bit cache (uint8)")
+                scales = (P, Hk, D // 32, page_size)
+            else:
+                self.format, scales = CACHE_E4M3, (P, Hk, page_size)
+                if k_pages.dtype not in (torch.uint8, torch.float8_e4m3fn):
+                    raise ValueError(f"k_pages: dtype {k_pages.dtype} is not an 8-bit cache")
+            _need(k_scales, "k_scales", scales, torch.uint8)
+            _need(v_scales, "v_scales", scales, torch.uint8)
+        self.e4m3 = self.format == CACHE_E4M3
+        _need(k_pages, "k_pages", (P, Hk, page_size, row))
+        _need(v_pages, "v_pages", (P, Hk, page_size, row), k_pages.dtype)
         _need(page_table, "page_table", tuple(page_table.shape), torch.int32)
         for x, name in ((v_pages, "v_pages"), (page_table, "page_table"), (k_scales, "k_scales"),
                         (v_scales, "v_scales")):
@@ -833,10 +875,11 @@ class KVCache:
             raise ValueError("page_table_host must have page_table's shape")
         self.num_reqs, max_pages = page_table.shape
         self.num_kv_heads, self.head_dim, self.index = Hk, D, k_pages.get_device()
+        self.num_pages, self.page_size = P, page_size
         self._keep = (k_pages, v_pages, k_scales, v_scales, page_table, host)
         self.struct = GdnKvCache(_ptr(k_pages), _ptr(v_pages), _ptr(k_scales), _ptr(v_scales), _ptr(page_table),
                                  host_ptr, P, page_size, max_pages, Hk, D, _io_code(self.io_dtype),
-                                 CACHE_E4M3 if self.e4m3 else CACHE_IO)
+                                 self.format)
         self.address = ctypes.addressof(self.struct)
 
 
@@ -1071,4 +1114,126 @@ def gdn_attn_forward(q, cache: KVCache, seq_lens, cu_seqlens, output, *, scale: 
     del keep
     if check and st != GDN_OK:
         raise GDNError(st, "gdn_attn_forward")
+    return st
+
+
+def gdn_kv_bounds(bounds, cache: KVCache, seq_lens, cu_seqlens=None, *, num_tokens: int, num_reqs: Optional[int] = None,
+                  cu_seqlens_host=None, seq_lens_host=None, stream=None, check: bool = True) -> int:
+    """gdn_kv_bounds of include/gdn_attn.h: the lowest and highest key, channel by channel, of
+    every page that holds one of the newest num_tokens tokens (as in gdn_kv_write) into bounds
+    [num_pages, Hk, 2, D] (the cache's I/O type); returns the status."""
+    index = cache.index
+    _page_bounds(bounds, cache, index)
+    R, lens, cu, len_h, cu_h, keep = _cache_rows(cache, seq_lens, cu_seqlens, num_reqs, cu_seqlens_host,
+                                                 seq_lens_host)
+    st = _call("gdn_kv_bounds")(_kv_params(num_tokens, R, 0, 0, 0, 0.0, 0, 0, 0),
+                                _kv_tensors(0, 0, cu, cu_h, lens, len_h, 0, 0, 0, 0), cache.address, bounds.data_ptr(),
+                                _stream_handle(stream, index))
+    del keep
+    if check and st != GDN_OK:
+        raise GDNError(st, "gdn_kv_bounds")
+    return st
+
+
+def _page_bounds(x, cache, index):
+    if x.shape != (cache.num_pages, cache.num_kv_heads, 2, cache.head_dim) or x.dtype is not cache.io_dtype or \
+            x.get_device() != index or not x.is_contiguous():
+        raise ValueError("bounds must be contiguous [num_pages, Hk, 2, D] in the cache's I/O type, on its GPU")
+
+
+def _page_lists(pages, counts, N, cache, index):
+    """K of lists [N, Hk, K] and their counts [N]."""
+    shape, i32 = pages.shape, _torch().int32
+    if len(shape) != 3 or shape[0] != N or shape[1] != cache.num_kv_heads or pages.dtype is not i32 or \
+            pages.get_device() != index or not pages.is_contiguous():
+        raise ValueError(f"pages must be a contiguous int32 [{N}, {cache.num_kv_heads}, K] on GPU {index}")
+    if counts is not None:
+        _int_vector(counts, "counts", N, index)
+    return shape[2]
+
+
+def _workspace(workspace, index):
+    if workspace is None:
+        return None, 0
+    if workspace.get_device() != index or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on the cache's GPU")
+    return workspace.data_ptr(), workspace.nbytes
+
+
+def gdn_attn_select_workspace_bytes(N: int, R: int, Hq: int, K: int, cache: KVCache) -> int:
+    """Workspace bytes gdn_attn_select needs for these sizes, whatever the lengths."""
+    params = GdnSelectParams(int(N), int(R), int(Hq), int(K), 0, 0, 0)
+    out = ctypes.c_size_t(0)
+    st = lib().gdn_attn_select_workspace_bytes(ctypes.byref(params), ctypes.byref(cache.struct), ctypes.byref(out))
+    if st != GDN_OK:
+        raise GDNError(st, "gdn_attn_select_workspace_bytes")
+    return int(out.value)
+
+
+def gdn_attn_select(q, bounds, cache: KVCache, seq_lens, cu_seqlens, pages, counts, *, first_pages: int = 1,
+                    newest_pages: int = 1, num_reqs: Optional[int] = None, cu_seqlens_host=None, seq_lens_host=None,
+                    workspace=None, stream=None, check: bool = True) -> int:
+    """gdn_attn_select of include/gdn_attn.h on torch tensors; returns the status.
+
+    q [N, Hq, D] in the cache's I/O type (the token dimension may be strided); bounds
+    [num_pages, Hk, 2, D] of gdn_kv_bounds; pages [N, Hk, K] int32 receives the selected
+    entries of the page table, ascending and -1 behind them, counts [N] int32 their number.
+    The first first_pages and the newest newest_pages are always in. workspace: a uint8 GPU
+    tensor of gdn_attn_select_workspace_bytes().
+    """
+    index, io = cache.index, cache.io_dtype
+    N, Hq = q.shape[0], q.shape[1]
+    qs = _token_rows(q, "q", Hq, cache.head_dim, io, index)
+    _page_bounds(bounds, cache, index)
+    K = _page_lists(pages, counts, N, cache, index)
+    ws, ws_bytes = _workspace(workspace, index)
+    R, lens, cu, len_h, cu_h, keep = _cache_rows(cache, seq_lens, cu_seqlens, num_reqs, cu_seqlens_host,
+                                                 seq_lens_host)
+    st = _call("gdn_attn_select")(_select_params(N, R, Hq, K, first_pages, newest_pages, qs),
+                                  _select_tensors(q.data_ptr(), cu, cu_h, lens, len_h, bounds.data_ptr(),
+                                                  pages.data_ptr(), counts.data_ptr()),
+                                  cache.address, ws, ws_bytes, _stream_handle(stream, index))
+    del keep
+    if check and st != GDN_OK:
+        raise GDNError(st, "gdn_attn_select")
+    return st
+
+
+def gdn_attn_sparse_workspace_bytes(N: int, R: int, Hq: int, K: int, cache: KVCache) -> int:
+    """Workspace bytes gdn_attn_sparse_forward needs for these sizes, whatever the lists."""
+    params = GdnSparseParams(int(N), int(R), int(Hq), int(K), 0.0, 0)
+    out = ctypes.c_size_t(0)
+    st = lib().gdn_attn_sparse_workspace_bytes(ctypes.byref(params), ctypes.byref(cache.struct), ctypes.byref(out))
+    if st != GDN_OK:
+        raise GDNError(st, "gdn_attn_sparse_workspace_bytes")
+    return int(out.value)
+
+
+def gdn_attn_sparse_forward(q, cache: KVCache, seq_lens, cu_seqlens, pages, counts, output, *, scale: float = 0.0,
+                            num_reqs: Optional[int] = None, cu_seqlens_host=None, seq_lens_host=None, workspace=None,
+                            stream=None, check: bool = True) -> int:
+    """gdn_attn_sparse_forward of include/gdn_attn.h on torch tensors; returns the status.
+
+    q, output, seq_lens and cu_seqlens as in gdn_attn_forward; pages [N, Hk, K] int32 the
+    entries of its request's page table that each token and key head attends, counts [N]
+    int32 how many of them (None: K); workspace a uint8 GPU tensor of
+    gdn_attn_sparse_workspace_bytes().
+    """
+    index, io = cache.index, cache.io_dtype
+    shape = q.shape
+    N, Hq = shape[0], shape[1]
+    qs = _token_rows(q, "q", Hq, cache.head_dim, io, index)
+    if output.shape != shape or output.dtype is not io or output.get_device() != index or not output.is_contiguous():
+        raise ValueError("output must be contiguous and have q's shape, type and device")
+    K = _page_lists(pages, counts, N, cache, index)
+    ws, ws_bytes = _workspace(workspace, index)
+    R, lens, cu, len_h, cu_h, keep = _cache_rows(cache, seq_lens, cu_seqlens, num_reqs, cu_seqlens_host,
+                                                 seq_lens_host)
+    st = _call("gdn_attn_sparse_forward")(_sparse_params(N, R, Hq, K, scale, qs),
+                                          _sparse_tensors(q.data_ptr(), cu, cu_h, lens, len_h, pages.data_ptr(),
+                                                          0 if counts is None else counts.data_ptr(), output.data_ptr()),
+                                          cache.address, ws, ws_bytes, _stream_handle(stream, index))
+    del keep
+    if check and st != GDN_OK:
+        raise GDNError(st, "gdn_attn_sparse_forward")
     return st

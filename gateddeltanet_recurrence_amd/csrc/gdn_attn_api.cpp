@@ -63,18 +63,18 @@ int64_t token_stride(int32_t given, int64_t heads, int64_t D) {
 int check_cache(const gdn_kv_cache* c, bool pointers) {
   if (c == nullptr) return GDN_ERR_NULL;
   if (c->io_dtype != GDN_F32 && c->io_dtype != GDN_F16) return GDN_ERR_DTYPE;
-  if (c->format != GDN_CACHE_IO && c->format != GDN_CACHE_E4M3) return GDN_ERR_DTYPE;
-  if (c->format == GDN_CACHE_E4M3 && c->io_dtype != GDN_F16) return GDN_ERR_DTYPE;
+  if (c->format != GDN_CACHE_IO && c->format != GDN_CACHE_E4M3 && c->format != GDN_CACHE_E2M1) return GDN_ERR_DTYPE;
+  if (c->format != GDN_CACHE_IO && c->io_dtype != GDN_F16) return GDN_ERR_DTYPE;
   if (c->num_pages < 1 || c->max_pages < 1 || c->num_kv_heads < 1) return GDN_ERR_SHAPE;
   if (!page_size_ok(c->page_size) || !head_dim_ok(c->head_dim)) return GDN_ERR_SHAPE;
   if ((int64_t)c->max_pages * c->page_size > kMaxPositions) return GDN_ERR_SHAPE;
   // a pool's rows are counted in 64 bits; its bytes must fit a size_t with room to spare
   if ((double)c->num_pages * c->num_kv_heads * c->page_size * c->head_dim > 4e15) return GDN_ERR_SHAPE;
   if (!pointers) return GDN_OK;
-  const bool e4m3 = c->format == GDN_CACHE_E4M3;
+  const bool coded = c->format != GDN_CACHE_IO;
   if (c->k_pages == nullptr || c->v_pages == nullptr || c->page_table == nullptr) return GDN_ERR_NULL;
-  if (e4m3 && (c->k_scales == nullptr || c->v_scales == nullptr)) return GDN_ERR_NULL;
-  if (!e4m3 && (c->k_scales != nullptr || c->v_scales != nullptr)) return GDN_ERR_SHAPE;
+  if (coded && (c->k_scales == nullptr || c->v_scales == nullptr)) return GDN_ERR_NULL;
+  if (!coded && (c->k_scales != nullptr || c->v_scales != nullptr)) return GDN_ERR_SHAPE;
   for (const void* ptr : {c->k_pages, c->v_pages, (void*)c->k_scales, (void*)c->v_scales})
     if (ptr != nullptr && !aligned16(ptr)) return GDN_ERR_SHAPE;
   return GDN_OK;
@@ -83,13 +83,14 @@ int check_cache(const gdn_kv_cache* c, bool pointers) {
 struct CacheSpans {
   Span pages[2], scales[2], table;
   CacheSpans(const gdn_kv_cache& c, int64_t R) {
-    const bool e4m3 = c.format == GDN_CACHE_E4M3;
+    const bool coded = c.format != GDN_CACHE_IO, four = c.format == GDN_CACHE_E2M1;
     const size_t rows = (size_t)c.num_pages * c.num_kv_heads * c.page_size;
-    const size_t bytes = rows * c.head_dim * (e4m3 ? 1 : io_bytes(c.io_dtype));
+    const size_t bytes = four ? rows * c.head_dim / 2 : rows * c.head_dim * (coded ? 1 : io_bytes(c.io_dtype));
+    const size_t scale_bytes = four ? rows * (c.head_dim / 32) : coded ? rows : 0;
     pages[0] = Span(c.k_pages, bytes);
     pages[1] = Span(c.v_pages, bytes);
-    scales[0] = Span(c.k_scales, e4m3 ? rows : 0);
-    scales[1] = Span(c.v_scales, e4m3 ? rows : 0);
+    scales[0] = Span(c.k_scales, scale_bytes);
+    scales[1] = Span(c.v_scales, scale_bytes);
     table = Span(c.page_table, (size_t)R * c.max_pages * 4);
   }
   bool overlap_each_other() const {
@@ -161,7 +162,7 @@ gdn::CacheArgs cache_args(const gdn_kv_cache& c) {
   gdn::CacheArgs a{};
   a.k = c.k_pages; a.v = c.v_pages; a.k_scales = c.k_scales; a.v_scales = c.v_scales; a.table = c.page_table;
   a.num_pages = c.num_pages; a.max_pages = c.max_pages; a.Hk = c.num_kv_heads; a.D = c.head_dim;
-  a.e4m3 = c.format == GDN_CACHE_E4M3 ? 1 : 0;
+  a.format = c.format;
   while ((1 << a.page_shift) < c.page_size) ++a.page_shift;
   return a;
 }
@@ -183,6 +184,15 @@ int tokens_per_block(int64_t N, int64_t heads, int64_t D, size_t io) {
   const int64_t items = heads * D * (int64_t)io / 32;
   const int64_t t = std::min<int64_t>(512 / std::max<int64_t>(items, 1), N / 1024);
   return (int)std::min<int64_t>(std::max<int64_t>(t, 1), gdn::kRopeMaxTokens);
+}
+
+// The most tokens of a request, as far as the host knows.
+int64_t most_tokens(const Rows& w) {
+  if (w.dense()) return w.dense_len();
+  if (w.cu_host == nullptr) return w.N;
+  int64_t tokens = 0;
+  for (int64_t r = 0; r < w.R; ++r) tokens = std::max(tokens, w.tokens(r));
+  return tokens;
 }
 
 int status_of(hipError_t err) { return err == hipSuccess ? GDN_OK : GDN_ERR_HIP; }
@@ -374,7 +384,8 @@ int gdn_attn_workspace_bytes(const gdn_attn_params* p, const gdn_kv_cache* c, si
   const int st = check_attn(p, c, &qs);
   if (st != GDN_OK) return st;
   if (bytes == nullptr) return GDN_ERR_NULL;
-  *bytes = gdn::attn_workspace_bytes(p->num_tokens, p->num_reqs, p->num_q_heads, c->num_kv_heads, c->head_dim);
+  *bytes = gdn::attn_workspace_bytes(p->num_tokens, p->num_reqs, p->num_q_heads, c->num_kv_heads, c->head_dim,
+                                     c->format);
   return GDN_OK;
 }
 
@@ -394,7 +405,7 @@ int gdn_attn_forward(const gdn_attn_params* p, const gdn_attn_tensors* t, const 
   if (N == 0) return GDN_OK;
   if (t->q == nullptr || t->output == nullptr) return GDN_ERR_NULL;
   if (!aligned16(t->q) || !aligned16(t->output)) return GDN_ERR_SHAPE;
-  const size_t need = gdn::attn_workspace_bytes(N, R, (int)Hq, (int)Hk, (int)D);
+  const size_t need = gdn::attn_workspace_bytes(N, R, (int)Hq, (int)Hk, (int)D, c->format);
   if (need > 0 && (workspace == nullptr || workspace_bytes < need || !aligned16(workspace))) return GDN_ERR_WORKSPACE;
   const size_t io = io_bytes(c->io_dtype);
   const RowSpan q(t->q, Hq * D * io, qs * io, N);
@@ -410,13 +421,8 @@ int gdn_attn_forward(const gdn_attn_params* p, const gdn_attn_tensors* t, const 
   a.scale = p->scale > 0.f ? p->scale : 1.0f / std::sqrt((float)D);
   // the most tokens of a request, and the most positions one attends, as far as they are known here: a
   // mirror's, else what the call and the table hold
-  int64_t tokens = N, longest = (int64_t)c->max_pages * c->page_size;
-  if (w.dense()) tokens = w.dense_len();
-  if (w.cu_host != nullptr) {
-    tokens = 0;
-    for (int64_t r = 0; r < R; ++r) tokens = std::max(tokens, w.tokens(r));
-  }
-  int64_t sum = 0;
+  const int64_t tokens = most_tokens(w);
+  int64_t longest = (int64_t)c->max_pages * c->page_size, sum = 0;
   if (p->window > 0) longest = std::min(longest, (int64_t)p->window + tokens);
   if (w.lens_host != nullptr) {
     const int64_t most = longest;
@@ -433,6 +439,195 @@ int gdn_attn_forward(const gdn_attn_params* p, const gdn_attn_tensors* t, const 
   a.cache = cache_args(*c);
   a.rows = row_args(w);
   return status_of(gdn::launch_attn(a, c->io_dtype, workspace, static_cast<hipStream_t>(stream)));
+}
+
+int gdn_kv_bounds(const gdn_kv_params* p, const gdn_kv_tensors* t, const gdn_kv_cache* c, void* bounds, void* stream) {
+  if (p == nullptr || t == nullptr) return GDN_ERR_NULL;
+  int st = check_cache(c, false);
+  if (st != GDN_OK) return st;
+  const int64_t N = p->num_tokens, R = p->num_reqs, Hk = c->num_kv_heads, D = c->head_dim;
+  if (N < 0 || R < 0 || p->num_q_heads != 0 || p->rotary_dim != 0) return GDN_ERR_SHAPE;
+  if (p->q_stride != 0 || p->k_stride != 0 || p->v_stride != 0) return GDN_ERR_SHAPE;
+  if (2 * Hk * D > std::numeric_limits<int32_t>::max()) return GDN_ERR_SHAPE;
+  if (R == 0) return N == 0 ? GDN_OK : GDN_ERR_SHAPE;
+  st = check_cache(c, true);
+  if (st != GDN_OK) return st;
+  const Rows w{N, R, t->cu_seqlens, t->cu_seqlens_host, t->seq_lens, t->seq_lens_host};
+  st = check_rows(w, *c);
+  if (st != GDN_OK) return st;
+  if (N == 0) return GDN_OK;
+  if (bounds == nullptr) return GDN_ERR_NULL;
+  if (!aligned16(bounds)) return GDN_ERR_SHAPE;
+  const Span out(bounds, (size_t)c->num_pages * Hk * 2 * D * io_bytes(c->io_dtype));
+  const CacheSpans cs(*c, R);
+  if (cs.overlap(out) || out.overlaps(Span(t->cu_seqlens, (R + 1) * 4)) || out.overlaps(Span(t->seq_lens, R * 4)))
+    return GDN_ERR_ALIAS;
+  if (pages_collide(w, *c)) return GDN_ERR_ALIAS;
+  gdn::BoundsArgs a{};
+  a.bounds = bounds;
+  // a page holds 16 tokens at least: of a prompt's, one workgroup looks at 16, of a decode step's at one
+  a.tokens_per_block = N > 4096 ? 16 : 1;
+  a.cache = cache_args(*c);
+  a.rows = row_args(w);
+  return status_of(gdn::launch_bounds(a, c->io_dtype, static_cast<hipStream_t>(stream)));
+}
+
+// What gdn_attn_select and gdn_attn_sparse_forward, and their workspace queries, check alike.
+static int check_lists(int64_t N, int64_t R, int64_t Hq, int64_t K, int32_t stride, const gdn_kv_cache* c, int64_t* q_stride) {
+  const int st = check_cache(c, false);
+  if (st != GDN_OK) return st;
+  const int64_t Hk = c->num_kv_heads, D = c->head_dim;
+  if (N < 0 || R < 0 || Hq < 1 || Hq % Hk != 0 || K < 1 || K * c->page_size > kMaxPositions) return GDN_ERR_SHAPE;
+  if (Hq * D > std::numeric_limits<int32_t>::max()) return GDN_ERR_SHAPE;
+  // lists are addressed in 64 bits; their bytes must fit a size_t with room to spare
+  if ((double)N * Hk * K > 1e15) return GDN_ERR_SHAPE;
+  *q_stride = token_stride(stride, Hq, D);
+  return *q_stride < 0 ? GDN_ERR_SHAPE : GDN_OK;
+}
+
+static int check_select(const gdn_select_params* p, const gdn_kv_cache* c, int64_t* q_stride) {
+  if (p == nullptr) return GDN_ERR_NULL;
+  const int st = check_lists(p->num_tokens, p->num_reqs, p->num_q_heads, p->list_len, p->q_stride, c, q_stride);
+  if (st != GDN_OK) return st;
+  if (p->first_pages < 0 || p->newest_pages < 0 || (int64_t)p->first_pages + p->newest_pages > p->list_len) return GDN_ERR_SHAPE;
+  // keys of all entries, 8 bytes each; lists are numbered in 32 bits
+  if ((int64_t)p->num_tokens * c->num_kv_heads > std::numeric_limits<int32_t>::max()) return GDN_ERR_SHAPE;
+  return (int64_t)p->num_tokens * c->num_kv_heads > ((int64_t)1 << 40) / c->max_pages ? GDN_ERR_SHAPE : GDN_OK;
+}
+
+static size_t select_workspace_bytes(const gdn_select_params& p, const gdn_kv_cache& c) {
+  return p.num_reqs == 0 ? 0 : (size_t)p.num_tokens * c.num_kv_heads * c.max_pages * sizeof(uint64_t);
+}
+
+int gdn_attn_select_workspace_bytes(const gdn_select_params* p, const gdn_kv_cache* c, size_t* bytes) {
+  int64_t qs = 0;
+  const int st = check_select(p, c, &qs);
+  if (st != GDN_OK) return st;
+  if (bytes == nullptr) return GDN_ERR_NULL;
+  *bytes = select_workspace_bytes(*p, *c);
+  return GDN_OK;
+}
+
+int gdn_attn_select(const gdn_select_params* p, const gdn_select_tensors* t, const gdn_kv_cache* c, void* workspace,
+                    size_t workspace_bytes, void* stream) {
+  int64_t qs = 0;
+  int st = check_select(p, c, &qs);
+  if (st != GDN_OK) return st;
+  if (t == nullptr) return GDN_ERR_NULL;
+  const int64_t N = p->num_tokens, R = p->num_reqs, Hq = p->num_q_heads, Hk = c->num_kv_heads, D = c->head_dim, K = p->list_len;
+  if (R == 0) return N == 0 ? GDN_OK : GDN_ERR_SHAPE;
+  st = check_cache(c, true);
+  if (st != GDN_OK) return st;
+  const Rows w{N, R, t->cu_seqlens, t->cu_seqlens_host, t->seq_lens, t->seq_lens_host};
+  st = check_rows(w, *c);
+  if (st != GDN_OK) return st;
+  if (N == 0) return GDN_OK;
+  if (t->q == nullptr || t->bounds == nullptr || t->pages == nullptr || t->counts == nullptr) return GDN_ERR_NULL;
+  if (!aligned16(t->q) || !aligned16(t->bounds)) return GDN_ERR_SHAPE;
+  const size_t need = select_workspace_bytes(*p, *c);
+  if (need > 0 && (workspace == nullptr || workspace_bytes < need || !aligned16(workspace))) return GDN_ERR_WORKSPACE;
+  const size_t io = io_bytes(c->io_dtype);
+  const RowSpan q(t->q, Hq * D * io, qs * io, N);
+  const Span pages(t->pages, (size_t)N * Hk * K * 4), counts(t->counts, (size_t)N * 4), ws(workspace, need);
+  const Span inputs[] = {Span(t->bounds, (size_t)c->num_pages * Hk * 2 * D * io), Span(t->cu_seqlens, (R + 1) * 4),
+                         Span(t->seq_lens, R * 4)};
+  const CacheSpans cs(*c, R);
+  for (const Span& o : {pages, counts, ws}) {
+    if (q.overlaps(o) || cs.overlap(o)) return GDN_ERR_ALIAS;
+    for (const Span& s : inputs)
+      if (o.overlaps(s)) return GDN_ERR_ALIAS;
+  }
+  if (pages.overlaps(counts) || pages.overlaps(ws) || counts.overlaps(ws)) return GDN_ERR_ALIAS;
+  gdn::SelectArgs a{};
+  a.q = t->q; a.bounds = t->bounds; a.pages = t->pages; a.counts = t->counts; a.keys = static_cast<uint64_t*>(workspace);
+  a.q_stride = qs; a.group = (int32_t)(Hq / Hk); a.K = (int32_t)K; a.first = p->first_pages; a.newest = p->newest_pages;
+  int64_t held = c->max_pages;
+  if (w.lens_host != nullptr) {
+    held = 0;
+    for (int64_t r = 0; r < R; ++r) held = std::max<int64_t>(held, (w.lens_host[r] + c->page_size - 1) / c->page_size);
+  }
+  a.max_held = (int32_t)held;
+  a.cache = cache_args(*c);
+  a.rows = row_args(w);
+  return status_of(gdn::launch_select(a, c->io_dtype, static_cast<hipStream_t>(stream)));
+}
+
+static int check_sparse(const gdn_sparse_params* p, const gdn_kv_cache* c, int64_t* q_stride) {
+  if (p == nullptr) return GDN_ERR_NULL;
+  const int st = check_lists(p->num_tokens, p->num_reqs, p->num_q_heads, p->list_len, p->q_stride, c, q_stride);
+  if (st != GDN_OK) return st;
+  if (std::isnan(p->scale) || std::isinf(p->scale)) return GDN_ERR_SHAPE;
+  // as in gdn_attn_forward of N requests
+  return 2 * (int64_t)p->num_tokens * p->num_q_heads * (c->head_dim / 64) > ((int64_t)1 << 30) ? GDN_ERR_SHAPE : GDN_OK;
+}
+
+static size_t sparse_workspace_bytes(const gdn_sparse_params& p, const gdn_kv_cache& c) {
+  if (p.num_reqs == 0) return 0;
+  return gdn::attn_workspace_bytes(p.num_tokens, p.num_tokens, p.num_q_heads, c.num_kv_heads, c.head_dim, c.format);
+}
+
+int gdn_attn_sparse_workspace_bytes(const gdn_sparse_params* p, const gdn_kv_cache* c, size_t* bytes) {
+  int64_t qs = 0;
+  const int st = check_sparse(p, c, &qs);
+  if (st != GDN_OK) return st;
+  if (bytes == nullptr) return GDN_ERR_NULL;
+  *bytes = sparse_workspace_bytes(*p, *c);
+  return GDN_OK;
+}
+
+int gdn_attn_sparse_forward(const gdn_sparse_params* p, const gdn_sparse_tensors* t, const gdn_kv_cache* c, void* workspace,
+                            size_t workspace_bytes, void* stream) {
+  int64_t qs = 0;
+  int st = check_sparse(p, c, &qs);
+  if (st != GDN_OK) return st;
+  if (t == nullptr) return GDN_ERR_NULL;
+  const int64_t N = p->num_tokens, R = p->num_reqs, Hq = p->num_q_heads, Hk = c->num_kv_heads, D = c->head_dim, K = p->list_len;
+  if (R == 0) return N == 0 ? GDN_OK : GDN_ERR_SHAPE;
+  st = check_cache(c, true);
+  if (st != GDN_OK) return st;
+  const Rows w{N, R, t->cu_seqlens, t->cu_seqlens_host, t->seq_lens, t->seq_lens_host};
+  st = check_rows(w, *c);
+  if (st != GDN_OK) return st;
+  if (N == 0) return GDN_OK;
+  if (t->q == nullptr || t->pages == nullptr || t->output == nullptr) return GDN_ERR_NULL;
+  if (!aligned16(t->q) || !aligned16(t->output)) return GDN_ERR_SHAPE;
+  const size_t need = sparse_workspace_bytes(*p, *c);
+  if (need > 0 && (workspace == nullptr || workspace_bytes < need || !aligned16(workspace))) return GDN_ERR_WORKSPACE;
+  const size_t io = io_bytes(c->io_dtype);
+  const RowSpan q(t->q, Hq * D * io, qs * io, N);
+  const Span out(t->output, (size_t)N * Hq * D * io), ws(workspace, need);
+  const Span inputs[] = {Span(t->pages, (size_t)N * Hk * K * 4), Span(t->counts, (size_t)N * 4), Span(t->cu_seqlens, (R + 1) * 4),
+                         Span(t->seq_lens, R * 4)};
+  const CacheSpans cs(*c, R);
+  for (const Span& o : {out, ws}) {
+    if (q.overlaps(o) || cs.overlap(o)) return GDN_ERR_ALIAS;
+    for (const Span& s : inputs)
+      if (o.overlaps(s)) return GDN_ERR_ALIAS;
+  }
+  if (out.overlaps(ws)) return GDN_ERR_ALIAS;
+  gdn::SparseArgs a{};
+  a.q = t->q; a.output = t->output; a.q_stride = qs;
+  a.Hq = (int32_t)Hq; a.group = (int32_t)(Hq / Hk);
+  a.scale = p->scale > 0.f ? p->scale : 1.0f / std::sqrt((float)D);
+  // a list is as long as it can be, or as its request where the host knows that
+  const int64_t most = K * c->page_size;
+  int64_t longest = w.lens_host != nullptr ? 0 : most, sum = 0;
+  if (w.lens_host != nullptr)
+    for (int64_t r = 0; r < R; ++r) {
+      const int64_t n = std::min<int64_t>(((int64_t)w.lens_host[r] + c->page_size - 1) / c->page_size * c->page_size, most);
+      const int64_t tokens = w.tokens(r);
+      if (tokens != 0) longest = std::max(longest, n);
+      sum += n * std::max<int64_t>(tokens, 0);
+    }
+  a.max_tokens = 1;
+  a.max_len = (int32_t)longest;
+  a.sum_len = sum;
+  a.cache = cache_args(*c);
+  a.rows.N = a.rows.R = (int32_t)N;
+  a.rows.dense_len = 1;
+  a.lists = t->pages; a.counts = t->counts; a.list_len = (int32_t)K;
+  a.owners = row_args(w);
+  return status_of(gdn::launch_attn_sparse(a, c->io_dtype, workspace, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

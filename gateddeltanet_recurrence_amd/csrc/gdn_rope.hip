@@ -87,6 +87,43 @@ __device__ __forceinline__ uint2_t encode8(const float (&x)[8], float inv) {
   return uint2_t{(uint32_t)a, (uint32_t)b};
 }
 
+// Exponent byte of a block of 32 whose largest magnitude has the fp16 bits `bits`: 2^(s - 127) is the smallest power
+// of two, up to 2^13, with a <= 6 * 2^(s - 127). With a = 1.m * 2^e and 6 = 1.5 * 2^2 that is 2^(e - 2), or twice it
+// when 1.m > 1.5; 255 for an infinity or NaN.
+__device__ __forceinline__ int block_scale_byte(uint32_t bits) {
+  if (bits >= 0x7c00u) return 255;
+  const uint32_t b = __float_as_uint((float)__builtin_bit_cast(_Float16, (uint16_t)bits));
+  return bits > 0 ? min((int)(b >> 23) - 2 + ((b & 0x7fffffu) > 0x400000u ? 1 : 0), 140) : 0;
+}
+
+// Magnitude bits of two halves, the larger of each half.
+__device__ __forceinline__ uint32_t max_magnitudes(uint32_t a, uint32_t b) {
+  typedef uint16_t ushort2_t __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(ushort2_t, a & 0x7fff7fffu),
+                                                                __builtin_bit_cast(ushort2_t, b & 0x7fff7fffu)));
+}
+
+// e2m1 codes of 8 halves over the scale: v_cvt_scalef32_pk_fp4_f16 divides exactly, rounds to nearest even and stops at 6.
+typedef _Float16 half2_t __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ uint32_t encode4(const uint32_t (&w)[4], float scale) {
+  uint32_t c = 0;
+  c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(c, __builtin_bit_cast(half2_t, w[0]), scale, 0);
+  c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(c, __builtin_bit_cast(half2_t, w[1]), scale, 1);
+  c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(c, __builtin_bit_cast(half2_t, w[2]), scale, 2);
+  c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(c, __builtin_bit_cast(half2_t, w[3]), scale, 3);
+  return c;
+}
+
+// 8 e2m1 codes times 2^(s - 127), exact (s = 255: NaN).
+__device__ __forceinline__ half8_t decode4(uint32_t c, int s) {
+  const float scale = __uint_as_float((uint32_t)s << 23);
+  typedef uint32_t uint4_t __attribute__((ext_vector_type(4)));
+  return __builtin_bit_cast(half8_t, uint4_t{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c, scale, 0)),
+                                             __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c, scale, 1)),
+                                             __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c, scale, 2)),
+                                             __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c, scale, 3))});
+}
+
 // Request of the workgroup's first token n0 (the same in every thread): the
 // number of requests that end at or before n0, at most R - 1. Every thread must
 // call it; the result lies in [0, R) whatever cu_seqlens holds.
@@ -149,7 +186,7 @@ __device__ __forceinline__ float2 turn_of(double position, double frequency, dou
   return float2{q == 1 || q == 2 ? -a : a, q >= 2 ? -b : b};
 }
 
-template <typename IO, int D, bool CACHE, bool E4M3>
+template <typename IO, int D, bool CACHE, int FMT>
 __global__ void __launch_bounds__(kThreads) gdn_rope_k(RopeArgs p) {
   constexpr int V = Vec<IO>::n;            // elements of a vector
   constexpr int E = D / (2 * V);           // items of a head
@@ -255,7 +292,7 @@ __global__ void __launch_bounds__(kThreads) gdn_rope_k(RopeArgs p) {
       // the lanes of a head share its token, so they leave together
       if (row_of[t] < 0) continue;
       const int64_t row = row_of[t] + ((int64_t)hh << p.cache.page_shift);
-      if constexpr (E4M3) {
+      if constexpr (FMT == kCacheE4M3) {
         // what is stored is the io value's code, as if k had been rotated and written apart
         float m = 0.f;
 #pragma unroll
@@ -272,6 +309,33 @@ __global__ void __launch_bounds__(kThreads) gdn_rope_k(RopeArgs p) {
         store_stream(dst + a, encode8(x, inv));
         store_stream(dst + b, encode8(y, inv));
         if (e == 0) (is_v ? p.cache.v_scales : p.cache.k_scales)[row] = (uint8_t)s;
+      } else if constexpr (FMT == kCacheE2M1) {
+        // Blocks of 32 neighbours: the halves of a rotation lie in other lanes, so a head's row goes through LDS and
+        // comes back 16 elements a lane. Its lanes are of one wave, whose LDS accesses keep their order.
+        __shared__ alignas(16) _Float16 heads_row[kThreads / E][D];
+        typedef uint32_t uint4_t __attribute__((ext_vector_type(4)));
+        _Float16* mine = heads_row[threadIdx.x / E];
+        *reinterpret_cast<vec_t*>(mine + a) = ra;
+        *reinterpret_cast<vec_t*>(mine + b) = rb;
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+        const uint4_t lo4 = *reinterpret_cast<const uint4_t*>(mine + 16 * e), hi4 = *reinterpret_cast<const uint4_t*>(mine + 16 * e + 8);
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        const uint32_t lo[4] = {lo4[0], lo4[1], lo4[2], lo4[3]}, hi[4] = {hi4[0], hi4[1], hi4[2], hi4[3]};
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) m = max_magnitudes(m, max_magnitudes(lo[i], hi[i]));
+        m = max(m & 0xffffu, m >> 16);
+        m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, kDppQuadXor1, 0xF, 0xF, true));
+        const int s = block_scale_byte(m);
+        const float scale = __uint_as_float((uint32_t)(s == 0 || s == 255 ? 127 : s) << 23);
+        uint2_t codes = uint2_t{encode4(lo, scale), encode4(hi, scale)};
+        if (s == 255) codes = uint2_t{0, 0};
+        store_stream(static_cast<uint8_t*>(is_v ? p.cache.v : p.cache.k) + row * (D / 2) + 8 * e, codes);
+        if ((e & 1) == 0)
+          (is_v ? p.cache.v_scales : p.cache.k_scales)[block_scale_at(row, e >> 1, p.cache.page_shift, D)] = (uint8_t)s;
       } else {
         IO* dst = static_cast<IO*>(is_v ? p.cache.v : p.cache.k) + row * D;
         store_stream(dst + a, ra);
@@ -281,7 +345,7 @@ __global__ void __launch_bounds__(kThreads) gdn_rope_k(RopeArgs p) {
   }
 }
 
-template <typename IO, int D, bool E4M3>
+template <typename IO, int D, int FMT>
 __global__ void __launch_bounds__(kThreads) gdn_kv_read_k(ReadArgs p) {
   constexpr int V = Vec<IO>::n;
   constexpr int E = D / (2 * V);
@@ -311,7 +375,7 @@ __global__ void __launch_bounds__(kThreads) gdn_kv_read_k(ReadArgs p) {
     vec_t xa = {}, xb = {};
     if (row_of[t] >= 0) {
       const int64_t row = row_of[t] + ((int64_t)hh << p.cache.page_shift);
-      if constexpr (E4M3) {
+      if constexpr (FMT == kCacheE4M3) {
         const uint8_t* src = static_cast<const uint8_t*>(is_v ? p.cache.v : p.cache.k) + row * D;
         const uint2_t ca = *reinterpret_cast<const uint2_t*>(src + a), cb = *reinterpret_cast<const uint2_t*>(src + b);
         const int s = (is_v ? p.cache.v_scales : p.cache.k_scales)[row];
@@ -327,6 +391,11 @@ __global__ void __launch_bounds__(kThreads) gdn_kv_read_k(ReadArgs p) {
           to[4 * (i & 1) + 2] = (IO)(hi[0] * scale);
           to[4 * (i & 1) + 3] = (IO)(hi[1] * scale);
         }
+      } else if constexpr (FMT == kCacheE2M1) {
+        const uint8_t* src = static_cast<const uint8_t*>(is_v ? p.cache.v : p.cache.k) + row * (D / 2);
+        const uint8_t* scales = is_v ? p.cache.v_scales : p.cache.k_scales;
+        xa = decode4(*reinterpret_cast<const uint32_t*>(src + a / 2), scales[block_scale_at(row, a >> 5, p.cache.page_shift, D)]);
+        xb = decode4(*reinterpret_cast<const uint32_t*>(src + b / 2), scales[block_scale_at(row, b >> 5, p.cache.page_shift, D)]);
       } else {
         const IO* src = static_cast<const IO*>(is_v ? p.cache.v : p.cache.k) + row * D;
         xa = *reinterpret_cast<const vec_t*>(src + a);
@@ -344,14 +413,18 @@ hipError_t launch_rope_d(const RopeArgs& p, hipStream_t stream) {
   const dim3 grid = grid_of(p.N, p.tokens_per_block);
   const size_t lds = (size_t)p.tokens_per_block * (p.rot / 2) * sizeof(float2);
   if (!p.to_cache) {
-    hipLaunchKernelGGL((gdn_rope_k<IO, D, false, false>), grid, dim3(kThreads), lds, stream, p);
-  } else if (!p.cache.e4m3) {
-    hipLaunchKernelGGL((gdn_rope_k<IO, D, true, false>), grid, dim3(kThreads), lds, stream, p);
+    hipLaunchKernelGGL((gdn_rope_k<IO, D, false, kCacheIo>), grid, dim3(kThreads), lds, stream, p);
+  } else if (p.cache.format == kCacheIo) {
+    hipLaunchKernelGGL((gdn_rope_k<IO, D, true, kCacheIo>), grid, dim3(kThreads), lds, stream, p);
   } else {
-    if constexpr (sizeof(IO) == 2)
-      hipLaunchKernelGGL((gdn_rope_k<IO, D, true, true>), grid, dim3(kThreads), lds, stream, p);
-    else
+    if constexpr (sizeof(IO) == 2) {
+      if (p.cache.format == kCacheE4M3)
+        hipLaunchKernelGGL((gdn_rope_k<IO, D, true, kCacheE4M3>), grid, dim3(kThreads), lds, stream, p);
+      else
+        hipLaunchKernelGGL((gdn_rope_k<IO, D, true, kCacheE2M1>), grid, dim3(kThreads), lds, stream, p);
+    } else {
       return hipErrorInvalidValue;
+    }
   }
   return hipGetLastError();
 }
@@ -359,13 +432,17 @@ hipError_t launch_rope_d(const RopeArgs& p, hipStream_t stream) {
 template <typename IO, int D>
 hipError_t launch_read_d(const ReadArgs& p, hipStream_t stream) {
   const dim3 grid = grid_of(p.rows.N, p.tokens_per_block);
-  if (!p.cache.e4m3) {
-    hipLaunchKernelGGL((gdn_kv_read_k<IO, D, false>), grid, dim3(kThreads), 0, stream, p);
+  if (p.cache.format == kCacheIo) {
+    hipLaunchKernelGGL((gdn_kv_read_k<IO, D, kCacheIo>), grid, dim3(kThreads), 0, stream, p);
   } else {
-    if constexpr (sizeof(IO) == 2)
-      hipLaunchKernelGGL((gdn_kv_read_k<IO, D, true>), grid, dim3(kThreads), 0, stream, p);
-    else
+    if constexpr (sizeof(IO) == 2) {
+      if (p.cache.format == kCacheE4M3)
+        hipLaunchKernelGGL((gdn_kv_read_k<IO, D, kCacheE4M3>), grid, dim3(kThreads), 0, stream, p);
+      else
+        hipLaunchKernelGGL((gdn_kv_read_k<IO, D, kCacheE2M1>), grid, dim3(kThreads), 0, stream, p);
+    } else {
       return hipErrorInvalidValue;
+    }
   }
   return hipGetLastError();
 }

@@ -15,6 +15,13 @@
  *   gdn_kv_read        cached tokens back as packed keys and values
  *   gdn_attn_forward   attention of every request's newest tokens over its pages
  *
+ * and, for contexts whose every position is too much to read at each step, attention
+ * over the pages that a cheap score selects for each token:
+ *
+ *   gdn_kv_bounds            the lowest and the highest key of a page, channel by channel
+ *   gdn_attn_select          which pages a token attends, by a bound of its scores over each
+ *   gdn_attn_sparse_forward  attention over the selected pages
+ *
  * Draft tokens that are not accepted need no replay: the caller leaves
  * seq_lens behind them and the next step overwrites them.
  *
@@ -59,16 +66,29 @@ extern "C" {
  *                  the way back exact, so a code is the only rounding. Rows of FP16 have
  *                  s = 0 or 95 .. 135, and no other byte may stand beside a position that
  *                  is attended (attention takes a value's byte below 94 as 94).
+ *  GDN_CACHE_E2M1  (GDN_F16 io only) the pages hold 4-bit floats (e2m1: a sign bit above a
+ *                  magnitude code 0 .. 7 for 0, 0.5, 1, 1.5, 2, 3, 4, 6), two a byte with
+ *                  element 2 i in the low half: k_pages, v_pages [num_pages, num_kv_heads,
+ *                  page_size, head_dim / 2] bytes; and k_scales, v_scales [num_pages,
+ *                  num_kv_heads, head_dim / 32, page_size] an exponent byte s per block of 32
+ *                  neighbouring elements of a row: element = code * 2^(s - 127). Writing takes
+ *                  a = the largest |x| of the block, 2^(s - 127) = the smallest power of two,
+ *                  but at most 2^13, with a <= 6 * 2^(s - 127), and code = x / 2^(s - 127)
+ *                  rounded to nearest even, at most 6 (so that what is read back is an FP16
+ *                  value: |x| from 49152 on is stored as 49152); s = 0 when the block is zero.
+ *                  A block with an x that is not finite has s = 255: all of it reads as NaN.
+ *                  Blocks of FP16 have s = 0, 101 .. 140 or 255, and no other byte may stand
+ *                  beside a position that is attended.
  *
  * A page number outside [0, num_pages) (e.g. -1) names no page: nothing is
  * written there, reads give zeros, and attention leaves those positions out.
  * The same holds for positions outside [0, max_pages * page_size). */
-typedef enum gdn_cache_format { GDN_CACHE_IO = 0, GDN_CACHE_E4M3 = 1 } gdn_cache_format;
+typedef enum gdn_cache_format { GDN_CACHE_IO = 0, GDN_CACHE_E4M3 = 1, GDN_CACHE_E2M1 = 4 } gdn_cache_format;
 
 typedef struct gdn_kv_cache {
   void* k_pages;
   void* v_pages;
-  uint8_t* k_scales;              /* GDN_CACHE_E4M3 only, else NULL                  */
+  uint8_t* k_scales;              /* GDN_CACHE_E4M3 and E2M1 only, else NULL         */
   uint8_t* v_scales;
   const int32_t* page_table;      /* device, i32 [R, max_pages]                      */
   const int32_t* page_table_host; /* host mirror or NULL. When given every entry must
@@ -211,7 +231,8 @@ typedef struct gdn_kv_tensors {
 int gdn_kv_write(const gdn_kv_params* params, const gdn_kv_tensors* tensors, const gdn_kv_cache* cache, void* stream);
 
 /* Reads the tokens' keys and values from their pages into packed rows k and v
- * (E4M3 rows as code * 2^(s - 127), rounded to io where that is out of its range),
+ * (E4M3 rows as code * 2^(s - 127), rounded to io where that is out of its range; E2M1
+ * blocks likewise, which is exact),
  * zeros where there is no page. With T_r = seq_lens[r] that is all a request has
  * cached. Errors as gdn_kv_write. */
 int gdn_kv_read(const gdn_kv_params* params, const gdn_kv_tensors* tensors, const gdn_kv_cache* cache, void* stream);
@@ -263,6 +284,98 @@ int gdn_attn_forward(const gdn_attn_params* params, const gdn_attn_tensors* tens
 /* Workspace bytes gdn_attn_forward needs for these sizes, whatever the lengths
  * (the cache's pointers are not read). */
 int gdn_attn_workspace_bytes(const gdn_attn_params* params, const gdn_kv_cache* cache, size_t* bytes);
+
+/* ---- Sparse attention: the bounds of a page's keys, the selection, the attention.
+ *
+ * bounds [num_pages, num_kv_heads, 2, head_dim] holds, for each page and head, the lowest
+ * and then the highest value of every channel over the page's cached keys, in io. A caller
+ * that keeps it calls gdn_kv_bounds after every gdn_kv_write, with the same rows. */
+
+/* Writes the bounds of every page that holds one of the call's tokens (as in gdn_kv_write:
+ * the newest T_r of seq_lens[r]), from all positions of the page up to seq_lens[r] - 1 as
+ * the cache holds them, so tokens that were not accepted leave no trace. Other pages'
+ * bounds stay as they are. A NaN key makes its channel's bounds NaN. Of params, the
+ * numbers of tokens and requests are read (the others are 0), of tensors what describes
+ * the rows (k, v, q, q_out, positions and inv_freq are not read). bounds: device, io,
+ * disjoint from the cache. No page may hold tokens of two requests of one call (with
+ * mirrors that show it, GDN_ERR_ALIAS). Errors as gdn_kv_read. */
+int gdn_kv_bounds(const gdn_kv_params* params, const gdn_kv_tensors* tensors, const gdn_kv_cache* cache, void* bounds,
+                  void* stream);
+
+typedef struct gdn_select_params {
+  int32_t num_tokens;            /* N >= 0                                          */
+  int32_t num_reqs;              /* R >= 0                                          */
+  int32_t num_q_heads;           /* Hq: a multiple of the cache's Hk                */
+  int32_t list_len;              /* K: entries of a list, 1 .. 2^30 / page_size      */
+  int32_t first_pages;           /* the request's first f >= 0 pages and the        */
+  int32_t newest_pages;          /* token's newest m >= 0, f + m <= K, are always in */
+  int32_t q_stride;              /* as in gdn_rope_params                           */
+} gdn_select_params;
+
+typedef struct gdn_select_tensors {
+  const void* q;                 /* device, io [N, Hq, D], rows q_stride apart       */
+  const int32_t* cu_seqlens;     /* as in gdn_kv_tensors                            */
+  const int32_t* cu_seqlens_host;
+  const int32_t* seq_lens;
+  const int32_t* seq_lens_host;
+  const void* bounds;            /* device, io [num_pages, Hk, 2, D]                 */
+  int32_t* pages;                /* device, i32 [N, Hk, K]: the lists               */
+  int32_t* counts;               /* device, i32 [N]: entries of a token's lists      */
+} gdn_select_tensors;
+
+/* Selects K pages for every token and key head: of the entries i of its request's page
+ * table that hold one of the positions 0 .. P (i <= P / page_size) and name a page, the
+ * first and newest ones asked for and those of the highest score
+ *   score[n, h, i] = sum_d w+_d high_d + w-_d low_d      w+ = sum over the group of max(q, 0)
+ *                                                        w- = sum over the group of min(q, 0)
+ * with low and high the page's bounds: the group's sum of a bound that no q . k of the
+ * page exceeds. Equal scores go to the lower i, and a NaN score counts as the highest, so
+ * that what is wrong in a page or in q shows. The sums are taken in 64 bits: which page
+ * of two near ones is selected does not depend on how the work is split, but for their
+ * last bits. pages[n, h] is the selected i's in ascending order, -1 behind them, and
+ * counts[n] their number, min(K, the entries there are), for every h. Tokens behind the
+ * last request's are left as they are. The cache's k_pages, v_pages and scales are not read.
+ * The workspace is as in gdn_attn_forward, of gdn_attn_select_workspace_bytes() bytes.
+ * N Hk max_pages is at most 2^40, else GDN_ERR_SHAPE.
+ * Errors: GDN_ERR_NULL, GDN_ERR_SHAPE, GDN_ERR_DTYPE, GDN_ERR_CAPACITY,
+ * GDN_ERR_WORKSPACE, GDN_ERR_ALIAS. */
+int gdn_attn_select(const gdn_select_params* params, const gdn_select_tensors* tensors, const gdn_kv_cache* cache,
+                    void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace bytes gdn_attn_select needs for these sizes, whatever the lengths. */
+int gdn_attn_select_workspace_bytes(const gdn_select_params* params, const gdn_kv_cache* cache, size_t* bytes);
+
+typedef struct gdn_sparse_params {
+  int32_t num_tokens;            /* N >= 0                                          */
+  int32_t num_reqs;              /* R >= 0                                          */
+  int32_t num_q_heads;           /* Hq: a multiple of the cache's Hk                */
+  int32_t list_len;              /* K: entries of a list, 1 .. 2^30 / page_size      */
+  float scale;                   /* of q . k; <= 0 selects D^-1/2                   */
+  int32_t q_stride;              /* as in gdn_rope_params                           */
+} gdn_sparse_params;
+
+typedef struct gdn_sparse_tensors {
+  const void* q;                 /* device, io [N, Hq, D], rows q_stride apart       */
+  const int32_t* cu_seqlens;     /* as in gdn_kv_tensors                            */
+  const int32_t* cu_seqlens_host;
+  const int32_t* seq_lens;
+  const int32_t* seq_lens_host;
+  const int32_t* pages;          /* device, i32 [N, Hk, K]                           */
+  const int32_t* counts;         /* device, i32 [N], taken within 0 .. K; NULL: K each */
+  void* output;                  /* device, io [N, Hq, D]                           */
+} gdn_sparse_tensors;
+
+/* gdn_attn_forward where token n's heads h Hq / Hk .. attend, of the positions 0 .. P,
+ * those of the entries pages[n, h, 0 .. counts[n] - 1] of its request's page table
+ * only, in any order. An entry that is out of range, past P or without a page holds
+ * nothing (-1 skips it); one that is listed twice counts twice. A token that attends no
+ * position gives zeros. Everything else is as there; each token's pages are read for it
+ * alone. 2 N Hq D / 64 is at most 2^30, else GDN_ERR_SHAPE. Errors as there. */
+int gdn_attn_sparse_forward(const gdn_sparse_params* params, const gdn_sparse_tensors* tensors,
+                            const gdn_kv_cache* cache, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace bytes gdn_attn_sparse_forward needs for these sizes, whatever the lists. */
+int gdn_attn_sparse_workspace_bytes(const gdn_sparse_params* params, const gdn_kv_cache* cache, size_t* bytes);
 
 #ifdef __cplusplus
 }
