@@ -547,6 +547,7 @@ int gdn_attn_select(const gdn_select_params* p, const gdn_select_tensors* t, con
     for (int64_t r = 0; r < R; ++r) held = std::max<int64_t>(held, (w.lens_host[r] + c->page_size - 1) / c->page_size);
   }
   a.max_held = (int32_t)held;
+  a.group_tokens = most_tokens(w) > 1 ? gdn::kSelectGroup : 1;
   a.cache = cache_args(*c);
   a.rows = row_args(w);
   return status_of(gdn::launch_select(a, c->io_dtype, static_cast<hipStream_t>(stream)));

@@ -97,6 +97,9 @@ struct SelectArgs {
   int64_t q_stride;
   int32_t group, K, first, newest;
   int32_t max_held;             // no token has more entries, as far as the host knows
+  int32_t lds_entries;          // keys that a list may have in LDS
+  int32_t group_tokens;         // that share the bounds they read: 1 or kSelectGroup
+  int32_t chunk;                // entries of a workgroup, where a list is split
   CacheArgs cache;
   RowArgs rows;
 };
@@ -123,6 +126,7 @@ struct SparseArgs : AttnArgs {
   RowArgs owners;               // the requests that the tokens belong to
 };
 
+constexpr int kSelectGroup = 4;
 constexpr int kRopeMaxTokens = 16;   // tokens one workgroup of the rotation and cache kernels handles
 
 // io_dtype: 0 = f32, 1 = f16 (gdn_dtype values).

@@ -89,10 +89,11 @@ __global__ void __launch_bounds__(kThreads) gdn_kv_bounds_k(BoundsArgs p) {
   __shared__ float low[kWaves][D], high[kWaves][D];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int ps = 1 << p.cache.page_shift;
-  const int64_t work = ((int64_t)p.rows.N + p.tokens_per_block - 1) / p.tokens_per_block * p.cache.Hk;
+  const unsigned work = ((unsigned)p.rows.N + p.tokens_per_block - 1) / (unsigned)p.tokens_per_block * (unsigned)p.cache.Hk;   // the host: below 2^31
   const int tokens = min(row_start(p.rows, p.rows.R), p.rows.N);
-  for (int64_t job = blockIdx.x; job < work; job += gridDim.x) {
-    const int h = (int)(job % p.cache.Hk), n0 = (int)(job / p.cache.Hk) * p.tokens_per_block;
+  for (unsigned job = blockIdx.x; job < work; job += gridDim.x) {
+    const unsigned group = job / (unsigned)p.cache.Hk;     // 64-bit divisions would take a microsecond
+    const int h = (int)(job - group * p.cache.Hk), n0 = (int)group * p.tokens_per_block;
     const int n1 = min(n0 + p.tokens_per_block, tokens);
     if (n0 >= n1) continue;
     int r = owner_of(p.rows, n0, lane);
@@ -149,9 +150,10 @@ __global__ void __launch_bounds__(kThreads) gdn_kv_bounds_k(BoundsArgs p) {
 // ------------------------------------------------------------------------- selection
 
 // Scores are kept as 64-bit keys that order as they do: 0 for an entry that may not be
-// selected, the highest for a NaN.
+// selected, one below the highest for a NaN, the highest for an entry that is always in.
+constexpr uint64_t kAlways = ~(uint64_t)0;
 __device__ __forceinline__ uint64_t key_of(double x) {
-  if (x != x) return ~(uint64_t)0;
+  if (x != x) return kAlways - 1;
   const uint64_t b = (uint64_t)__double_as_longlong(x);
   return (b >> 63) != 0 ? ~b : b | ((uint64_t)1 << 63);
 }
@@ -164,243 +166,473 @@ __device__ __forceinline__ double dpp64(double x) {
   return __longlong_as_double((long long)((uint64_t)hi << 32 | lo));
 }
 
-// A token's pages: its request's table, the entries that it holds.
+// Token n of request r: the request's table, the entries of it that the token holds.
 struct Token {
   const int32_t* table;
+  int64_t pos;
   int held;
 };
-__device__ __forceinline__ Token token_at(const SelectArgs& p, int n, int lane) {
-  const int r = owner_of(p.rows, n, lane);
-  const int64_t pos = (int64_t)p.rows.seq_lens[r] - row_start(p.rows, r + 1) + n;
+__device__ __forceinline__ int held_at(const SelectArgs& p, int64_t pos) {
+  return pos < 0 ? 0 : (int)min((pos >> p.cache.page_shift) + 1, (int64_t)p.cache.max_pages);
+}
+__device__ __forceinline__ Token token_at(const SelectArgs& p, int r, int n) {
   Token t;
+  t.pos = (int64_t)p.rows.seq_lens[r] - row_start(p.rows, r + 1) + n;
   t.table = p.cache.table + (int64_t)r * p.cache.max_pages;
-  t.held = pos < 0 ? 0 : (int)min((pos >> p.cache.page_shift) + 1, (int64_t)p.cache.max_pages);
+  t.held = held_at(p, t.pos);
   return t;
 }
 
-// 8 elements as doubles.
-template <typename IO>
-__device__ __forceinline__ void load8(const IO* src, double (&x)[8]) {
-  if constexpr (sizeof(IO) == 2) {
-    const half8_t h = *reinterpret_cast<const half8_t*>(src);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = (double)(float)h[i];
-  } else {
-    const float4_t a = *reinterpret_cast<const float4_t*>(src), b = *reinterpret_cast<const float4_t*>(src + 4);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      x[i] = (double)a[i];
-      x[4 + i] = (double)b[i];
-    }
-  }
-}
-
-// Keys of the entries [i0, i1) of token n, key head h: L = D / 16 lanes an entry, 16
-// channels of both bounds each.
-template <typename IO, int D>
-__device__ __forceinline__ void score_entries(const SelectArgs& p, const Token& t, int n, int h, int i0, int i1, uint64_t* keys) {
-  constexpr int L = D / 16;
-  const int tid = threadIdx.x, e = tid % L;
-  double plus[2][8], minus[2][8];
-#pragma unroll
-  for (int c = 0; c < 2; ++c)
-#pragma unroll
-    for (int i = 0; i < 8; ++i) plus[c][i] = minus[c][i] = 0.0;
-  for (int g = 0; g < p.group; ++g) {
-    const IO* q = static_cast<const IO*>(p.q) + (int64_t)n * p.q_stride + (int64_t)(h * p.group + g) * D;
-#pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      double x[8];
-      load8(q + 8 * (c * L + e), x);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        plus[c][i] += x[i] < 0.0 ? 0.0 : x[i];             // a NaN goes into both
-        minus[c][i] += x[i] > 0.0 ? 0.0 : x[i];
-      }
-    }
-  }
-  for (int i = i0 + tid / L; i < i1; i += kThreads / L) {
-    const int page = t.table[i];
-    const bool there = page >= 0 && page < p.cache.num_pages;
-    const IO* low = static_cast<const IO*>(p.bounds) + ((int64_t)(there ? page : 0) * p.cache.Hk + h) * 2 * D;
-    double sum = 0.0;
-#pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      double lo[8], hi[8];
-      load8(low + 8 * (c * L + e), lo);
-      load8(low + D + 8 * (c * L + e), hi);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) sum = fma(plus[c][k], hi[k], fma(minus[c][k], lo[k], sum));
-    }
-    sum += dpp64<kDppQuadXor1>(sum);
-    sum += dpp64<kDppQuadXor2>(sum);
-    if constexpr (L >= 8) sum += dpp64<kDppHalfMirror>(sum);
-    if constexpr (L >= 16) sum += dpp64<kDppRowMirror>(sum);
-    if (e == 0) keys[i] = there ? key_of(sum) : 0;
-  }
-}
-
-// Inclusive sum over a workgroup's threads, and the total. `sums` is free again after the call's second barrier.
-__device__ __forceinline__ uint64_t block_scan(uint64_t x, uint64_t (&sums)[kWaves], uint64_t* total) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-#pragma unroll
-  for (int m = 1; m < 64; m <<= 1) {
-    const uint64_t y = __shfl_up(x, m);
-    if (lane >= m) x += y;
-  }
-  if (lane == 63) sums[wave] = x;
-  __syncthreads();
-  uint64_t before = 0, all = 0;
-#pragma unroll
-  for (int w = 0; w < kWaves; ++w) {
-    before += w < wave ? sums[w] : 0;
-    all += sums[w];
-  }
-  __syncthreads();
-  *total = all;
-  return x + before;
-}
-
-constexpr int kBuckets = 2048;
-
-struct PickShared {
-  uint32_t hist[kBuckets];
-  uint64_t sums[kWaves], low[kWaves], high[kWaves];
-  uint32_t bucket, above, inside;
+// 16 bytes of io elements as they are, and as doubles.
+template <typename IO> struct Vec;
+template <> struct Vec<_Float16> {
+  typedef half8_t type;
+};
+template <> struct Vec<float> {
+  typedef float4_t type;
 };
 
-// The K entries of a list from the keys of its `held` entries, those from `first_end` on and before `newest_begin`
-// by key. The K-th largest key is found by counting keys in 2,048 equal parts of their range, and then in the part
-// that it lies in, until every key of the part is taken or all are equal.
-__device__ __forceinline__ void pick_entries(const SelectArgs& p, const uint64_t* keys, int held, int32_t* list, int32_t* count_out,
-                                             PickShared& s) {
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, K = p.K;
-  const int newest_begin = held - p.newest;
-  uint64_t forced = 0, others = 0, lo = ~(uint64_t)0, hi = 0;
-  for (int i = tid; i < held; i += kThreads) {
-    const uint64_t key = keys[i];
-    if (key == 0) continue;
-    if (i < p.first || i >= newest_begin) {
-      ++forced;
-    } else {
-      ++others;
-      lo = min(lo, key);
-      hi = max(hi, key);
+// The group's sums of the negative and of the positive parts of q, channel by channel, each channel by one thread, for
+// `count` tokens from n on.
+template <typename IO, int D, int TOKENS>
+__device__ __forceinline__ void sum_parts(const SelectArgs& p, int n, int count, int h, double (&parts)[TOKENS][2][D]) {
+  const int d = threadIdx.x;
+  if (d >= D) return;
+  const IO* q = static_cast<const IO*>(p.q) + (int64_t)n * p.q_stride + (int64_t)h * p.group * D + d;
+  double minus[TOKENS], plus[TOKENS];
+#pragma unroll
+  for (int j = 0; j < TOKENS; ++j) minus[j] = plus[j] = 0.0;
+#pragma unroll 4
+  for (int g = 0; g < p.group; ++g) {
+#pragma unroll
+    for (int j = 0; j < TOKENS; ++j) {
+      const float x = (float)q[min(j, count - 1) * p.q_stride + (int64_t)g * D];
+      minus[j] += (double)(x > 0.f ? 0.f : x);             // a NaN goes into both
+      plus[j] += (double)(x < 0.f ? 0.f : x);
     }
   }
-  uint64_t both;
-  block_scan(forced << 32 | others, s.sums, &both);
-  const int64_t all_forced = (int64_t)(both >> 32), all_others = (int64_t)(both & 0xffffffffu);
-  uint64_t over = 0;                                       // keys above this are taken, and `equal` of those that are it
-  int64_t equal = 0;
-  if (all_forced + all_others > K) {
-    // the range of the others' keys
 #pragma unroll
-    for (int m = 1; m < 64; m <<= 1) {
-      lo = min(lo, (uint64_t)__shfl_xor(lo, m));
-      hi = max(hi, (uint64_t)__shfl_xor(hi, m));
-    }
-    if (lane == 0) {
-      s.low[wave] = lo;
-      s.high[wave] = hi;
-    }
-    __syncthreads();
+  for (int j = 0; j < TOKENS; ++j) {
+    parts[j][0][d] = minus[j];
+    parts[j][1][d] = plus[j];
+  }
+}
+
+// Scores of the entries [i0, i1) of a table, for the tokens whose parts are in LDS: L lanes an entry, 16 channels of both
+// bounds each; kAhead entries of a lane's are on their way at once (a list of 256 entries took 18 us one at a time).
+template <typename IO, int D>
+struct Scorer {
+  static constexpr int L = D / 16, V = 16 / sizeof(IO), kVecs = 16 / V, kAhead = 4, kStep = kThreads / L;
+  typedef typename Vec<IO>::type vec_t;
+  const SelectArgs& p;
+  const int32_t* table;
+  int h, i, i1;                                            // this lane's next entry, the end
+  int page[kAhead], next[kAhead];
+  uint4_t lo[kAhead][kVecs], hi[kAhead][kVecs];
+  double minus[16], plus[16];
+
+  __device__ __forceinline__ Scorer(const SelectArgs& args, const int32_t* entries, int head, int begin, int end)
+      : p(args), table(entries), h(head), i(begin + (int)threadIdx.x / L), i1(end) {
+    look_up();
+  }
+  __device__ __forceinline__ void look_up() {
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w) {
-      lo = min(lo, s.low[w]);
-      hi = max(hi, s.high[w]);
-    }
-    int64_t need = K - all_forced;
-    if (need <= 0) {
-      over = ~(uint64_t)0;
-    } else {
-      for (;;) {
-        const uint64_t range = hi - lo;
-        const int bits = range == 0 ? 0 : 64 - __builtin_clzll(range), shift = max(bits - 11, 0);
-        for (int i = tid; i < kBuckets; i += kThreads) s.hist[i] = 0;
-        __syncthreads();
-        for (int i = tid; i < held; i += kThreads) {
-          const uint64_t key = keys[i];
-          if (key >= lo && key <= hi && i >= p.first && i < newest_begin) atomicAdd(&s.hist[(key - lo) >> shift], 1u);
-        }
-        __syncthreads();
-        // thread t holds buckets from the top: 8 t' .. 8 t' + 7, t' = 255 - t
-        const int base = kBuckets / kThreads * (kThreads - 1 - tid);
-        uint32_t mine[kBuckets / kThreads];
-        uint64_t sum = 0;
+    for (int u = 0; u < kAhead; ++u) next[u] = table[min(i + u * kStep, i1 - 1)];
+  }
+  __device__ __forceinline__ void load() {
+    const int e = threadIdx.x % L;
 #pragma unroll
-        for (int i = 0; i < kBuckets / kThreads; ++i) {
-          mine[i] = s.hist[base + i];
-          sum += mine[i];
-        }
-        uint64_t total;
-        const uint64_t upto = block_scan(sum, s.sums, &total);
-        if ((int64_t)(upto - sum) < need && need <= (int64_t)upto) {
-          uint64_t above = upto - sum;
-          int b = kBuckets / kThreads - 1;
+    for (int u = 0; u < kAhead; ++u) {
+      page[u] = next[u] >= 0 && next[u] < p.cache.num_pages ? next[u] : -1;
+      const IO* low = static_cast<const IO*>(p.bounds) + ((int64_t)max(page[u], 0) * p.cache.Hk + h) * 2 * D;
 #pragma unroll
-          for (int i = kBuckets / kThreads - 1; i > 0; --i)
-            if (b == i && (int64_t)(above + mine[i]) < need) {
-              above += mine[i];
-              b = i - 1;
-            }
-          s.bucket = (uint32_t)(base + b);
-          s.above = (uint32_t)above;
-          s.inside = 0;
-#pragma unroll
-          for (int i = 0; i < kBuckets / kThreads; ++i)
-            if (b == i) s.inside = mine[i];
-        }
-        __syncthreads();
-        need -= s.above;
-        lo += (uint64_t)s.bucket << shift;
-        hi = min(hi, lo + (((uint64_t)1 << shift) - 1));
-        const bool done = (int64_t)s.inside == need, same = shift == 0;
-        __syncthreads();                                   // s is written again
-        if (done || same) {
-          over = done ? lo - 1 : lo;
-          equal = done ? 0 : need;
-          break;
-        }
+      for (int c = 0; c < kVecs; ++c) {
+        lo[u][c] = *reinterpret_cast<const uint4_t*>(low + V * (c * L + e));
+        hi[u][c] = *reinterpret_cast<const uint4_t*>(low + D + V * (c * L + e));
       }
     }
   }
-  // in order: each thread's entries are neighbours
-  const int per = (held + kThreads - 1) / kThreads, i0 = min(tid * per, held), i1 = min(i0 + per, held);
-  uint64_t taken = 0, ties = 0;
-  for (int i = i0; i < i1; ++i) {
-    const uint64_t key = keys[i];
-    const bool always = key != 0 && (i < p.first || i >= newest_begin);
-    taken += always || key > over ? 1 : 0;
-    ties += !always && key != 0 && key == over ? 1 : 0;
+  // Keeps the compiler from holding the bounds as doubles from token to token, in four times the registers.
+  __device__ __forceinline__ void forget() {
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u)
+#pragma unroll
+      for (int c = 0; c < kVecs; ++c) asm volatile("" : "+v"(lo[u][c]), "+v"(hi[u][c]));
   }
-  uint64_t total;
-  const uint64_t upto = block_scan(taken << 32 | ties, s.sums, &total);
-  int64_t ties_before = (int64_t)(upto & 0xffffffffu) - (int64_t)ties;
-  int64_t at = (int64_t)(upto >> 32) - (int64_t)taken + min(ties_before, equal);
-  for (int i = i0; i < i1; ++i) {
-    const uint64_t key = keys[i];
-    const bool always = key != 0 && (i < p.first || i >= newest_begin), tie = !always && key != 0 && key == over;
-    if (always || key > over || (tie && ties_before < equal)) list[at++] = i;
-    if (tie) ++ties_before;
+  __device__ __forceinline__ void take(const double (&parts)[2][D]) {
+    const int e = threadIdx.x % L;
+#pragma unroll
+    for (int c = 0; c < kVecs; ++c)
+#pragma unroll
+      for (int k = 0; k < V; ++k) {
+        minus[V * c + k] = parts[0][V * (c * L + e) + k];
+        plus[V * c + k] = parts[1][V * (c * L + e) + k];
+      }
   }
-  const int count = (int)((int64_t)(total >> 32) + min((int64_t)(total & 0xffffffffu), equal));
-  for (int i = count + tid; i < K; i += kThreads) list[i] = -1;
-  if (tid == 0 && count_out != nullptr) *count_out = count;
+  // store(entry, page, score) for the loaded entries and the token that was taken, by an entry's first lane.
+  template <typename Store>
+  __device__ __forceinline__ void score(Store store) const {
+    const int e = threadIdx.x % L;
+    double sum[kAhead];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) sum[u] = 0.0;
+#pragma unroll
+    for (int c = 0; c < kVecs; ++c)
+#pragma unroll
+      for (int k = 0; k < V; ++k)
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u)
+          sum[u] = fma(plus[V * c + k], (double)(float)__builtin_bit_cast(vec_t, hi[u][c])[k],
+                       fma(minus[V * c + k], (double)(float)__builtin_bit_cast(vec_t, lo[u][c])[k], sum[u]));
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      double x = sum[u];
+      x += dpp64<kDppQuadXor1>(x);
+      x += dpp64<kDppQuadXor2>(x);
+      if constexpr (L >= 8) x += dpp64<kDppHalfMirror>(x);
+      if constexpr (L >= 16) x += dpp64<kDppRowMirror>(x);
+      const int at = i + u * kStep;
+      if (e == 0 && at < i1) store(at, page[u], x);
+    }
+  }
+  // On to the next entries; false where there are none for any lane of the workgroup.
+  __device__ __forceinline__ bool advance() {
+    i += kAhead * kStep;
+    if (i - (int)threadIdx.x / L >= i1) return false;
+    look_up();
+    load();
+    return true;
+  }
+};
+
+// The key of an entry of a token that holds `held`.
+__device__ __forceinline__ uint64_t entry_key(const SelectArgs& p, int held, int at, int page, double score) {
+  return page < 0 ? 0 : at < p.first || at >= held - p.newest ? kAlways : key_of(score);
 }
+
+// Writes the list's tail and its length.
+template <int WAVES>
+__device__ __forceinline__ void end_list(const SelectArgs& p, int count, int32_t* list, int32_t* count_out) {
+  for (int i = count + (int)threadIdx.x; i < p.K; i += 64 * WAVES) list[i] = -1;
+  if (threadIdx.x == 0 && count_out != nullptr) *count_out = count;
+}
+
+__device__ __forceinline__ uint64_t uniform(uint64_t x) {
+  return (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(x >> 32)) << 32 |
+         (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)x);
+}
+// Largest over a wave's lanes.
+template <int CTRL>
+__device__ __forceinline__ uint64_t dpp_max(uint64_t x) {
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)x, CTRL, 0xF, 0xF, true);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(x >> 32), CTRL, 0xF, 0xF, true);
+  return max(x, (uint64_t)hi << 32 | lo);
+}
+__device__ __forceinline__ uint64_t lane_of(uint64_t x, int lane) {
+  return (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(x >> 32), lane) << 32 |
+         (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)x, lane);
+}
+__device__ __forceinline__ uint64_t wave_max(uint64_t x) {
+  x = dpp_max<kDppRowMirror>(dpp_max<kDppHalfMirror>(dpp_max<kDppQuadXor2>(dpp_max<kDppQuadXor1>(x))));
+  return max(max(lane_of(x, 0), lane_of(x, 16)), max(lane_of(x, 32), lane_of(x, 48)));
+}
+// Sum over aligned groups of 16 lanes.
+__device__ __forceinline__ int row_sum(int x) {
+  x += __builtin_amdgcn_update_dpp(0, x, kDppQuadXor1, 0xF, 0xF, true);
+  x += __builtin_amdgcn_update_dpp(0, x, kDppQuadXor2, 0xF, 0xF, true);
+  x += __builtin_amdgcn_update_dpp(0, x, kDppHalfMirror, 0xF, 0xF, true);
+  return x + __builtin_amdgcn_update_dpp(0, x, kDppRowMirror, 0xF, 0xF, true);
+}
+__device__ __forceinline__ int count_lanes(bool x) { return __builtin_popcountll(__ballot(x)); }
+
+// What the waves of a workgroup that share a list's keys tell each other. `turn` alternates, so that one barrier is enough.
+struct PickShared {
+  uint64_t low[16], high[16];
+  int counts[2][4][16];
+};
+
+// The K entries of the highest keys among `held`, equal ones from the lowest entry on, in ascending order. A
+// threshold is found by cutting the keys' range into WAYS parts until K keys lie from it on, or none but equal ones are
+// left between its ends: as often as it takes to tell the K-th key from the next, 12 to 15 halvings among some
+// thousand scores, 64 at most.
+//
+// SHARED: the keys are split over the workgroup's waves, up to COLUMNS columns of 64 neighbours each (COLUMNS 0: any
+// number, read again each time), which add their counts behind a barrier; else WAVES is 1.
+constexpr int kColumns = 8, kFew = 64 * kColumns;          // keys that a wave holds in registers
+struct Three {
+  int a, b, c;
+};
+
+// Narrows [lo, hi], with `count` keys from lo on, K or more, and fewer than K above hi, until count is K or lo is hi;
+// counts(x, y, z) says how many keys there are from each of the cuts x >= y >= z on (two ways: from y).
+template <int WAYS, typename T, typename Counts>
+__device__ __forceinline__ void cut_range(int K, int& count, T& lo, T& hi, Counts counts) {
+  while (count != K && lo < hi) {
+    const T range = hi - lo, part = range >> 2;            // lo < z <= y <= x <= hi
+    const T y = hi - (range >> 1), x = WAYS == 2 || range < 4 ? y : hi - part, z = WAYS == 2 || range < 4 ? y : y - part;
+    const Three n = counts(x, y, z);
+    if (WAYS == 4 && n.a >= K) {
+      lo = x;
+      count = n.a;
+    } else if (n.b >= K) {
+      lo = y;
+      count = n.b;
+      if (WAYS == 4) hi = x - 1;
+    } else if (WAYS == 4 && n.c >= K) {
+      lo = z;
+      count = n.c;
+      hi = y - 1;
+    } else {
+      hi = z - 1;
+    }
+  }
+}
+template <int WAVES, int COLUMNS, bool SHARED, typename Keys>
+__device__ __forceinline__ void pick(const SelectArgs& p, const Keys& keys, int held, int32_t* list, int32_t* count_out,
+                                     PickShared& s) {
+  constexpr int WAYS = SHARED ? 4 : 2;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  const int columns = (held + (SHARED ? 64 * WAVES : 64) - 1) / (SHARED ? 64 * WAVES : 64);
+  const int first = SHARED ? wave * columns : 0;           // column of this wave
+  uint64_t mine[COLUMNS > 0 ? COLUMNS : 1];
+  const auto load = [&](int c) -> uint64_t {
+    const int64_t i = 64 * (int64_t)(first + c) + lane;
+    return i < held ? keys[i] : 0;
+  };
+  // f(key, column) of this wave's keys, all lanes together
+  const auto each = [&](auto f) {
+    if constexpr (COLUMNS > 0) {
+#pragma unroll
+      for (int c = 0; c < COLUMNS; ++c)
+        if (c < columns) f(mine[c], c);
+    } else {
+      for (int c = 0; c < columns; ++c) f(load(c), c);
+    }
+  };
+  if constexpr (COLUMNS > 0) {
+#pragma unroll
+    for (int c = 0; c < COLUMNS; ++c) mine[c] = c < columns ? load(c) : 0;
+  }
+  int turn = 0;
+  // Sums over the waves of three numbers: row i of 16 lanes adds the waves' i-th. One read of LDS a wave (each wave
+  // reading all of them took most of the time), and no array of the numbers, which the compiler would put into LDS by
+  // the thread's number, read from the launch's packet in host memory (512 workgroups: 13 us).
+  const auto total = [&](int a, int b, int c) -> Three {
+    if constexpr (!SHARED) return Three{a, b, c};
+    if (lane < 3) s.counts[turn][lane][wave] = lane == 0 ? a : lane == 1 ? b : c;
+    __syncthreads();
+    const int x = row_sum((lane & 15) < WAVES ? s.counts[turn][lane >> 4][lane & 15] : 0);
+    turn ^= 1;
+    return Three{__builtin_amdgcn_readlane(x, 0), __builtin_amdgcn_readlane(x, 16), __builtin_amdgcn_readlane(x, 32)};
+  };
+
+  uint64_t hi = 0, lo = kAlways;
+  int some = 0, always = 0;
+  each([&](uint64_t key, int) {
+    some += count_lanes(key != 0);
+    always += count_lanes(key == kAlways);
+    hi = key != kAlways ? max(hi, key) : hi;
+    lo = key != 0 ? min(lo, key) : lo;
+  });
+  const Three have = total(some, always, 0);
+  const int there = have.a;
+  uint64_t least = 1;                                      // keys from this one on are taken, but for the last
+  int surplus = 0;                                         // of those that are equal to it
+  if (there > p.K && have.b == p.K) {
+    least = kAlways;
+  } else if (there > p.K) {
+    lo = ~wave_max(~lo);
+    hi = wave_max(hi);
+    if constexpr (SHARED) {
+      if (lane == 0) {
+        s.low[wave] = lo;
+        s.high[wave] = hi;
+      }
+      __syncthreads();
+      lo = ~wave_max(lane < WAVES ? ~s.low[lane] : 0);
+      hi = wave_max(lane < WAVES ? s.high[lane] : 0);
+    }
+    lo = uniform(lo);
+    hi = uniform(hi);
+    // From lo on there are K or more keys, above hi fewer. First by the 32 highest bits of the range, where a
+    // comparison takes a quarter of the time, then, where these do not tell the K-th from the next, by all.
+    const uint64_t range = hi - lo;
+    const int shift = max(32 - (range == 0 ? 32 : __builtin_clzll(range)), 0);
+    int count = there;
+    if (range > 0) {
+      uint32_t lo32 = 0, hi32 = (uint32_t)(range >> shift), short_keys[COLUMNS > 0 ? COLUMNS : 1];
+      // what is always in is above every cut, what is none below
+      const auto short_of = [&](uint64_t key) { return key == kAlways ? ~0u : key < lo ? 0 : (uint32_t)((key - lo) >> shift); };
+      if constexpr (COLUMNS > 0) {
+#pragma unroll
+        for (int c = 0; c < COLUMNS; ++c) short_keys[c] = c < columns ? short_of(mine[c]) : 0;
+      }
+      cut_range<WAYS>(p.K, count, lo32, hi32, [&](uint32_t x, uint32_t y, uint32_t z) {
+        int nx = 0, ny = 0, nz = 0;
+        each([&](uint64_t key, int c) {
+          const uint32_t k = COLUMNS > 0 ? short_keys[COLUMNS > 0 ? c : 0] : short_of(key);
+          ny += count_lanes(k >= y);
+          if constexpr (WAYS == 4) {
+            nx += count_lanes(k >= x);
+            nz += count_lanes(k >= z);
+          }
+        });
+        return total(nx, ny, nz);
+      });
+      hi = min(hi, lo + ((uint64_t)hi32 << shift) + (((uint64_t)1 << shift) - 1));
+      lo += (uint64_t)lo32 << shift;
+    }
+    cut_range<WAYS>(p.K, count, lo, hi, [&](uint64_t x, uint64_t y, uint64_t z) {
+      int nx = 0, ny = 0, nz = 0;
+      each([&](uint64_t key, int) {
+        ny += count_lanes(key >= y);
+        if constexpr (WAYS == 4) {
+          nx += count_lanes(key >= x);
+          nz += count_lanes(key >= z);
+        }
+      });
+      return total(nx, ny, nz);
+    });
+    least = lo;
+    surplus = count - p.K;
+  }
+  // before this wave's: what is taken, and how many of the keys equal to `least`
+  int before = 0, kept = 0;
+  if constexpr (SHARED) {
+    int n = 0, equal = 0;
+    each([&](uint64_t key, int) {
+      n += count_lanes(key >= least);
+      equal += count_lanes(key == least);
+    });
+    if (lane == 0) {
+      s.counts[turn][0][wave] = n;
+      s.counts[turn][1][wave] = equal;
+    }
+    __syncthreads();
+    // rows of 16 lanes: what is taken before this wave, ties before it, all ties
+    const int w = lane & 15, row = lane >> 4;
+    const int x = row_sum(w < (row == 2 ? WAVES : wave) ? s.counts[turn][row == 0 ? 0 : 1][w] : 0);
+    before = __builtin_amdgcn_readlane(x, 0);
+    const int equal_before = __builtin_amdgcn_readlane(x, 16), all_equal = __builtin_amdgcn_readlane(x, 32);
+    const int keep = all_equal - surplus;                  // of all ties, the first ones
+    before -= max(equal_before - keep, 0);
+    kept = max(keep - equal_before, 0);
+  } else if (surplus > 0) {
+    each([&](uint64_t key, int) { kept += count_lanes(key == least); });
+    kept -= surplus;
+  }
+  int32_t* to = list + before;
+  int at = 0;
+  each([&](uint64_t key, int c) {
+    const uint64_t below = ((uint64_t)1 << lane) - 1;
+    uint64_t in = __ballot(key >= least);
+    if (surplus > 0) {
+      const uint64_t ties = __ballot(key == least);
+      in &= ~ties | __ballot(__builtin_popcountll(ties & below) < kept);
+      kept -= __builtin_popcountll(ties);
+    }
+    if ((in >> lane & 1) != 0) to[at + __builtin_popcountll(in & below)] = 64 * (first + c) + lane;
+    at += __builtin_popcountll(in);
+  });
+  end_list<WAVES>(p, min(there, p.K), list, count_out);
+}
+
+extern __shared__ uint64_t lds_keys[];                     // p.lds_entries of them
 
 // One list a workgroup: all of its keys, then the selection among them.
 template <typename IO, int D>
 __global__ void __launch_bounds__(kThreads) gdn_attn_select_k(SelectArgs p) {
   __shared__ PickShared shared;
-  const int64_t lists = (int64_t)min(row_start(p.rows, p.rows.R), p.rows.N) * p.cache.Hk;
-  for (int64_t job = blockIdx.x; job < lists; job += gridDim.x) {
-    const int n = (int)(job / p.cache.Hk), h = (int)(job % p.cache.Hk);
-    const Token t = token_at(p, n, threadIdx.x & 63);
-    uint64_t* keys = p.keys + job * p.cache.max_pages;
-    score_entries<IO, D>(p, t, n, h, 0, t.held, keys);
+  __shared__ double parts[1][2][D];
+  const unsigned lists = (unsigned)min(row_start(p.rows, p.rows.R), p.rows.N) * (unsigned)p.cache.Hk;
+  for (unsigned job = blockIdx.x; job < lists; job += gridDim.x) {
+    const int n = (int)(job / (unsigned)p.cache.Hk), h = (int)job - n * p.cache.Hk;
+    const Token t = token_at(p, owner_of(p.rows, n, threadIdx.x & 63), n);
+    int32_t *list = p.pages + (int64_t)job * p.K, *count = h == 0 ? p.counts + n : nullptr;
+    uint64_t* keys = p.keys + (int64_t)job * p.cache.max_pages;
+    const bool in_lds = t.held <= p.lds_entries;
+    if (t.held > 0) {
+      sum_parts<IO, D, 1>(p, n, 1, h, parts);
+      Scorer<IO, D> s(p, t.table, h, 0, t.held);
+      __syncthreads();
+      s.take(parts[0]);
+      s.load();
+      do {
+        s.score([&](int at, int page, double x) { (in_lds ? lds_keys[at] : keys[at]) = entry_key(p, t.held, at, page, x); });
+      } while (s.advance());
+      __syncthreads();
+    }
+    if (!in_lds)
+      pick<kWaves, 0, true>(p, keys, t.held, list, count, shared);
+    else if (t.held > kFew)
+      pick<kWaves, kColumns, true>(p, lds_keys, t.held, list, count, shared);
+    else if (threadIdx.x < 64)
+      pick<1, kColumns, false>(p, lds_keys, t.held, list, count, shared);
     __syncthreads();
-    pick_entries(p, keys, t.held, p.pages + job * p.K, h == 0 ? p.counts + n : nullptr, shared);
+  }
+}
+
+// Long lists in two launches: the keys of p.chunk entries for TOKENS tokens a workgroup (those of one request
+// share the bounds that they read), then the selection.
+template <typename IO, int D, int TOKENS>
+__global__ void __launch_bounds__(kThreads) gdn_select_score_k(SelectArgs p) {
+  __shared__ double parts[TOKENS][2][D];
+  const int tokens = min(row_start(p.rows, p.rows.R), p.rows.N);
+  const unsigned jobs = ((unsigned)p.rows.N + TOKENS - 1) / TOKENS * (unsigned)p.cache.Hk;
+  for (unsigned job = blockIdx.x; job < jobs; job += gridDim.x) {
+    const unsigned group = job / (unsigned)p.cache.Hk;
+    const int h = (int)(job - group * p.cache.Hk), past = min((int)group * TOKENS + TOKENS, tokens);
+    int n = (int)group * TOKENS;
+    while (n < past) {
+      // the tokens from n on that are of one request: the last of them holds the most entries
+      const int r = owner_of(p.rows, n, threadIdx.x & 63);
+      const int count = min(past, row_start(p.rows, r + 1)) - n;
+      const Token t = token_at(p, r, n + count - 1);
+      // the last chunk takes what the host did not know of
+      const int i0 = min((int)blockIdx.y * p.chunk, t.held);
+      const int i1 = blockIdx.y == gridDim.y - 1 ? t.held : min(i0 + p.chunk, t.held);
+      if (i0 < i1) {
+        Scorer<IO, D> s(p, t.table, h, i0, i1);
+        s.load();
+        sum_parts<IO, D, TOKENS>(p, n, count, h, parts);
+        __syncthreads();
+        if (TOKENS == 1) s.take(parts[0]);
+        do {
+#pragma unroll 1
+          for (int j = 0; j < (TOKENS == 1 ? 1 : count); ++j) {
+            if (TOKENS > 1) {
+              s.forget();
+              s.take(parts[j]);
+            }
+            const int held = held_at(p, t.pos - (count - 1 - j));
+            uint64_t* keys = p.keys + ((int64_t)(n + j) * p.cache.Hk + h) * p.cache.max_pages;
+            s.score([&](int at, int page, double x) {
+              if (at < held) keys[at] = entry_key(p, held, at, page, x);
+            });
+          }
+        } while (s.advance());
+        __syncthreads();                                   // parts are written again
+      }
+      n += count;
+    }
+  }
+}
+
+template <int WAVES>
+__global__ void __launch_bounds__(64 * WAVES) gdn_select_pick_k(SelectArgs p) {
+  __shared__ PickShared shared;
+  const unsigned lists = (unsigned)min(row_start(p.rows, p.rows.R), p.rows.N) * (unsigned)p.cache.Hk;
+  for (unsigned job = blockIdx.x; job < lists; job += gridDim.x) {
+    const int n = (int)(job / (unsigned)p.cache.Hk);
+    const Token t = token_at(p, owner_of(p.rows, n, threadIdx.x & 63), n);
+    int32_t *list = p.pages + (int64_t)job * p.K, *count = (int)job == n * p.cache.Hk ? p.counts + n : nullptr;
+    const uint64_t* keys = p.keys + (int64_t)job * p.cache.max_pages;
+    if (t.held > kFew * WAVES)
+      pick<WAVES, 0, true>(p, keys, t.held, list, count, shared);
+    else if (WAVES > 1 && t.held > kFew)
+      pick<WAVES, kColumns, true>(p, keys, t.held, list, count, shared);
+    else if (threadIdx.x < 64)
+      pick<1, kColumns, false>(p, keys, t.held, list, count, shared);
     __syncthreads();
   }
 }
@@ -434,11 +666,41 @@ hipError_t launch_bounds_io(const BoundsArgs& p, hipStream_t stream) {
   }
 }
 
+unsigned blocks_of(int64_t jobs) { return (unsigned)(jobs < kMostBlocks ? jobs : kMostBlocks); }
+
+constexpr int kMostLds = kFew * kWaves;   // keys of a list in LDS: what its workgroup's waves hold
+
+// One launch where lists are short and few, so that their latency counts, two where they are split over workgroups or
+// fill the device anyway. Measured, one against two, 8 key heads of 128 fp16 (bounds of 512 bytes): a request of 64
+// pages 5.6 and 7.5 us, 64 of them 9.3 and 11.5, 256 of them 27.7 and 22.6; 64 of up to 256 pages 13.6 and 15.0; one
+// of 2,048 37 and 12, 16 of 1,024 28 and 22, 64 of 512 36 and 39.
+constexpr int kShort = 256, kFewLists = 1024;
+
 template <typename IO, int D>
-hipError_t launch_select_d(const SelectArgs& p, hipStream_t stream) {
+hipError_t launch_select_d(SelectArgs p, hipStream_t stream) {
   const int64_t lists = (int64_t)p.rows.N * p.cache.Hk;
-  const dim3 grid((unsigned)(lists < kMostBlocks ? lists : kMostBlocks));
-  hipLaunchKernelGGL((gdn_attn_select_k<IO, D>), grid, dim3(kThreads), 0, stream, p);
+  p.lds_entries = p.max_held < kMostLds ? p.max_held : kMostLds;
+  if (p.max_held <= kShort && lists <= kFewLists) {
+    hipLaunchKernelGGL((gdn_attn_select_k<IO, D>), dim3(blocks_of(lists)), dim3(kThreads), p.lds_entries * sizeof(uint64_t),
+                       stream, p);
+    return hipGetLastError();
+  }
+  // entries of a workgroup: 64 at least (what its lanes have on their way at once), about 1,024 workgroups
+  const int64_t share = (lists * p.max_held / 1024 + 63) / 64 * 64, fits = (p.max_held + 32767) / 32768;
+  p.chunk = (int)(share > 64 ? (share < (1 << 30) ? share : 1 << 30) : 64);
+  if (p.chunk < fits) p.chunk = (int)fits;
+  const int64_t jobs = ((int64_t)p.rows.N + p.group_tokens - 1) / p.group_tokens * p.cache.Hk;
+  const dim3 grid(blocks_of(jobs), (unsigned)((p.max_held + p.chunk - 1) / p.chunk));
+  if (p.group_tokens == 1)
+    hipLaunchKernelGGL((gdn_select_score_k<IO, D, 1>), grid, dim3(kThreads), 0, stream, p);
+  else
+    hipLaunchKernelGGL((gdn_select_score_k<IO, D, kSelectGroup>), grid, dim3(kThreads), 0, stream, p);
+  if (p.max_held <= kFew)
+    hipLaunchKernelGGL(gdn_select_pick_k<1>, dim3(blocks_of(lists)), dim3(64), 0, stream, p);
+  else if (p.max_held <= 4 * kFew)
+    hipLaunchKernelGGL(gdn_select_pick_k<4>, dim3(blocks_of(lists)), dim3(256), 0, stream, p);
+  else
+    hipLaunchKernelGGL(gdn_select_pick_k<16>, dim3(blocks_of(lists)), dim3(1024), 0, stream, p);
   return hipGetLastError();
 }
 
