@@ -465,8 +465,10 @@ int gdn_kv_bounds(const gdn_kv_params* p, const gdn_kv_tensors* t, const gdn_kv_
   if (pages_collide(w, *c)) return GDN_ERR_ALIAS;
   gdn::BoundsArgs a{};
   a.bounds = bounds;
-  // a page holds 16 tokens at least: of a prompt's, one workgroup looks at 16, of a decode step's at one
-  a.tokens_per_block = N > 4096 ? 16 : 1;
+  // a request's T tokens lie on T pages at most, and on (T - 1) / page_size + 2
+  const int64_t slots = std::min(N, N / c->page_size + 2 * R);
+  if (slots * Hk > std::numeric_limits<int32_t>::max()) return GDN_ERR_SHAPE;
+  a.slots = (int32_t)slots;
   a.cache = cache_args(*c);
   a.rows = row_args(w);
   return status_of(gdn::launch_bounds(a, c->io_dtype, static_cast<hipStream_t>(stream)));

@@ -82,7 +82,7 @@ struct ReadArgs {
 // Channel bounds of the pages that hold a call's tokens.
 struct BoundsArgs {
   void* bounds;                 // [P, Hk, 2, D] io: lowest, highest
-  int32_t tokens_per_block;
+  int32_t slots;                // pages at most
   CacheArgs cache;
   RowArgs rows;
 };

@@ -69,6 +69,51 @@ def test_bounds_of_prompts_of_many_tokens():
         assert np.array_equal(_run_bounds(c, T, old, N=4800, mirrors=False).astype(np.float64), want)    # a padded batch
 
 
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_bounds_of_many_pages(fmt, D):
+    """Enough short pages for a wave each."""
+    lens, T = [1500, 3, 1, 900, 40], [1500, 2, 1, 890, 17]
+    _case(f"bounds of many pages {fmt} D={D}")
+    for page, Hk in ((16, 8), (32, 16)):
+        c = any_cache(lens, fmt=fmt, Hk=Hk, D=D, page=page, seed=1)
+        old = queries(c["P"] * Hk, 2, D, fmt, 3).reshape(c["P"], Hk, 2, D)
+        want = SO.bounds(c["k"], c["table"], cu_of(T), lens, old)
+        assert np.array_equal(_run_bounds(c, T, old).astype(np.float64), want)
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "e2m1"])
+def test_bounds_of_every_code(fmt):
+    """Every code beside every exponent byte that a cache holds, one key a page: what gdn_kv_read gives for it."""
+    _case(f"bounds of every code {fmt}")
+    scales = np.array([0, *range(95, 136)] if fmt == "e4m3" else [0, *range(101, 141), 255], np.uint8)
+    R, D = len(scales), 256
+    c = any_cache([1] * R, fmt=fmt, Hk=1, D=D, page=16, seed=0)
+    page = c["table"][:, 0]
+    codes = np.arange(256, dtype=np.uint8) if fmt == "e4m3" else np.arange(128, dtype=np.uint8) * 2 + 1
+    c["k_codes"][page, 0, 0] = codes
+    if fmt == "e4m3":
+        c["k_scales"][page, 0, 0] = scales
+    else:
+        c["k_scales"][page, 0, :, 0] = scales[:, None]
+    if fmt == "e2m1":
+        c["k_codes"][page[0], 0, 0] = 0                      # a block of scale 0 is zero
+    else:
+        c["k_codes"][page[0], 0, 0] = np.where((codes & 127) == 127, codes, 0)
+    old = np.zeros((c["P"], 1, 2, D), np.float16)
+    got = _run_bounds(c, [1] * R, old, dense=True)[page, 0]
+    k, v = (torch.empty((R, 1, D), dtype=torch.float16, device="cuda") for _ in range(2))
+    gdn.gdn_kv_read(k, v, any_device_cache(c, torch, gdn), dev(c["lens"], torch))
+    want = k.cpu().numpy()[:, 0]
+    with np.errstate(over="ignore"):
+        exact = AO.dequantise(c["k_codes"][page, 0, 0], scales) if fmt == "e4m3" else \
+            SO.dequantise(SO.unpack(c["k_codes"][page, 0, 0]), np.repeat(scales[:, None], D // 32, 1))
+        half = exact.astype(np.float16)
+    inside = (np.abs(exact) >= 2.0 ** -24) | (exact == 0) | np.isnan(exact)
+    assert np.array_equal(np.where(inside, want, 0), np.where(inside, half, 0), equal_nan=True)
+    assert np.array_equal(got[:, 0], want, equal_nan=True) and np.array_equal(got[:, 1], want, equal_nan=True)
+
+
 def test_bounds_without_pages_and_with_nan_keys():
     c = any_cache([50, 33, 20], fmt="f16", Hk=2, D=64, page=16, seed=2)
     _case("bounds: no page, NaN, infinity")
