@@ -13,8 +13,9 @@ hipError_t launch_attn(const AttnArgs& p, int io_dtype, void* workspace, hipStre
 
 size_t attn_workspace_bytes(int64_t N, int64_t R, int Hq, int Hk, int D, int format) {
   if (N == 0 || R == 0) return 0;
-  const int groups = D == 64 || format == kCacheE2M1 ? kMostGroups : kGroups;
-  return kNoteBytes + (size_t)2 * groups * part_rows(N, Hq / Hk) * (D + 2) * sizeof(float);
+  const int rows = part_rows(N, Hq / Hk);
+  if (format == kCacheE2M1) return kNoteBytes4 + (size_t)2 * kMostGroups4 * rows * (D + 2) * sizeof(float);
+  return kNoteBytes + (size_t)2 * (D == 64 ? kMostGroups : kGroups) * rows * (D + 2) * sizeof(float);
 }
 
 }  // namespace gdn

@@ -62,6 +62,7 @@ constexpr int kMostLines = 8;             // see block_of
 // lose (128 requests of 1 .. 4 drafts, 64 columns in 8 bits, 28 and 32 us).
 constexpr int kOneEach = 1024;
 constexpr int kSegmentBytes = 200000;
+constexpr int kSegmentBytes4 = 30000;     // of 4-bit pages: 256 of 90 .. 700, D = 128, 39.8 us, with 200,000 43.9
 constexpr int64_t kMostShared = 1 << 22;
 constexpr int kWholeShift = 30;           // one unit per segment: nothing is split
 constexpr int kGroups = 256;              // workgroups of a split launch: one per CU
@@ -442,8 +443,12 @@ struct Shape {
   static constexpr int kSetBytes = kCols * kBits / 8;                    // of a set in one position
   static constexpr int kVWords = (kSetBytes + 3) / 4;                    // dwords of it
   static constexpr int kTileBytes = 2 * kTile * kRow;                    // of k and v
-  // tiles a wave has in flight: 128 KiB a workgroup, at most 4
-  static constexpr int kAhead = 131072 / WAVES / kTileBytes < 4 ? 131072 / WAVES / kTileBytes : 4;
+  // tiles a wave has in flight: 128 KiB a workgroup, at most 4. With 4 bits one: they are bound by what is done with
+  // them, and more waves with fewer registers, in a loop of a quarter of the code, do that sooner (with 1, 2 and 4:
+  // 64 requests of up to 16,384 positions, D = 128, 99, 101 and 114 us, D = 64 71, 78 and 88; 16 x 4 drafts of 6 heads
+  // over 8,192, D = 256, 36, 38 and 43).
+  static constexpr int kMostAhead = FMT == kE2M1 ? 1 : 4;
+  static constexpr int kAhead = 131072 / WAVES / kTileBytes < kMostAhead ? 131072 / WAVES / kTileBytes : kMostAhead;
   static constexpr int kPitch = D + 4;                                   // floats between rows in LDS
 };
 
@@ -858,54 +863,59 @@ __global__ void __launch_bounds__(64 * WAVES, 1) gdn_attn_k(Args<LISTS> p, Split
                   acc[r][4 * c + e] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(vw[u][i][c][e]), wgt[r][i],
                                                                            acc[r][4 * c + e], 0, 0, 0);
         } else {
-          float vs[8];                                     // e2m1: scales of this lane's columns
-          if constexpr (FMT == kE2M1) {
+          // 32 positions a product
 #pragma unroll
-            for (int i = 0; i < 8; ++i) vs[i] = __uint_as_float(((vscale[u][i >> 2] >> (8 * (i & 3))) & 255u) << 23);
-          }
-          uint4_t pw[TILES], pl[TILES];
+          for (int b = 0; b < S::kPos; b += 8) {
+            float vs[8];                                   // e2m1: scales of this lane's columns
+            if constexpr (FMT == kE2M1) {
 #pragma unroll
-          for (int r = 0; r < TILES; ++r)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const HalfPair w = split_weights(wgt[r][2 * i], wgt[r][2 * i + 1]);
-              pw[r][i] = w.hi;
-              pl[r][i] = w.lo;
+              for (int i = 0; i < 8; ++i) vs[i] = __uint_as_float(((vscale[u][(b + i) >> 2] >> (8 * (i & 3))) & 255u) << 23);
             }
+            uint4_t pw[TILES], pl[TILES];
 #pragma unroll
-          for (int c = 0; c < S::kSets; ++c)
-#pragma unroll
-            for (int k = 0; k < S::kCols / 2; ++k) {     // two columns at a time
-              uint32_t pair[8];
-#pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                if constexpr (FMT == kF16)
-                  pair[i] = vw[u][i][c][k];
-                else if constexpr (FMT == kE2M1)
-                  pair[i] = (k & 3) == 0   ? nibbles_to_half2<0>(vw[u][i][c][k >> 2], vs[i])
-                            : (k & 3) == 1 ? nibbles_to_half2<1>(vw[u][i][c][k >> 2], vs[i])
-                            : (k & 3) == 2 ? nibbles_to_half2<2>(vw[u][i][c][k >> 2], vs[i])
-                                           : nibbles_to_half2<3>(vw[u][i][c][k >> 2], vs[i]);
-                else
-                  pair[i] = (k & 1) ? codes_to_half2<true>(vw[u][i][c][k >> 1]) : codes_to_half2<false>(vw[u][i][c][k >> 1]);
-              }
-              uint4_t a0, a1;
+            for (int r = 0; r < TILES; ++r)
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
-                a0[i] = __builtin_amdgcn_perm(pair[2 * i + 1], pair[2 * i], 0x05040100u);
-                a1[i] = __builtin_amdgcn_perm(pair[2 * i + 1], pair[2 * i], 0x07060302u);
+                const HalfPair w = split_weights(wgt[r][b + 2 * i], wgt[r][b + 2 * i + 1]);
+                pw[r][i] = w.hi;
+                pl[r][i] = w.lo;
               }
-              const int o = S::kCols * c + 2 * k;
 #pragma unroll
-              for (int r = 0; r < TILES; ++r) {
-                const half8_t v0 = __builtin_bit_cast(half8_t, a0), v1 = __builtin_bit_cast(half8_t, a1);
-                const half8_t hi = __builtin_bit_cast(half8_t, pw[r]), lo = __builtin_bit_cast(half8_t, pl[r]);
-                acc[r][o] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v0, hi, acc[r][o], 0, 0, 0);
-                acc[r][o + 1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v1, hi, acc[r][o + 1], 0, 0, 0);
-                acc[r][o] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v0, lo, acc[r][o], 0, 0, 0);
-                acc[r][o + 1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v1, lo, acc[r][o + 1], 0, 0, 0);
+            for (int c = 0; c < S::kSets; ++c)
+#pragma unroll
+              for (int k = 0; k < S::kCols / 2; ++k) {     // two columns at a time
+                uint32_t pair[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                  const uint32_t(&w)[S::kVWords] = vw[u][b + i][c];
+                  if constexpr (FMT == kF16)
+                    pair[i] = w[k];
+                  else if constexpr (FMT == kE2M1)
+                    pair[i] = (k & 3) == 0   ? nibbles_to_half2<0>(w[k >> 2], vs[i])
+                              : (k & 3) == 1 ? nibbles_to_half2<1>(w[k >> 2], vs[i])
+                              : (k & 3) == 2 ? nibbles_to_half2<2>(w[k >> 2], vs[i])
+                                             : nibbles_to_half2<3>(w[k >> 2], vs[i]);
+                  else
+                    pair[i] = (k & 1) ? codes_to_half2<true>(w[k >> 1]) : codes_to_half2<false>(w[k >> 1]);
+                }
+                uint4_t a0, a1;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  a0[i] = __builtin_amdgcn_perm(pair[2 * i + 1], pair[2 * i], 0x05040100u);
+                  a1[i] = __builtin_amdgcn_perm(pair[2 * i + 1], pair[2 * i], 0x07060302u);
+                }
+                const int o = S::kCols * c + 2 * k;
+#pragma unroll
+                for (int r = 0; r < TILES; ++r) {
+                  const half8_t v0 = __builtin_bit_cast(half8_t, a0), v1 = __builtin_bit_cast(half8_t, a1);
+                  const half8_t hi = __builtin_bit_cast(half8_t, pw[r]), lo = __builtin_bit_cast(half8_t, pl[r]);
+                  acc[r][o] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v0, hi, acc[r][o], 0, 0, 0);
+                  acc[r][o + 1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v1, hi, acc[r][o + 1], 0, 0, 0);
+                  acc[r][o] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v0, lo, acc[r][o], 0, 0, 0);
+                  acc[r][o + 1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v1, lo, acc[r][o + 1], 0, 0, 0);
+                }
               }
-            }
+          }
         }
         if (__builtin_expect(mixed, 0)) {
           // the values left out above, for the rows that attend them: position by position, element by
@@ -1124,16 +1134,18 @@ constexpr int many_waves() {
 // Workgroups of a split launch: one per CU keeps the waves' shares equal in time (of two
 // on a CU the older one's loads go first: 64 requests of 8,192 positions, D = 128, the
 // first 256 workgroups were done after 230 us and the others after 313), two where a
-// wave's tiles in flight are small (8-bit heads of 64: 222 -> 195 us).
-template <int FMT, int D>
+// wave's tiles in flight are small (8-bit heads of 64: 222 -> 195 us), and with 4 bits as
+// many as the registers, or for two row tiles of 256 columns the LDS, let in.
+template <int FMT, int D, int TILES>
 constexpr int split_groups() {
+  if (FMT == kE2M1) return (TILES == 1 ? (D == 64 ? 4 : D == 128 ? 3 : 2) : D == 256 ? 1 : 2) * kGroups;
   typedef Shape<FMT, D, 4> S;
   return 4 * S::kAhead * S::kTileBytes < 131072 ? 2 * kGroups : kGroups;
 }
-constexpr int kMostGroups = 2 * kGroups;
+constexpr int kMostGroups = 2 * kGroups, kMostGroups4 = 4 * kGroups;   // of a 4-bit cache
 
-// Notes: two int4 each, one a workgroup or segment, at most kMostGroups.
-constexpr size_t kNoteBytes = (size_t)kMostGroups * 2 * sizeof(int4);
+// Notes: two int4 each, one a workgroup or segment, at most the workgroups.
+constexpr size_t kNoteBytes = (size_t)kMostGroups * 2 * sizeof(int4), kNoteBytes4 = (size_t)kMostGroups4 * 2 * sizeof(int4);
 
 // Rows of a part: a segment's, of at most kTiles tiles.
 int part_rows(int64_t N, int group) {
@@ -1148,10 +1160,14 @@ int part_rows(int64_t N, int group) {
 // may take before the others wait for it. Measured, whole against split: 64 requests of
 // 1,000 positions, 8 key heads of 128 fp16 47 and 49 us, 16 of 600 13 and 18, one of 333
 // 8.3 and 9.4, of 700 12.7 and 9.3, 4 of 1,000 in 8 bits 14.3 and 10.8; 16 of 2,048 with
-// 4 heads 28 and 18 us. Without the host's lengths the sum is not known and counts as
+// 4 heads 28 and 18 us. 4-bit pages are taken in at 110 to 160 positions a us, of any
+// width: one of 1,000, 8 heads of 128, 12.1 and 8.5 us, 64 of 2,000 29.6 and 34.4; 64 of
+// 1,000, 4 heads of 256, 17.4 and 21.1. Without the host's lengths the sum is not known and counts as
 // nothing.
-bool one_group_each(int64_t longest, int64_t sum, int heads, int64_t position_bytes, bool eight_bits) {
-  const double alone = (double)longest * position_bytes / (eight_bits ? 29e3 : 47e3);
+template <int FMT, int D>
+bool one_group_each(int64_t longest, int64_t sum, int heads, int64_t position_bytes) {
+  constexpr double kRate = FMT == kE2M1 ? (D == 256 ? 29e3 : D == 128 ? 20e3 : 10e3) : FMT == kE4M3 ? 29e3 : 47e3;
+  const double alone = (double)longest * position_bytes / kRate;
   const double together = (double)sum * heads * position_bytes / 6.4e6;
   return alone <= together / 2 + 5.0;
 }
@@ -1175,7 +1191,7 @@ hipError_t launch_attn_d(const Args<LISTS>& p, void* workspace, hipStream_t stre
   static_assert(kRows == 16 && kTiles == 2, "see seg_shift");
   const int64_t segments = ((most <= seg_rows ? 0 : (int64_t)p.rows.N * p.group / seg_rows) + p.rows.R) * p.cache.Hk;
   int64_t groups = segments;
-  const bool whole = one_group_each(p.max_len, p.sum_len, p.cache.Hk, 2 * Shape<FMT, D, 4>::kRow, FMT == kE4M3 || FMT == kE2M1);
+  const bool whole = one_group_each<FMT, D>(p.max_len, p.sum_len, p.cache.Hk, 2 * Shape<FMT, D, 4>::kRow);
   int64_t notes = 0;
   int64_t cap = (int64_t)p.cache.max_pages << p.cache.page_shift;
   if constexpr (LISTS) cap = (int64_t)p.list_len << p.cache.page_shift;
@@ -1185,13 +1201,14 @@ hipError_t launch_attn_d(const Args<LISTS>& p, void* workspace, hipStream_t stre
   } else if (whole) {
     groups = 2 * kGroups;
     sp.chunk_shift = 5;
-    sp.whole = kSegmentBytes / (32 * 2 * Shape<FMT, D, 4>::kRow);
+    sp.whole = (FMT == kE2M1 ? kSegmentBytes4 : kSegmentBytes) / (32 * 2 * Shape<FMT, D, 4>::kRow);
     while (segments * ((cap >> sp.chunk_shift) + 1 + sp.whole) > ((int64_t)1 << 30)) ++sp.chunk_shift;
   } else {
-    static_assert(D == 64 || FMT == kE2M1 || split_groups<FMT, D>() == kGroups, "see attn_workspace_bytes");
-    groups = split_groups<FMT, D>();
+    static_assert(FMT == kE2M1 || split_groups<FMT, D, 1>() == (D == 64 ? split_groups<FMT, 64, 1>() : kGroups),
+                  "see attn_workspace_bytes");
+    groups = few ? split_groups<FMT, D, 1>() : split_groups<FMT, D, kTiles>();
     sp.notes = static_cast<int4*>(workspace);
-    sp.parts = reinterpret_cast<float*>(static_cast<char*>(workspace) + kNoteBytes);
+    sp.parts = reinterpret_cast<float*>(static_cast<char*>(workspace) + (FMT == kE2M1 ? kNoteBytes4 : kNoteBytes));
     sp.part_rows = few ? kRows : part_rows(p.rows.N, p.group);
     sp.chunk_shift = kChunkShift;
     while (segments * ((cap >> sp.chunk_shift) + 1) > ((int64_t)1 << 30)) ++sp.chunk_shift;
