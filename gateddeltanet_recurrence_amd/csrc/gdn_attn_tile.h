@@ -531,13 +531,15 @@ struct Pages {
   __device__ __forceinline__ int64_t row(int page, int pos) const {
     return (((int64_t)max(page, 0) * p.cache.Hk + h) << p.cache.page_shift) + (pos & ((1 << p.cache.page_shift) - 1));
   }
-  // Rows of the block that exist: up to `end`, none without a page. Scalar, so that the resources made of it are.
-  __device__ __forceinline__ int rows(int page, int pos) const {
-    return __builtin_amdgcn_readfirstlane(page >= 0 ? min(max((LISTS ? newest : end) - pos, 0), 16) : 0);
+  // Rows of the block (or run of blocks) that exist: up to `end`, none without a page. Scalar, so that the resources made of it are.
+  __device__ __forceinline__ int rows(int page, int pos, int most) const {
+    return __builtin_amdgcn_readfirstlane(page >= 0 ? min(max((LISTS ? newest : end) - pos, 0), most) : 0);
   }
 };
 
-template <int FMT, int D, int WAVES, int TILES, bool LISTS>
+// WIDE: pages hold a whole tile (its two blocks share one look-up and one set of resources: with 4 bits, where the
+// scalar unit's share of the time shows, and pages of 32 or more).
+template <int FMT, int D, int WAVES, int TILES, bool LISTS, bool WIDE>
 __global__ void __launch_bounds__(64 * WAVES, 1) gdn_attn_k(Args<LISTS> p, SplitArgs sp) {
   typedef Shape<FMT, D, WAVES> S;
   typedef typename std::conditional<FMT == kF32, float, _Float16>::type IO;
@@ -575,19 +577,20 @@ __global__ void __launch_bounds__(64 * WAVES, 1) gdn_attn_k(Args<LISTS> p, Split
   uint32_t kscale[U][S::kBlocks][kScaleLoads], vscale[U][S::kBlocks];
   // table entries of the next tile, pages of this one; with lists the entries' numbers of the one after, and how many
   // positions a block of this one holds
-  int entry[U][S::kBlocks], held[U][S::kBlocks];
-  int pick[U][S::kBlocks], first_pos[U][S::kBlocks], block_pos[U][S::kBlocks], there_of[U][S::kBlocks];
+  constexpr int kRun = WIDE ? S::kBlocks : 1, kFind = S::kBlocks / kRun;   // blocks that are looked up together, look-ups
+  int entry[U][kFind], held[U][kFind];
+  int pick[U][kFind], first_pos[U][kFind], block_pos[U][kFind], there_of[U][kFind];
   const int pos_mask = (1 << p.cache.page_shift) - 1;
   constexpr int kStep = WAVES * S::kTile;
   auto look_up = [&](int u, int t) {
 #pragma unroll
-    for (int a = 0; a < S::kBlocks; ++a) {
+    for (int a = 0; a < kFind; ++a) {
       if constexpr (LISTS) {
-        first_pos[u][a] = pages.first(pick[u][a], t + 16 * a);
+        first_pos[u][a] = pages.first(pick[u][a], t + 16 * kRun * a);
         entry[u][a] = pages.entry(first_pos[u][a]);
-        pick[u][a] = pages.listed(t + U * kStep + 16 * a);
+        pick[u][a] = pages.listed(t + U * kStep + 16 * kRun * a);
       } else {
-        entry[u][a] = pages.entry(t + 16 * a);
+        entry[u][a] = pages.entry(t + 16 * kRun * a);
       }
     }
   };
@@ -598,10 +601,10 @@ __global__ void __launch_bounds__(64 * WAVES, 1) gdn_attn_k(Args<LISTS> p, Split
   };
   auto load_k = [&](int u, int t) {
 #pragma unroll
-    for (int a = 0; a < S::kBlocks; ++a) {
-      const int pos = LISTS ? first_pos[u][a] : t + 16 * a, page = pages.page(entry[u][a], pos);
+    for (int a = 0; a < kFind; ++a) {
+      const int pos = LISTS ? first_pos[u][a] : t + 16 * kRun * a, page = pages.page(entry[u][a], pos);
       const int64_t row = pages.row(page, pos);
-      const int count = pages.rows(page, pos);
+      const int count = pages.rows(page, pos, 16 * kRun);
       held[u][a] = page;
       if constexpr (LISTS) {
         block_pos[u][a] = pos;
@@ -609,33 +612,45 @@ __global__ void __launch_bounds__(64 * WAVES, 1) gdn_attn_k(Args<LISTS> p, Split
       }
       const rsrc_t rs = make_rsrc(static_cast<const char*>(p.cache.k) + row * S::kRow, count * S::kRow);
 #pragma unroll
-      for (int c = 0; c < S::kKLoads; ++c) load_words<0, 4>(rs, k_at + 64 * c, kw[u][a][c]);
+      for (int b = 0; b < kRun; ++b)
+#pragma unroll
+        for (int c = 0; c < S::kKLoads; ++c) load_words<0, 4>(rs, k_at + 64 * c + 16 * b * S::kRow, kw[u][kRun * a + b][c]);
       if constexpr (FMT == kE4M3)
         kscale[u][a][0] = __builtin_amdgcn_raw_buffer_load_b32(make_rsrc(p.cache.k_scales + row, count > 0 ? 16 : 0), 4 * g, 0, 0);
       if constexpr (FMT == kE2M1) {
         // of row n, the block that holds this lane's elements
         const rsrc_t ss = scales_of(p.cache.k_scales, row, count);
 #pragma unroll
-        for (int c = 0; c < S::kKLoads; ++c)
-          kscale[u][a][c] = __builtin_amdgcn_raw_buffer_load_b8(ss, ((4 * c + g * S::kKWords / 4) << p.cache.page_shift) + n, 0, 0);
+        for (int b = 0; b < kRun; ++b)
+#pragma unroll
+          for (int c = 0; c < S::kKLoads; ++c)
+            kscale[u][kRun * a + b][c] = __builtin_amdgcn_raw_buffer_load_b8(
+                ss, ((4 * c + g * S::kKWords / 4) << p.cache.page_shift) + n + 16 * b, 0, 0);
       }
     }
   };
   auto load_v = [&](int u, int t) {
 #pragma unroll
-    for (int a = 0; a < S::kBlocks; ++a) {
-      const int pos = LISTS ? block_pos[u][a] : t + 16 * a, page = held[u][a];
+    for (int a = 0; a < kFind; ++a) {
+      const int pos = LISTS ? block_pos[u][a] : t + 16 * kRun * a, page = held[u][a];
       const int64_t row = pages.row(page, pos);
-      const int count = pages.rows(page, pos);
+      const int count = pages.rows(page, pos, 16 * kRun);
       const rsrc_t rs = make_rsrc(static_cast<const char*>(p.cache.v) + row * S::kRow, count * S::kRow);
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
+      for (int b = 0; b < kRun; ++b)
 #pragma unroll
-        for (int c = 0; c < S::kSets; ++c)
-          load_words<kStream, S::kSetBytes == 2 ? 2 : 4>(rs, v_at + e * S::kRow + 16 * S::kSetBytes * c, vw[u][4 * a + e][c]);
-      if constexpr (FMT == kE2M1)                          // of this lane's 4 positions, the block that holds its columns
-        vscale[u][a] = __builtin_amdgcn_raw_buffer_load_b32(scales_of(p.cache.v_scales, row, count),
-                                                            ((n * S::kCols / 32) << p.cache.page_shift) + 4 * g, 0, 0);
+        for (int e = 0; e < 4; ++e)
+#pragma unroll
+          for (int c = 0; c < S::kSets; ++c)
+            load_words<kStream, S::kSetBytes == 2 ? 2 : 4>(rs, v_at + (16 * b + e) * S::kRow + 16 * S::kSetBytes * c,
+                                                           vw[u][4 * (kRun * a + b) + e][c]);
+      if constexpr (FMT == kE2M1) {                        // of this lane's 4 positions, the block that holds its columns
+        const rsrc_t ss = scales_of(p.cache.v_scales, row, count);
+#pragma unroll
+        for (int b = 0; b < kRun; ++b)
+          vscale[u][kRun * a + b] = __builtin_amdgcn_raw_buffer_load_b32(
+              ss, ((n * S::kCols / 32) << p.cache.page_shift) + 4 * g + 16 * b, 0, 0);
+      }
       if constexpr (FMT == kE4M3)
         vscale[u][a] = __builtin_amdgcn_raw_buffer_load_b32(make_rsrc(p.cache.v_scales + row, count > 0 ? 16 : 0), 4 * g, 0, 0);
     }
@@ -650,7 +665,7 @@ __global__ void __launch_bounds__(64 * WAVES, 1) gdn_attn_k(Args<LISTS> p, Split
 #pragma unroll
       for (int u = 0; u < U; ++u)
 #pragma unroll
-        for (int a = 0; a < S::kBlocks; ++a) pick[u][a] = pages.listed(t + u * kStep + 16 * a);
+        for (int a = 0; a < kFind; ++a) pick[u][a] = pages.listed(t + u * kStep + 16 * kRun * a);
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) look_up(u, t + u * kStep);
@@ -747,15 +762,16 @@ __global__ void __launch_bounds__(64 * WAVES, 1) gdn_attn_k(Args<LISTS> p, Split
             }
           }
         }
-        int page[S::kBlocks];                              // of this tile: the next one's are looked up below
-        int in_block[S::kBlocks];                          // with lists, the positions of it that exist
+        int page[kFind];                                   // of this tile: the next one's are looked up below
+        int in_run[kFind];                                 // with lists, the positions of it that exist
         uint32_t ks[S::kBlocks];
 #pragma unroll
-        for (int a = 0; a < S::kBlocks; ++a) {
+        for (int a = 0; a < kFind; ++a) {
           page[a] = held[u][a];
-          in_block[a] = LISTS ? there_of[u][a] : 16;
-          ks[a] = FMT == kE4M3 ? kscale[u][a][0] : 0;
+          in_run[a] = LISTS ? there_of[u][a] : 16 * kRun;
         }
+#pragma unroll
+        for (int a = 0; a < S::kBlocks; ++a) ks[a] = FMT == kE4M3 ? kscale[u][a][0] : 0;
         // not before the products above: the loads then need registers of their own, and copies that wait
         // for them
         __builtin_amdgcn_sched_barrier(0);
@@ -784,13 +800,14 @@ __global__ void __launch_bounds__(64 * WAVES, 1) gdn_attn_k(Args<LISTS> p, Split
         // ---- masks, where some row does not attend all of the tile, or part of it has no page
         bool whole = t >= rw[0].lo_max && t + S::kTile <= rw[0].hi_min && t + S::kTile <= end;
 #pragma unroll
-        for (int a = 0; a < S::kBlocks; ++a) whole = whole && (LISTS ? in_block[a] == 16 : page[a] >= 0);
+        for (int a = 0; a < kFind; ++a) whole = whole && (LISTS ? in_run[a] == 16 * kRun : page[a] >= 0);
         bool mixed = false;                                // a non-finite value that only some rows attend
         if (__builtin_expect(!whole, 0)) {
 #pragma unroll
           for (int i = 0; i < S::kPos; ++i) {
             const int pos = t + 16 * (i >> 2) + 4 * g + (i & 3);
-            const bool there = LISTS ? 4 * g + (i & 3) < in_block[i >> 2] : page[i >> 2] >= 0 && pos < end;
+            const int run = (i >> 2) / kRun;
+            const bool there = LISTS ? 16 * ((i >> 2) % kRun) + 4 * g + (i & 3) < in_run[run] : page[run] >= 0 && pos < end;
 #pragma unroll
             for (int r = 0; r < TILES; ++r)
               if (!(there && pos >= lo[r] && pos < hi[r])) xs[r][i] = -INFINITY;
@@ -1172,13 +1189,16 @@ bool one_group_each(int64_t longest, int64_t sum, int heads, int64_t position_by
   return alone <= together / 2 + 5.0;
 }
 
-template <int FMT, int D, int TILES, bool LISTS>
+template <int FMT, int D, int TILES, bool LISTS, bool WIDE>
 void launch_few(const Args<LISTS>& p, const SplitArgs& sp, int groups, hipStream_t stream) {
+  if constexpr (FMT == kE2M1 && !WIDE) {
+    if (p.cache.page_shift >= 5) return launch_few<FMT, D, TILES, LISTS, true>(p, sp, groups, stream);
+  }
   constexpr int kMany = many_waves<FMT, D, TILES>();
   if (groups <= kGroups)
-    hipLaunchKernelGGL((gdn_attn_k<FMT, D, kMany, TILES, LISTS>), dim3((unsigned)groups), dim3(64 * kMany), 0, stream, p, sp);
+    hipLaunchKernelGGL((gdn_attn_k<FMT, D, kMany, TILES, LISTS, WIDE>), dim3((unsigned)groups), dim3(64 * kMany), 0, stream, p, sp);
   else
-    hipLaunchKernelGGL((gdn_attn_k<FMT, D, 4, TILES, LISTS>), dim3((unsigned)groups), dim3(256), 0, stream, p, sp);
+    hipLaunchKernelGGL((gdn_attn_k<FMT, D, 4, TILES, LISTS, WIDE>), dim3((unsigned)groups), dim3(256), 0, stream, p, sp);
 }
 
 template <int FMT, int D, bool LISTS>
@@ -1221,9 +1241,9 @@ hipError_t launch_attn_d(const Args<LISTS>& p, void* workspace, hipStream_t stre
   }
   sp.line_groups = (int)groups >> sp.line_shift;
   if (few)
-    launch_few<FMT, D, 1, LISTS>(p, sp, (int)groups, stream);
+    launch_few<FMT, D, 1, LISTS, false>(p, sp, (int)groups, stream);
   else
-    launch_few<FMT, D, kTiles, LISTS>(p, sp, (int)groups, stream);
+    launch_few<FMT, D, kTiles, LISTS, false>(p, sp, (int)groups, stream);
   if (!whole) {
     // 16 slices where a segment has more than 16 parts on average, else 2
     const unsigned rows = (unsigned)(most < seg_rows ? most : seg_rows);
