@@ -502,8 +502,8 @@ struct Pages {
         }
         owner = __builtin_amdgcn_readfirstlane(min(owner, p.owners.R - 1));
       }
-      const int past_own = p.owners.seq_lens[owner] - row_start(p.owners, owner + 1) + r + 1;
-      newest = clamp_pos(past_own, p.cache.max_pages << p.cache.page_shift);
+      const int64_t past_own = (int64_t)p.owners.seq_lens[owner] - row_start(p.owners, owner + 1) + r + 1;
+      newest = (int)min(max(past_own, (int64_t)0), (int64_t)p.cache.max_pages << p.cache.page_shift);
       table = (table_t)(p.cache.table + (int64_t)owner * p.cache.max_pages);
     } else {
       table = (table_t)(p.cache.table + (int64_t)r * p.cache.max_pages);

@@ -17,8 +17,9 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
 
-// Workgroups are numbered in the grid's x dimension, which takes 2^32 work-items.
-constexpr int64_t kMostBlocks = (int64_t)1 << 23;
+// A launch takes fewer than 2^32 work-items in a dimension (more are dropped without an error), of workgroups of up to
+// 1,024: they walk what is left.
+constexpr int64_t kMostBlocks = (int64_t)1 << 21;
 
 typedef uint32_t uint2_t __attribute__((ext_vector_type(2)));
 typedef uint32_t uint4_t __attribute__((ext_vector_type(4)));
@@ -665,7 +666,7 @@ __global__ void __launch_bounds__(kThreads) gdn_select_score_k(SelectArgs p) {
     while (n < past) {
       // the tokens from n on that are of one request: the last of them holds the most entries
       const int r = owner_of(p.rows, n, threadIdx.x & 63);
-      const int count = min(past, row_start(p.rows, r + 1)) - n;
+      const int count = max(min(past, row_start(p.rows, r + 1)) - n, 1);   // on, whatever cu_seqlens holds
       const Token t = token_at(p, r, n + count - 1);
       // the last chunk takes what the host did not know of
       const int i0 = min((int)blockIdx.y * p.chunk, t.held);
@@ -772,7 +773,7 @@ hipError_t launch_select_d(SelectArgs p, hipStream_t stream) {
   p.chunk = (int)(share > 64 ? (share < (1 << 30) ? share : 1 << 30) : 64);
   if (p.chunk < fits) p.chunk = (int)fits;
   const int64_t jobs = ((int64_t)p.rows.N + p.group_tokens - 1) / p.group_tokens * p.cache.Hk;
-  const dim3 grid(blocks_of(jobs), (unsigned)((p.max_held + p.chunk - 1) / p.chunk));
+  const dim3 grid(blocks_of(jobs), (unsigned)(p.max_held > 0 ? (p.max_held + p.chunk - 1) / p.chunk : 1));
   if (p.group_tokens == 1)
     hipLaunchKernelGGL((gdn_select_score_k<IO, D, 1>), grid, dim3(kThreads), 0, stream, p);
   else

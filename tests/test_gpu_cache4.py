@@ -206,6 +206,13 @@ def test_drafts_windows_and_empty_rows(D):
     _check([5000], [3], Hk=2, G=4, D=D, page=64, window=1)
 
 
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("page", [16, 32, 64, 512])
+@pytest.mark.parametrize("window", [7, 33, 100, 1000])
+def test_windows_end_inside_pages_and_tiles(D, page, window):
+    _check([700, 33, 1, 90], [3, 1, 1, 5], Hk=2, G=4, D=D, page=page, window=window, seed=window)
+
+
 @pytest.mark.parametrize("D,Hk,G", [(64, 1, 4), (128, 2, 8), (256, 1, 6)])
 @pytest.mark.parametrize("mirrors", [True, False])
 def test_split_lengths(D, Hk, G, mirrors):
@@ -271,3 +278,25 @@ def test_pages_left_out():
     got = run_attention(c, q, cu, torch, gdn, cache=any_device_cache(c, torch, gdn))
     assert_within(got, want, tol, "missing pages")
     assert not got[2].any()
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_strided_q_and_the_ends_of_int32(D):
+    """q as a slice of a projection's output; lengths at the ends of int32, of which the table holds what it holds."""
+    _case(f"strided q, int32 lengths D={D}")
+    c = make_cache4([64, 64], Hk=2, D=D, page=16, seed=1)
+    c["table"] = c["table"][:, :4]
+    q = queries(2, 8, D, "f16", 2)
+    wide = torch.zeros((2, 8 * D + 64), dtype=torch.float16, device="cuda")
+    wide[:, :8 * D] = dev(q, torch).view(2, -1)
+    cache = any_device_cache(c, torch, gdn)
+    ws = torch.empty(gdn.gdn_attn_workspace_bytes(2, 2, 8, cache), dtype=torch.uint8, device="cuda")
+    out = torch.full((2, 8, D), -7.75, dtype=torch.float16, device="cuda")
+    for lens in ([64, 64], [(1 << 31) - 1, -(1 << 31)]):
+        c["lens"] = np.asarray(lens, np.int32)
+        gdn.gdn_attn_forward(wide[:, :8 * D].view(2, 8, D), cache, dev(c["lens"], torch), None, out, workspace=ws)
+        torch.cuda.synchronize()
+        want, tol = oracle_attention({**c, "lens": np.clip(np.asarray(lens, np.int64), 0, 64)}, q, [0, 1, 2])
+        if lens[1] < 0:
+            want[1], tol[1] = 0, 0
+        assert_within(out.double().cpu().numpy(), want, tol, f"lens {lens}")

@@ -368,3 +368,76 @@ def test_sparse_padded_batch(fmt):
             got = run_sparse(c, q, cu, lists, counts, torch, gdn, mirrors=mirrors)
             assert_within(got[:3], want, tol + half_step(fmt, np.abs(want) + tol), f"padded {lens}")
             assert (got[3:] == -7.75).all()
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("T", [1, 3])
+def test_strided_q(fmt, T):
+    """q as a slice of a projection's output, of the selection and of the attention."""
+    _case(f"strided q {fmt} T={T}")
+    lens, Hk, Hq, D, K = [300, 77], 2, 8, 128, 5
+    c = any_cache(lens, fmt=fmt, Hk=Hk, D=D, page=16, seed=3)
+    b, N = _bounds_of(c, 4, D, Hk), 2 * T
+    cu, q = cu_of([T, T]), queries(N, Hq, D, fmt, 5)
+    wide = torch.full((N, Hq * D + 256), float("nan"), dtype=dev(q, torch).dtype, device="cuda")
+    wide[:, 64:64 + Hq * D] = dev(q, torch).view(N, -1)
+    dq, cache, dlens = wide[:, 64:64 + Hq * D].view(N, Hq, D), any_device_cache(c, torch, gdn), dev(c["lens"], torch)
+    lists, counts = torch.empty((N, Hk, K), dtype=torch.int32, device="cuda"), torch.empty(N, dtype=torch.int32, device="cuda")
+    out = torch.empty((N, Hq, D), dtype=dq.dtype, device="cuda")
+    ws = torch.empty(max(gdn.gdn_attn_select_workspace_bytes(N, 2, Hq, K, cache), gdn.gdn_attn_sparse_workspace_bytes(N, 2, Hq, K, cache)),
+                     dtype=torch.uint8, device="cuda")
+    gdn.gdn_attn_select(dq, dev(b, torch), cache, dlens, None, lists, counts, num_reqs=2, workspace=ws)
+    gdn.gdn_attn_sparse_forward(dq, cache, dlens, None, lists, counts, out, num_reqs=2, workspace=ws)
+    torch.cuda.synchronize()
+    want_l, want_n, gaps = SO.select(q, b, c["table"], 16, cu, lens, K, 1, 1)
+    assert gaps.min() > 1e-12
+    assert np.array_equal(lists.cpu().numpy(), want_l) and np.array_equal(counts.cpu().numpy(), want_n)
+    want, tol = SO.sparse_attention(q, c["k"], c["v"], c["table"], cu, lens, want_l, want_n)
+    assert_within(out.double().cpu().numpy(), want, tol + half_step(fmt, np.abs(want) + tol), "strided q")
+
+
+def test_a_nan_query_selects_the_lowest_entries():
+    _case("NaN q")
+    c = any_cache([700, 700], fmt="f16", Hk=2, D=64, page=16, seed=0)
+    b, q = _bounds_of(c, 1, 64, 2), queries(2, 4, 64, "f16", 2)
+    q[0, 1, 5] = np.nan                                      # of key head 0
+    want, counts, _ = SO.select(q, b, c["table"], 16, [0, 1, 2], c["lens"], 6, 1, 1)
+    got, n = run_select(c, q, b, [0, 1, 2], torch, gdn, K=6)
+    assert np.array_equal(got, want) and np.array_equal(n, counts)
+    assert got[0, 0].tolist() == [0, 1, 2, 3, 4, 43]
+
+
+@pytest.mark.parametrize("fmt", ["f16", "e2m1"])
+def test_lengths_at_the_ends_of_int32(fmt):
+    """The table's positions are all there are, and a negative length has none."""
+    _case(f"int32 lengths {fmt}")
+    c = any_cache([64, 64], fmt=fmt, Hk=1, D=64, page=16, seed=1)
+    c["table"] = c["table"][:, :4]
+    c["lens"] = np.array([(1 << 31) - 1, -(1 << 31)], np.int32)
+    cu, q, b = cu_of([2, 2]), queries(4, 4, 64, fmt, 2), _bounds_of(c, 1, 64, 1)
+    lists, counts = run_select(c, q, b, cu, torch, gdn, K=3, mirrors=False)
+    assert counts.tolist() == [3, 3, 0, 0] and (lists[2:] == -1).all()
+    got = run_sparse(c, q, cu, lists, counts, torch, gdn, mirrors=False)
+    want, tol = SO.sparse_attention(q[:2], c["k"], c["v"], c["table"], [0, 2], [(1 << 31) - 1], lists[:2], counts[:2])
+    assert_within(got[:2], want, tol + half_step(fmt, np.abs(want) + tol), "int32 lengths")
+    assert not got[2:].any()
+    old = np.full((c["P"], 1, 2, 64), 3.0, io_np(fmt))
+    assert np.array_equal(_run_bounds(c, [2, 2], old, mirrors=False), old)    # no new token lies on a page
+
+
+def test_many_lists_whose_lengths_the_host_says_are_none():
+    """A mirror of zeros with the device's lengths: lists in two launches, over what the device says."""
+    _case("mirror of zeros")
+    R = 160
+    c = any_cache([200] * R, fmt="f16", Hk=8, D=64, page=16, seed=0)
+    b, q, cu = _bounds_of(c, 1, 64, 8), queries(R, 8, 64, "f16", 2), np.arange(R + 1, dtype=np.int32)
+    want, counts, gaps = SO.select(q, b, c["table"], 16, cu, c["lens"], 5, 1, 1)
+    assert gaps.min() > 1e-12
+    lists = torch.full((R, 8, 5), -77, dtype=torch.int32, device="cuda")
+    n = torch.full((R,), -77, dtype=torch.int32, device="cuda")
+    cache = any_device_cache(c, torch, gdn)
+    ws = torch.full((gdn.gdn_attn_select_workspace_bytes(R, R, 8, 5, cache),), 0xff, dtype=torch.uint8, device="cuda")
+    gdn.gdn_attn_select(dev(q, torch), dev(b, torch), cache, dev(c["lens"], torch), dev(cu, torch), lists, n,
+                        seq_lens_host=np.zeros(R, np.int32), workspace=ws)
+    torch.cuda.synchronize()
+    assert np.array_equal(lists.cpu().numpy(), want) and np.array_equal(n.cpu().numpy(), counts)
