@@ -38,6 +38,16 @@
 // (6.3 TB/s; counted HBM reads equal the bytes of the attended keys and values); 16 x up
 // to 4 drafts over up to 8,192 positions of 4 x 256 fp16, 279 MB, 60 us; one request of
 // 131,072 positions in 8 bits, 270 MB, 51 us; one of 333 positions 8 us.
+//
+// 4-bit pages (GDN_CACHE_E2M1) have a scale per 32 elements, applied by the conversion to FP16, exactly. Their tiles are
+// bound by instruction issue, not by bytes: 219 vector instructions for 32 positions of 128 columns, 64 of them
+// conversions. More waves a SIMD hide more than more tiles in flight a wave do: 16 x up to 4 drafts over up to 8,191
+// positions, D = 256, 75 MB, four tiles 103, one 35 us; 64 requests of up to 16,384, D = 128, 491 MB, 113 and 95 to 106 us
+// (4.7 to 5.2 TB/s, by where the pages lie).
+//
+// LISTS: the positions of a token and key head are those of its listed pages, each list a segment of its own: 64 requests
+// x 8 key heads x 32 pages of 64, D = 128 fp16, 530 MB, 86 to 90 us (5.9 to 6.2 TB/s, HBM); 2 drafts x 65 pages, D = 256
+// in 4 bits, 13.7 us (latency, the join's 4 us among it).
 #pragma once
 
 #include <type_traits>

@@ -5,6 +5,11 @@
 // w- . low with w+ (w-) the group's sum of the positive (negative) parts of q. That is two
 // rows of D elements a page and head instead of page_size rows: the pages of the highest
 // bounds are selected.
+//
+// Both are bound by the latency of lengths -> table -> keys or bounds, and the selection by its 64-bit sums too.
+// Measured: bounds of 64 new tokens, 8 key heads of 128 fp16, pages of 64, 3.7 us (a launch); of prompts of 28,746 tokens,
+// 4 of 256 in 8 bits, 31 MB, 10.5 us. Selection for 64 requests x 8 key heads, 32 of up to 256 pages, 30 MB, 13.7 us
+// (about 11 the scores, 3 the list); 3 drafts x 4 key heads of 256 fp32, 128 of 4,097 pages, 34 MB, 26 us.
 #include <type_traits>
 
 #include "gdn_attn_kernels.h"
