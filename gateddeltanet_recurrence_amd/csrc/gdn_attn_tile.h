@@ -92,8 +92,8 @@ struct SplitArgs {
   int32_t seg_shift;                      // log2 of a segment's rows: 4 or 5
   int32_t line_shift, line_groups;        // log2 of the lines, workgroups of a line (see block_of)
   int32_t chunk_shift;                    // log2 of a unit's positions
-  int32_t whole;                          // > 0: a share is the segments that begin in it, each as long as this many
-                                          // units more
+  int32_t whole;                          // > 0: a share is the segments that begin in it
+  int32_t more;                           // units that a segment's fixed part counts as: before its own where it is split
   int32_t max_segs;                       // > 0: notes by segment, this many of a request and key head; 0: by workgroup
 };
 
@@ -151,7 +151,7 @@ __device__ __forceinline__ Plan plan_of(const Args<LISTS>& p, const SplitArgs& s
   s.base = p.window > 0 ? window_start(p, s.len - s.T + 1, s.hi) & ~31 : 0;
   s.segs = (s.T * p.group + (1 << sp.seg_shift) - 1) >> sp.seg_shift;
   if (sp.max_segs > 0) s.segs = min(s.segs, sp.max_segs);  // no note past the request's, whatever cu_seqlens holds
-  s.chunks = s.T > 0 ? max((int)(((unsigned)(s.hi - s.base) + (1u << sp.chunk_shift) - 1) >> sp.chunk_shift) + sp.whole, 1) : 0;
+  s.chunks = s.T > 0 ? max((int)(((unsigned)(s.hi - s.base) + (1u << sp.chunk_shift) - 1) >> sp.chunk_shift) + sp.more, 1) : 0;
   return s;
 }
 
@@ -298,8 +298,9 @@ __device__ __forceinline__ Segment next_segment(const Args<LISTS>& p, const Spli
   x.rows = line < x.s.segs ? min(1 << sp.seg_shift, x.s.T * p.group - x.seg_row) : 0;   // 0: fewer segments than lines
   const int cap = capacity_of<LISTS>(p);
   const int past_last = x.rows == 0 ? 0 : x.s.len - x.s.T + token_of(p, x.s, x.seg_row + x.rows - 1) + 1;
-  x.t0 = x.s.base + (x.c0 << sp.chunk_shift);
-  x.end = (int)min((unsigned)x.s.base + ((unsigned)x.c1 << sp.chunk_shift), (unsigned)clamp_pos(past_last, cap));
+  x.t0 = x.s.base + (max(x.c0 - sp.more, 0) << sp.chunk_shift);
+  x.end = (int)min((unsigned)x.s.base + ((unsigned)(sp.whole > 0 ? x.c1 : max(x.c1 - sp.more, 0)) << sp.chunk_shift),
+                   (unsigned)clamp_pos(past_last, cap));
   return x;
 }
 
@@ -345,6 +346,12 @@ __device__ __forceinline__ float row_max(float x) {
   x = fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
   auto b = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
   return fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
+}
+__device__ __forceinline__ float row_maximum(float x) {     // NaN where one is
+  auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  x = __builtin_elementwise_maximum(__uint_as_float(a[0]), __uint_as_float(a[1]));
+  auto b = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return __builtin_elementwise_maximum(__uint_as_float(b[0]), __uint_as_float(b[1]));
 }
 __device__ __forceinline__ float row_sum(float x) {
   auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
@@ -547,6 +554,18 @@ struct Pages {
   }
 };
 
+// Byte I of w at a float's exponent, in one instruction (the compiler takes a shift and a mask).
+template <int I>
+__device__ __forceinline__ uint32_t exponent_of(uint32_t w) {
+  uint32_t x;
+  const uint32_t by = 23;
+  if constexpr (I == 0) asm("v_lshlrev_b32_sdwa %0, %1, %2 dst_sel:DWORD dst_unused:UNUSED_PAD src0_sel:DWORD src1_sel:BYTE_0" : "=v"(x) : "v"(by), "v"(w));
+  if constexpr (I == 1) asm("v_lshlrev_b32_sdwa %0, %1, %2 dst_sel:DWORD dst_unused:UNUSED_PAD src0_sel:DWORD src1_sel:BYTE_1" : "=v"(x) : "v"(by), "v"(w));
+  if constexpr (I == 2) asm("v_lshlrev_b32_sdwa %0, %1, %2 dst_sel:DWORD dst_unused:UNUSED_PAD src0_sel:DWORD src1_sel:BYTE_2" : "=v"(x) : "v"(by), "v"(w));
+  if constexpr (I == 3) asm("v_lshlrev_b32_sdwa %0, %1, %2 dst_sel:DWORD dst_unused:UNUSED_PAD src0_sel:DWORD src1_sel:BYTE_3" : "=v"(x) : "v"(by), "v"(w));
+  return x;
+}
+
 // WIDE: pages hold a whole tile (its two blocks share one look-up and one set of resources: with 4 bits, where the
 // scalar unit's share of the time shows, and pages of 32 or more).
 template <int FMT, int D, int WAVES, int TILES, bool LISTS, bool WIDE>
@@ -563,7 +582,9 @@ __global__ void __launch_bounds__(64 * WAVES, 1) gdn_attn_k(Args<LISTS> p, Split
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int n = lane & 15, g = lane >> 4;
   Share sh = find_share<LISTS>(p, sp, lane);
-  const float to_log2 = p.scale * 1.4426950408889634f;
+  // (with 4 bits it multiplies -inf, too, and must not be 0 there)
+  float to_log2 = p.scale * 1.4426950408889634f;
+  if (FMT == kE2M1 && to_log2 < 0x1p-126f) to_log2 = 0x1p-126f;
   const IO* __restrict__ qs = static_cast<const IO*>(p.q);
   if (tid == 0 && sp.notes != nullptr && sp.max_segs == 0) sp.notes[2 * sh.id] = int4{0, 0, 0, 0};
   bool again = false;
@@ -571,6 +592,7 @@ __global__ void __launch_bounds__(64 * WAVES, 1) gdn_attn_k(Args<LISTS> p, Split
   const int k_at = n * S::kRow + 4 * S::kKWords * g, v_at = 4 * g * S::kRow + S::kSetBytes * n;
 
   if (sh.u >= sh.u_end) return;
+  int turn = blockIdx.x / kGroups;                         // see below
   Segment sg;
   Rows rw[TILES];                                          // of row 16 i + n
   Pages<LISTS> pages(p);
@@ -728,6 +750,17 @@ __global__ void __launch_bounds__(64 * WAVES, 1) gdn_attn_k(Args<LISTS> p, Split
     while (some) {
 #pragma unroll
       for (int u = 0; u < U; ++u) {
+        // Of the workgroups that share a CU, the oldest wave's instructions go first: their equal shares were done after
+        // 66, 73 and 81 us (64 requests of up to 16,384 positions, D = 128; D = 64 33 to 50 us). Priorities that go
+        // round, a tile each, make it 75 to 78 (40 to 48), the call 2 % shorter.
+        if constexpr (FMT == kE2M1 && TILES == 1) {
+          if (turn & 2) {
+            if (turn & 1) __builtin_amdgcn_s_setprio(3); else __builtin_amdgcn_s_setprio(2);
+          } else {
+            if (turn & 1) __builtin_amdgcn_s_setprio(1); else __builtin_amdgcn_s_setprio(0);
+          }
+          ++turn;
+        }
         // ---- scores: block a of lane group g holds positions t + 16 a + 4 g + (0 .. 3)
         float4_t x[TILES][S::kBlocks];
 #pragma unroll
@@ -802,8 +835,9 @@ __global__ void __launch_bounds__(64 * WAVES, 1) gdn_attn_k(Args<LISTS> p, Split
               xs[r][i] = fmaf(x[r][i >> 2][i & 3], to_log2 * __uint_as_float(kb << 23), (float)((int)vb - 127));
             inv[i] = __uint_as_float((254u - min(vb, 253u)) << 23);
           } else {
+            // with 4 bits the factor is left to the exponent's multiply-add, one instruction less
 #pragma unroll
-            for (int r = 0; r < TILES; ++r) xs[r][i] = x[r][i >> 2][i & 3] * to_log2;
+            for (int r = 0; r < TILES; ++r) xs[r][i] = FMT == kE2M1 ? x[r][i >> 2][i & 3] : x[r][i >> 2][i & 3] * to_log2;
           }
         }
 
@@ -855,9 +889,16 @@ __global__ void __launch_bounds__(64 * WAVES, 1) gdn_attn_k(Args<LISTS> p, Split
 #pragma unroll
         for (int r = 0; r < TILES; ++r) {
           float m = xs[r][0];
+          if constexpr (FMT == kE2M1) {
+            // NaN where one is, which takes fewer instructions; M stays then, and l shows the NaN
 #pragma unroll
-          for (int i = 1; i < S::kPos; ++i) m = fmaxf(m, xs[r][i]);
-          m = fmaxf(row_max(m) - kLift<FMT>, M[r]);
+            for (int i = 1; i < S::kPos; ++i) m = __builtin_elementwise_maximum(m, xs[r][i]);
+            m = __builtin_elementwise_maximum(fmaf(row_maximum(m), to_log2, -kLift<FMT>), M[r]);
+          } else {
+#pragma unroll
+            for (int i = 1; i < S::kPos; ++i) m = fmaxf(m, xs[r][i]);
+            m = fmaxf(row_max(m) - kLift<FMT>, M[r]);
+          }
           if (__any(m > M[r])) {
             const float f = M[r] == m ? 1.f : exp2_fast(M[r] - m);   // -inf - -inf is not asked for
             l[r] *= f;
@@ -868,7 +909,7 @@ __global__ void __launch_bounds__(64 * WAVES, 1) gdn_attn_k(Args<LISTS> p, Split
           const float ref = M[r] == -INFINITY ? 0.f : M[r];
 #pragma unroll
           for (int i = 0; i < S::kPos; ++i) {
-            wgt[r][i] = exp2_fast(xs[r][i] - ref);
+            wgt[r][i] = exp2_fast(FMT == kE2M1 ? fmaf(xs[r][i], to_log2, -ref) : xs[r][i] - ref);
             if constexpr (FMT == kE4M3)
               l[r] = fmaf(wgt[r][i], inv[i], l[r]);
             else
@@ -896,7 +937,13 @@ __global__ void __launch_bounds__(64 * WAVES, 1) gdn_attn_k(Args<LISTS> p, Split
             float vs[8];                                   // e2m1: scales of this lane's columns
             if constexpr (FMT == kE2M1) {
 #pragma unroll
-              for (int i = 0; i < 8; ++i) vs[i] = __uint_as_float(((vscale[u][(b + i) >> 2] >> (8 * (i & 3))) & 255u) << 23);
+              for (int a = 0; a < 2; ++a) {
+                const uint32_t s = vscale[u][(b >> 2) + a];
+                vs[4 * a] = __uint_as_float(exponent_of<0>(s));
+                vs[4 * a + 1] = __uint_as_float(exponent_of<1>(s));
+                vs[4 * a + 2] = __uint_as_float(exponent_of<2>(s));
+                vs[4 * a + 3] = __uint_as_float(exponent_of<3>(s));
+              }
             }
             uint4_t pw[TILES], pl[TILES];
 #pragma unroll
@@ -1199,6 +1246,17 @@ bool one_group_each(int64_t longest, int64_t sum, int heads, int64_t position_by
   return alone <= together / 2 + 5.0;
 }
 
+// Units of kChunkShift positions that a segment's beginning and joining count as where 4-bit lengths are split, so that
+// workgroups with two segments are not the last: one, or with two row tiles two. Not where few workgroups hold two
+// or shares are one or two units, which a unit more rounds up for all. Without and with, D = 128 (256): 64 requests of up to
+// 16,384 positions, 8 (4) key heads, 104 and 91 us (100 and 90), of up to 2,000 22.6 and 20.9 (22.7 and 22.7); 16 of up to 2,000
+// 13.0 and 12.7 (12.9 and 13.5); 16 x up to 4 drafts of 6 heads over up to 8,191, D = 256, 34.0 and 31.4, 64 x 4 over 8,192 81
+// and 78, 1 x 4 over 8,191 15.9 and 17.3. Three and four units are no better than two.
+inline int fixed_part(int tiles, int64_t segments, int64_t positions, int64_t rows, int64_t groups) {
+  const int64_t units = positions * ((rows + tiles * kRows - 1) / (tiles * kRows)) >> kChunkShift;
+  return segments * 8 >= groups && units >= 2 * groups ? tiles : 0;
+}
+
 template <int FMT, int D, int TILES, bool LISTS, bool WIDE>
 void launch_few(const Args<LISTS>& p, const SplitArgs& sp, int groups, hipStream_t stream) {
   if constexpr (FMT == kE2M1 && !WIDE) {
@@ -1231,8 +1289,9 @@ hipError_t launch_attn_d(const Args<LISTS>& p, void* workspace, hipStream_t stre
   } else if (whole) {
     groups = 2 * kGroups;
     sp.chunk_shift = 5;
-    sp.whole = (FMT == kE2M1 ? kSegmentBytes4 : kSegmentBytes) / (32 * 2 * Shape<FMT, D, 4>::kRow);
-    while (segments * ((cap >> sp.chunk_shift) + 1 + sp.whole) > ((int64_t)1 << 30)) ++sp.chunk_shift;
+    sp.whole = 1;
+    sp.more = (FMT == kE2M1 ? kSegmentBytes4 : kSegmentBytes) / (32 * 2 * Shape<FMT, D, 4>::kRow);
+    while (segments * ((cap >> sp.chunk_shift) + 1 + sp.more) > ((int64_t)1 << 30)) ++sp.chunk_shift;
   } else {
     static_assert(FMT == kE2M1 || split_groups<FMT, D, 1>() == (D == 64 ? split_groups<FMT, 64, 1>() : kGroups),
                   "see attn_workspace_bytes");
@@ -1241,7 +1300,8 @@ hipError_t launch_attn_d(const Args<LISTS>& p, void* workspace, hipStream_t stre
     sp.parts = reinterpret_cast<float*>(static_cast<char*>(workspace) + (FMT == kE2M1 ? kNoteBytes4 : kNoteBytes));
     sp.part_rows = few ? kRows : part_rows(p.rows.N, p.group);
     sp.chunk_shift = kChunkShift;
-    while (segments * ((cap >> sp.chunk_shift) + 1) > ((int64_t)1 << 30)) ++sp.chunk_shift;
+    if constexpr (FMT == kE2M1) sp.more = fixed_part(few ? 1 : kTiles, segments, p.sum_len * p.cache.Hk, most, groups);
+    while (segments * ((cap >> sp.chunk_shift) + 1 + sp.more) > ((int64_t)1 << 30)) ++sp.chunk_shift;
     // notes by segment where there are fewer segments than workgroups
     const int64_t segs = (most + seg_rows - 1) / seg_rows;
     notes = segs * p.rows.R * p.cache.Hk;

@@ -221,6 +221,22 @@ def test_split_lengths(D, Hk, G, mirrors):
     _check([6000, 2050], [5, 2], Hk=Hk, G=G, D=D, page=128, mirrors=mirrors)
 
 
+@pytest.mark.parametrize("D,Hk", [(64, 16), (128, 12), (256, 8)])
+@pytest.mark.parametrize("page", [16, 64])
+def test_split_of_many_segments(D, Hk, page):
+    """As many units as make a segment's fixed part count in the split: a share may begin, or lie, within one."""
+    lens = [6000, 4000, 2500, 2000, 1, 129, 0, 1500, 1300]
+    _check(lens, [1, 1, 1, 1, 1, 1, 0, 1, 1], Hk=Hk, G=2, D=D, page=page)
+    _check(lens[::-1], [1, 1, 0, 1, 1, 1, 1, 1, 1], Hk=Hk, G=2, D=D, page=page, window=5500, seed=1)
+
+
+@pytest.mark.parametrize("D,Hk", [(64, 8), (128, 8), (256, 4)])
+def test_split_of_many_segments_of_drafts(D, Hk):
+    lens = [6000, 4000, 2500, 2000, 1, 129, 0, 1500, 1300]
+    _check(lens, [4, 3, 1, 4, 1, 4, 0, 2, 4], Hk=Hk, G=6, D=D, page=64)
+    _check(lens, [9, 3, 1, 4, 1, 4, 0, 2, 8], Hk=Hk, G=6, D=D, page=32, seed=1)     # two segments of 32 rows
+
+
 @pytest.mark.parametrize("D", [64, 128, 256])
 def test_many_short_requests_share_workgroups(D):
     rng = np.random.default_rng(D)

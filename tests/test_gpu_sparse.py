@@ -292,6 +292,11 @@ def test_sparse_split(fmt, D, mirrors):
     _check([20000, 9000], [1, 3], Hk=2, G=6, D=D, fmt=fmt, page=64, K=100, mirrors=mirrors)
 
 
+def test_sparse_split_of_many_lists():
+    """As many lists as make a list's fixed part count in the split."""
+    _check([2100], [16], Hk=8, G=2, D=64, fmt="e2m1", page=64, K=32)
+
+
 @pytest.mark.parametrize("fmt", FORMATS)
 def test_sparse_many(fmt):
     """More segments than get a workgroup each, of a prompt and of a batch."""
