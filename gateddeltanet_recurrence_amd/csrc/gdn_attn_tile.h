@@ -39,11 +39,10 @@
 // to 4 drafts over up to 8,192 positions of 4 x 256 fp16, 279 MB, 60 us; one request of
 // 131,072 positions in 8 bits, 270 MB, 51 us; one of 333 positions 8 us.
 //
-// 4-bit pages (GDN_CACHE_E2M1) have a scale per 32 elements, applied by the conversion to FP16, exactly. Their tiles are
-// bound by instruction issue, not by bytes: 219 vector instructions for 32 positions of 128 columns, 64 of them
-// conversions. More waves a SIMD hide more than more tiles in flight a wave do: 16 x up to 4 drafts over up to 8,191
-// positions, D = 256, 75 MB, four tiles 103, one 35 us; 64 requests of up to 16,384, D = 128, 491 MB, 113 and 95 to 106 us
-// (4.7 to 5.2 TB/s, by where the pages lie).
+// 4-bit pages (GDN_CACHE_E2M1) have a scale per 32 elements, applied by the conversion to FP16, exactly: about 200 vector
+// instructions for 32 positions of 128 columns, 64 of them conversions. More waves a SIMD hide more than more tiles in
+// flight a wave do (see kMostAhead). 64 requests of up to 16,384, D = 128, 491 MB, 90 to 93 us (5.3 to 5.4 TB/s; its loop
+// alone 6.4); 16 x up to 4 drafts over up to 8,191 positions, D = 256, 75 MB, 31.5 us, of which about 20 are the loop.
 //
 // LISTS: the positions of a token and key head are those of its listed pages, each list a segment of its own: 64 requests
 // x 8 key heads x 32 pages of 64, D = 128 fp16, 530 MB, 86 to 90 us (5.9 to 6.2 TB/s, HBM); 2 drafts x 65 pages, D = 256
@@ -752,8 +751,8 @@ __global__ void __launch_bounds__(64 * WAVES, 1) gdn_attn_k(Args<LISTS> p, Split
       for (int u = 0; u < U; ++u) {
         // Of the workgroups that share a CU, the oldest wave's instructions go first: their equal shares were done after
         // 66, 73 and 81 us (64 requests of up to 16,384 positions, D = 128; D = 64 33 to 50 us). Priorities that go
-        // round, a tile each, make it 75 to 78 (40 to 48), the call 2 % shorter.
-        if constexpr (FMT == kE2M1 && TILES == 1) {
+        // round, a tile each, make it 75 to 78 (40 to 48), the call 93.3 -> 90.4 us (66.3 -> 64.2).
+        if (FMT == kE2M1 && TILES == 1 && sp.line_groups > kGroups) {
           if (turn & 2) {
             if (turn & 1) __builtin_amdgcn_s_setprio(3); else __builtin_amdgcn_s_setprio(2);
           } else {
@@ -1248,10 +1247,10 @@ bool one_group_each(int64_t longest, int64_t sum, int heads, int64_t position_by
 
 // Units of kChunkShift positions that a segment's beginning and joining count as where 4-bit lengths are split, so that
 // workgroups with two segments are not the last: one, or with two row tiles two. Not where few workgroups hold two
-// or shares are one or two units, which a unit more rounds up for all. Without and with, D = 128 (256): 64 requests of up to
-// 16,384 positions, 8 (4) key heads, 104 and 91 us (100 and 90), of up to 2,000 22.6 and 20.9 (22.7 and 22.7); 16 of up to 2,000
-// 13.0 and 12.7 (12.9 and 13.5); 16 x up to 4 drafts of 6 heads over up to 8,191, D = 256, 34.0 and 31.4, 64 x 4 over 8,192 81
-// and 78, 1 x 4 over 8,191 15.9 and 17.3. Three and four units are no better than two.
+// or shares are one or two units, which a unit more rounds up for all. Without and with, on the same buffers: 16 x up to 4
+// drafts of 6 heads over up to 8,191 positions, D = 256, 34.1 and 31.5 us, 64 x 4 over 8,192 81.3 and 78.3; 64 requests of
+// up to 2,000, 8 heads of 128, 22.8 and 21.1 (4 of 256 22.2 and 22.6), of up to 16,384 94.0 and 93.3. Where the rule leaves
+// it out, 1 x 4 over 8,191, it was 15.9 and 17.3.
 inline int fixed_part(int tiles, int64_t segments, int64_t positions, int64_t rows, int64_t groups) {
   const int64_t units = positions * ((rows + tiles * kRows - 1) / (tiles * kRows)) >> kChunkShift;
   return segments * 8 >= groups && units >= 2 * groups ? tiles : 0;
