@@ -14,6 +14,7 @@
 
 #include "gdn_attn_kernels.h"
 #include "gdn_common.h"
+#include "gdn_pick.h"
 
 namespace gdn {
 
@@ -234,15 +235,6 @@ __global__ void __launch_bounds__(kThreads) gdn_kv_bounds_k(BoundsArgs p) {
 
 // ------------------------------------------------------------------------- selection
 
-// Scores are kept as 64-bit keys that order as they do: 0 for an entry that may not be
-// selected, one below the highest for a NaN, the highest for an entry that is always in.
-constexpr uint64_t kAlways = ~(uint64_t)0;
-__device__ __forceinline__ uint64_t key_of(double x) {
-  if (x != x) return kAlways - 1;
-  const uint64_t b = (uint64_t)__double_as_longlong(x);
-  return (b >> 63) != 0 ? ~b : b | ((uint64_t)1 << 63);
-}
-
 template <int CTRL>
 __device__ __forceinline__ double dpp64(double x) {
   const uint64_t b = (uint64_t)__double_as_longlong(x);
@@ -439,39 +431,11 @@ struct PickShared {
 // The K entries of the highest keys among `held`, equal ones from the lowest entry on, in ascending order. A
 // threshold is found by cutting the keys' range into WAYS parts until K keys lie from it on, or none but equal ones are
 // left between its ends: as often as it takes to tell the K-th key from the next, 12 to 15 halvings among some
-// thousand scores, 64 at most.
+// thousand scores, 64 at most. Nothing is written outside the list's K places, whatever the keys.
 //
 // SHARED: the keys are split over the workgroup's waves, up to COLUMNS columns of 64 neighbours each (COLUMNS 0: any
 // number, read again each time), which add their counts behind a barrier; else WAVES is 1.
 constexpr int kColumns = 8, kFew = 64 * kColumns;          // keys that a wave holds in registers
-struct Three {
-  int a, b, c;
-};
-
-// Narrows [lo, hi], with `count` keys from lo on, K or more, and fewer than K above hi, until count is K or lo is hi;
-// counts(x, y, z) says how many keys there are from each of the cuts x >= y >= z on (two ways: from y).
-template <int WAYS, typename T, typename Counts>
-__device__ __forceinline__ void cut_range(int K, int& count, T& lo, T& hi, Counts counts) {
-  while (count != K && lo < hi) {
-    const T range = hi - lo, part = range >> 2;            // lo < z <= y <= x <= hi
-    const T y = hi - (range >> 1), x = WAYS == 2 || range < 4 ? y : hi - part, z = WAYS == 2 || range < 4 ? y : y - part;
-    const Three n = counts(x, y, z);
-    if (WAYS == 4 && n.a >= K) {
-      lo = x;
-      count = n.a;
-    } else if (n.b >= K) {
-      lo = y;
-      count = n.b;
-      if (WAYS == 4) hi = x - 1;
-    } else if (WAYS == 4 && n.c >= K) {
-      lo = z;
-      count = n.c;
-      hi = y - 1;
-    } else {
-      hi = z - 1;
-    }
-  }
-}
 template <int WAVES, int COLUMNS, bool SHARED, typename Keys>
 __device__ __forceinline__ void pick(const SelectArgs& p, const Keys& keys, int held, int32_t* list, int32_t* count_out,
                                      PickShared& s) {
@@ -537,37 +501,29 @@ __device__ __forceinline__ void pick(const SelectArgs& p, const Keys& keys, int 
       lo = ~wave_max(lane < WAVES ? ~s.low[lane] : 0);
       hi = wave_max(lane < WAVES ? s.high[lane] : 0);
     }
-    lo = uniform(lo);
-    hi = uniform(hi);
-    // From lo on there are K or more keys, above hi fewer. First by the 32 highest bits of the range, where a
-    // comparison takes a quarter of the time, then, where these do not tell the K-th from the next, by all.
-    const uint64_t range = hi - lo;
-    const int shift = max(32 - (range == 0 ? 32 : __builtin_clzll(range)), 0);
-    int count = there;
-    if (range > 0) {
-      uint32_t lo32 = 0, hi32 = (uint32_t)(range >> shift), short_keys[COLUMNS > 0 ? COLUMNS : 1];
-      // what is always in is above every cut, what is none below
-      const auto short_of = [&](uint64_t key) { return key == kAlways ? ~0u : key < lo ? 0 : (uint32_t)((key - lo) >> shift); };
+    uint32_t short_keys[COLUMNS > 0 ? COLUMNS : 1];
+    ShortKeys shorts{0, 0};
+    const auto prepare = [&](ShortKeys x) {
+      shorts = x;
       if constexpr (COLUMNS > 0) {
 #pragma unroll
-        for (int c = 0; c < COLUMNS; ++c) short_keys[c] = c < columns ? short_of(mine[c]) : 0;
+        for (int c = 0; c < COLUMNS; ++c) short_keys[c] = c < columns ? shorts.of(mine[c]) : 0;
       }
-      cut_range<WAYS>(p.K, count, lo32, hi32, [&](uint32_t x, uint32_t y, uint32_t z) {
-        int nx = 0, ny = 0, nz = 0;
-        each([&](uint64_t key, int c) {
-          const uint32_t k = COLUMNS > 0 ? short_keys[COLUMNS > 0 ? c : 0] : short_of(key);
-          ny += count_lanes(k >= y);
-          if constexpr (WAYS == 4) {
-            nx += count_lanes(k >= x);
-            nz += count_lanes(k >= z);
-          }
-        });
-        return total(nx, ny, nz);
+    };
+    const auto short_counts = [&](uint32_t x, uint32_t y, uint32_t z) {
+      int nx = 0, ny = 0, nz = 0;
+      each([&](uint64_t key, int c) {
+        const uint32_t k = COLUMNS > 0 ? short_keys[COLUMNS > 0 ? c : 0] : shorts.of(key);
+        ny += count_lanes(k >= y);
+        if constexpr (WAYS == 4) {
+          nx += count_lanes(k >= x);
+          nz += count_lanes(k >= z);
+        }
       });
-      hi = min(hi, lo + ((uint64_t)hi32 << shift) + (((uint64_t)1 << shift) - 1));
-      lo += (uint64_t)lo32 << shift;
-    }
-    cut_range<WAYS>(p.K, count, lo, hi, [&](uint64_t x, uint64_t y, uint64_t z) {
+      return total(nx, ny, nz);
+    };
+    const Cut cut = find_cut<WAYS>(p.K, there, uniform(lo), uniform(hi), prepare, short_counts,
+                                   [&](uint64_t x, uint64_t y, uint64_t z) {
       int nx = 0, ny = 0, nz = 0;
       each([&](uint64_t key, int) {
         ny += count_lanes(key >= y);
@@ -578,8 +534,8 @@ __device__ __forceinline__ void pick(const SelectArgs& p, const Keys& keys, int 
       });
       return total(nx, ny, nz);
     });
-    least = lo;
-    surplus = count - p.K;
+    least = cut.least;
+    surplus = cut.surplus;
   }
   // before this wave's: what is taken, and how many of the keys equal to `least`
   int before = 0, kept = 0;
@@ -606,8 +562,7 @@ __device__ __forceinline__ void pick(const SelectArgs& p, const Keys& keys, int 
     each([&](uint64_t key, int) { kept += count_lanes(key == least); });
     kept -= surplus;
   }
-  int32_t* to = list + before;
-  int at = 0;
+  int at = before;
   each([&](uint64_t key, int c) {
     const uint64_t below = ((uint64_t)1 << lane) - 1;
     uint64_t in = __ballot(key >= least);
@@ -616,7 +571,8 @@ __device__ __forceinline__ void pick(const SelectArgs& p, const Keys& keys, int 
       in &= ~ties | __ballot(__builtin_popcountll(ties & below) < kept);
       kept -= __builtin_popcountll(ties);
     }
-    if ((in >> lane & 1) != 0) to[at + __builtin_popcountll(in & below)] = 64 * (first + c) + lane;
+    const int place = at + __builtin_popcountll(in & below);
+    if ((in >> lane & 1) != 0 && (unsigned)place < (unsigned)p.K) list[place] = 64 * (first + c) + lane;
     at += __builtin_popcountll(in);
   });
   end_list<WAVES>(p, min(there, p.K), list, count_out);
