@@ -507,7 +507,10 @@ __device__ __forceinline__ void pick(const SelectArgs& p, const Keys& keys, int 
       shorts = x;
       if constexpr (COLUMNS > 0) {
 #pragma unroll
-        for (int c = 0; c < COLUMNS; ++c) short_keys[c] = c < columns ? shorts.of(mine[c]) : 0;
+        for (int c = 0; c < COLUMNS; ++c) {
+          short_keys[c] = c < columns ? shorts.of(mine[c]) : 0;
+          asm("" : "+v"(short_keys[c]));                   // a number from here on: else each cut asks again what is always in
+        }
       }
     };
     const auto short_counts = [&](uint32_t x, uint32_t y, uint32_t z) {
@@ -562,6 +565,7 @@ __device__ __forceinline__ void pick(const SelectArgs& p, const Keys& keys, int 
     each([&](uint64_t key, int) { kept += count_lanes(key == least); });
     kept -= surplus;
   }
+  const rsrc_t places = make_rsrc(list, 4 * p.K);          // whose bounds drop what lies outside
   int at = before;
   each([&](uint64_t key, int c) {
     const uint64_t below = ((uint64_t)1 << lane) - 1;
@@ -571,8 +575,8 @@ __device__ __forceinline__ void pick(const SelectArgs& p, const Keys& keys, int 
       in &= ~ties | __ballot(__builtin_popcountll(ties & below) < kept);
       kept -= __builtin_popcountll(ties);
     }
-    const int place = at + __builtin_popcountll(in & below);
-    if ((in >> lane & 1) != 0 && (unsigned)place < (unsigned)p.K) list[place] = 64 * (first + c) + lane;
+    if ((in >> lane & 1) != 0)
+      __builtin_amdgcn_raw_buffer_store_b32((uint32_t)(64 * (first + c) + lane), places, 4 * (at + __builtin_popcountll(in & below)), 0, 0);
     at += __builtin_popcountll(in);
   });
   end_list<WAVES>(p, min(there, p.K), list, count_out);
