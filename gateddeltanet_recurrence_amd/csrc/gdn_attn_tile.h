@@ -834,7 +834,7 @@ __global__ void __launch_bounds__(64 * WAVES, 1) gdn_attn_k(Args<LISTS> p, Split
               xs[r][i] = fmaf(x[r][i >> 2][i & 3], to_log2 * __uint_as_float(kb << 23), (float)((int)vb - 127));
             inv[i] = __uint_as_float((254u - min(vb, 253u)) << 23);
           } else {
-            // with 4 bits the factor is left to the exponent's multiply-add, one instruction less
+            // with 4 bits a score's distance from M takes the factor, below
 #pragma unroll
             for (int r = 0; r < TILES; ++r) xs[r][i] = FMT == kE2M1 ? x[r][i >> 2][i & 3] : x[r][i >> 2][i & 3] * to_log2;
           }
@@ -889,17 +889,18 @@ __global__ void __launch_bounds__(64 * WAVES, 1) gdn_attn_k(Args<LISTS> p, Split
         for (int r = 0; r < TILES; ++r) {
           float m = xs[r][0];
           if constexpr (FMT == kE2M1) {
-            // NaN where one is, which takes fewer instructions; M stays then, and l shows the NaN
+            // NaN where one is, which takes fewer instructions; M stays then, and l shows the NaN. M is a score as it is
+            // here: its distance to another is exact where they are near, however large they are.
 #pragma unroll
             for (int i = 1; i < S::kPos; ++i) m = __builtin_elementwise_maximum(m, xs[r][i]);
-            m = __builtin_elementwise_maximum(fmaf(row_maximum(m), to_log2, -kLift<FMT>), M[r]);
+            m = __builtin_elementwise_maximum(row_maximum(m), M[r]);
           } else {
 #pragma unroll
             for (int i = 1; i < S::kPos; ++i) m = fmaxf(m, xs[r][i]);
             m = fmaxf(row_max(m) - kLift<FMT>, M[r]);
           }
           if (__any(m > M[r])) {
-            const float f = M[r] == m ? 1.f : exp2_fast(M[r] - m);   // -inf - -inf is not asked for
+            const float f = M[r] == m ? 1.f : exp2_fast(FMT == kE2M1 ? (M[r] - m) * to_log2 : M[r] - m);   // -inf - -inf is not asked for
             l[r] *= f;
 #pragma unroll
             for (int i = 0; i < kAcc; ++i) acc[r][i] *= f;
@@ -908,7 +909,7 @@ __global__ void __launch_bounds__(64 * WAVES, 1) gdn_attn_k(Args<LISTS> p, Split
           const float ref = M[r] == -INFINITY ? 0.f : M[r];
 #pragma unroll
           for (int i = 0; i < S::kPos; ++i) {
-            wgt[r][i] = exp2_fast(FMT == kE2M1 ? fmaf(xs[r][i], to_log2, -ref) : xs[r][i] - ref);
+            wgt[r][i] = exp2_fast(FMT == kE2M1 ? fmaf(xs[r][i] - ref, to_log2, kLift<FMT>) : xs[r][i] - ref);
             if constexpr (FMT == kE4M3)
               l[r] = fmaf(wgt[r][i], inv[i], l[r]);
             else
@@ -1061,6 +1062,7 @@ __global__ void __launch_bounds__(64 * WAVES, 1) gdn_attn_k(Args<LISTS> p, Split
     again = true;
 #pragma unroll
     for (int r = 0; r < TILES; ++r) {
+      if (FMT == kE2M1) M[r] *= to_log2;                   // from here on as the other formats', but for the lift
       l[r] = row_sum(l[r]) * kFactor<FMT>;
       if (l[r] != l[r]) M[r] = INFINITY;                   // a NaN score is no maximum, but has to show
       if (g == 0) {
