@@ -73,6 +73,7 @@ constexpr int kOneEach = 1024;
 constexpr int kSegmentBytes = 200000;
 constexpr int kSegmentBytes4 = 30000;     // of 4-bit pages: 256 of 90 .. 700, D = 128, 39.8 us, with 200,000 43.9
 constexpr int64_t kMostShared = 1 << 22;
+constexpr int64_t kMostUnits = (int64_t)1 << 30;   // of a launch: they are counted in 32 bits
 constexpr int kWholeShift = 30;           // one unit per segment: nothing is split
 constexpr int kGroups = 256;              // workgroups of a split launch: one per CU
 
@@ -154,7 +155,7 @@ __device__ __forceinline__ Plan plan_of(const Args<LISTS>& p, const SplitArgs& s
   return s;
 }
 
-// The launch bounds the units of all requests by 2^30.
+// The launch bounds the units of all requests by kMostUnits.
 __device__ __forceinline__ int units_of(const SplitArgs& sp, const Plan& s, int Hk) {
   return (sp.line_shift > 0 ? 1 : s.segs) * Hk * s.chunks;
 }
@@ -1253,9 +1254,10 @@ bool one_group_each(int64_t longest, int64_t sum, int heads, int64_t position_by
 // drafts of 6 heads over up to 8,191 positions, D = 256, 34.1 and 31.5 us, 64 x 4 over 8,192 81.3 and 78.3; 64 requests of
 // up to 2,000, 8 heads of 128, 22.8 and 21.1 (4 of 256 22.2 and 22.6), of up to 16,384 94.0 and 93.3. Where the rule leaves
 // it out, 1 x 4 over 8,191, it was 15.9 and 17.3.
+// Nor where all segments' units would not fit kMostUnits, however many positions one holds.
 inline int fixed_part(int tiles, int64_t segments, int64_t positions, int64_t rows, int64_t groups) {
-  const int64_t units = positions * ((rows + tiles * kRows - 1) / (tiles * kRows)) >> kChunkShift;
-  return segments * 8 >= groups && units >= 2 * groups ? tiles : 0;
+  const double units = (double)positions * (double)((rows + tiles * kRows - 1) / (tiles * kRows)) / (1 << kChunkShift);
+  return segments * 8 >= groups && units >= 2.0 * (double)groups && segments * (1 + tiles) <= kMostUnits ? tiles : 0;
 }
 
 template <int FMT, int D, int TILES, bool LISTS, bool WIDE>
@@ -1292,7 +1294,7 @@ hipError_t launch_attn_d(const Args<LISTS>& p, void* workspace, hipStream_t stre
     sp.chunk_shift = 5;
     sp.whole = 1;
     sp.more = (FMT == kE2M1 ? kSegmentBytes4 : kSegmentBytes) / (32 * 2 * Shape<FMT, D, 4>::kRow);
-    while (segments * ((cap >> sp.chunk_shift) + 1 + sp.more) > ((int64_t)1 << 30)) ++sp.chunk_shift;
+    while (segments * ((cap >> sp.chunk_shift) + 1 + sp.more) > kMostUnits) ++sp.chunk_shift;
   } else {
     static_assert(FMT == kE2M1 || split_groups<FMT, D, 1>() == (D == 64 ? split_groups<FMT, 64, 1>() : kGroups),
                   "see attn_workspace_bytes");
@@ -1302,7 +1304,7 @@ hipError_t launch_attn_d(const Args<LISTS>& p, void* workspace, hipStream_t stre
     sp.part_rows = few ? kRows : part_rows(p.rows.N, p.group);
     sp.chunk_shift = kChunkShift;
     if constexpr (FMT == kE2M1) sp.more = fixed_part(few ? 1 : kTiles, segments, p.sum_len * p.cache.Hk, most, groups);
-    while (segments * ((cap >> sp.chunk_shift) + 1 + sp.more) > ((int64_t)1 << 30)) ++sp.chunk_shift;
+    while (segments * ((cap >> sp.chunk_shift) + 1 + sp.more) > kMostUnits) ++sp.chunk_shift;
     // notes by segment where there are fewer segments than workgroups
     const int64_t segs = (most + seg_rows - 1) / seg_rows;
     notes = segs * p.rows.R * p.cache.Hk;
