@@ -449,6 +449,7 @@ int gdn_kv_bounds(const gdn_kv_params* p, const gdn_kv_tensors* t, const gdn_kv_
   if (N < 0 || R < 0 || p->num_q_heads != 0 || p->rotary_dim != 0) return GDN_ERR_SHAPE;
   if (p->q_stride != 0 || p->k_stride != 0 || p->v_stride != 0) return GDN_ERR_SHAPE;
   if (2 * Hk * D > std::numeric_limits<int32_t>::max()) return GDN_ERR_SHAPE;
+  if (R > std::numeric_limits<int32_t>::max() - 63) return GDN_ERR_SHAPE;   // a wave's lanes share the requests, in 32 bits
   if (R == 0) return N == 0 ? GDN_OK : GDN_ERR_SHAPE;
   st = check_cache(c, true);
   if (st != GDN_OK) return st;

@@ -299,7 +299,7 @@ int gdn_attn_workspace_bytes(const gdn_attn_params* params, const gdn_kv_cache* 
  * the rows (k, v, q, q_out, positions and inv_freq are not read). bounds: device, io,
  * disjoint from the cache. No page may hold tokens of two requests of one call (with
  * mirrors that show it, GDN_ERR_ALIAS). (N / page_size + 2 R) Hk, and N Hk where that is
- * less, is below 2^31, else GDN_ERR_SHAPE. Errors as gdn_kv_read. */
+ * less, is below 2^31, and R at most 2^31 - 64, else GDN_ERR_SHAPE. Errors as gdn_kv_read. */
 int gdn_kv_bounds(const gdn_kv_params* params, const gdn_kv_tensors* tensors, const gdn_kv_cache* cache, void* bounds,
                   void* stream);
 

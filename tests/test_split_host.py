@@ -1,9 +1,11 @@
-"""Host: the attention's split of very many requests' lengths into units of work.
+"""Host: very many requests in a call: the attention's split of their lengths into units of work, and what
+gdn_kv_bounds takes.
 
 No call here launches a kernel (there is no GPU to launch it on), and the module runs only where none is visible.
 """
 from __future__ import annotations
 
+import ctypes
 import os
 import subprocess
 import sys
@@ -48,3 +50,14 @@ def test_more_segments_than_units_can_count_twice():
     r = subprocess.run([sys.executable, "-c", CALL], cwd=root, capture_output=True, text=True, timeout=60)
     assert r.returncode == 0, r.stderr
     assert int(r.stdout.split()[-1]) == gdn.GDN_ERR_HIP
+
+
+@pytest.mark.parametrize("R,status", [((1 << 31) - 1, gdn.GDN_ERR_SHAPE), ((1 << 31) - 63, gdn.GDN_ERR_SHAPE), ((1 << 31) - 64, gdn.GDN_ERR_HIP)])
+def test_as_many_requests_as_bounds_can_count(R, status):
+    """Past 2^31 - 64 the requests of a lane would pass 32 bits (and no page's bounds be written); below, the call ends here
+    for want of a device."""
+    at = [(i + 1) << 42 for i in range(7)]
+    cache = gdn.GdnKvCache(at[0], at[1], None, None, at[2], None, 1000, 16, 1, 1, 64, gdn.GDN_F16, gdn.CACHE_IO)
+    params = gdn.GdnKvParams(1, R, 0, 0, 0, 0.0, 0, 0, 0)
+    tensors = gdn.GdnKvTensors(None, None, at[3], None, at[4], None, None, None, None, None)
+    assert gdn.lib().gdn_kv_bounds(ctypes.byref(params), ctypes.byref(tensors), ctypes.byref(cache), at[5], None) == status
