@@ -105,9 +105,10 @@ def select(q, page_bounds, page_table, page_size, cu_seqlens, seq_lens, K, first
     return lists, counts, gaps
 
 
-def sparse_attention(q, k_pages, v_pages, page_table, cu_seqlens, seq_lens, lists, counts=None, scale=None):
+def sparse_attention(q, k_pages, v_pages, page_table, cu_seqlens, seq_lens, lists, counts=None, scale=None, rounded_weights=True):
     """(out, bound): attention of every token over the positions up to its own of the listed entries of its
-    request's page table; an entry listed twice counts twice. bound as AO.attention's, weights taken at 2^-11."""
+    request's page table; an entry listed twice counts twice. bound as AO.attention's, with weights taken at 2^-11 of
+    each and 2^-25 of the largest where they are rounded to FP16 (rounded_weights)."""
     q = np.asarray(q, np.float64)
     N, Hq, D = q.shape
     P, Hk, ps, _ = k_pages.shape
@@ -133,7 +134,9 @@ def sparse_attention(q, k_pages, v_pages, page_table, cu_seqlens, seq_lens, list
                 p = w / w.sum(-1, keepdims=True)
                 A = p @ np.abs(v)
                 size = scale * (np.abs(qr) @ np.abs(k).T).max(-1, keepdims=True)
-                rel = 2 * (D + 2) * u * size + 4 * u * np.abs(s).max(-1, keepdims=True) + 2 * (L + 8) * u + 2.0 ** -22 + 2.0 ** -11
+                rel = 2 * (D + 2) * u * size + 4 * u * np.abs(s).max(-1, keepdims=True) + 2 * (L + 8) * u + 2.0 ** -22
                 out[n, h * G:(h + 1) * G] = p @ v
-                bound[n, h * G:(h + 1) * G] = A * rel + 2.0 ** -25 * np.abs(v).sum(0) / w.sum(-1, keepdims=True)
+                bound[n, h * G:(h + 1) * G] = A * rel
+                if rounded_weights:
+                    bound[n, h * G:(h + 1) * G] += A * 2.0 ** -11 + 2.0 ** -25 * np.abs(v).sum(0) / w.sum(-1, keepdims=True)
     return out, bound
