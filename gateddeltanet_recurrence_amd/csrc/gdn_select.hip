@@ -27,7 +27,6 @@ constexpr int kWaves = kThreads / 64;
 // 1,024: they walk what is left.
 constexpr int64_t kMostBlocks = (int64_t)1 << 21;
 
-typedef uint32_t uint2_t __attribute__((ext_vector_type(2)));
 typedef uint32_t uint4_t __attribute__((ext_vector_type(4)));
 
 // Request that token n < the requests' tokens belongs to, found by a whole wave.
@@ -609,8 +608,6 @@ __global__ void __launch_bounds__(kThreads) gdn_attn_select_k(SelectArgs p) {
     }
     if (!in_lds)
       pick<kWaves, 0, true>(p, keys, t.held, list, count, shared);
-    else if (t.held > kFew)
-      pick<kWaves, kColumns, true>(p, lds_keys, t.held, list, count, shared);
     else if (threadIdx.x < 64)
       pick<1, kColumns, false>(p, lds_keys, t.held, list, count, shared);
     __syncthreads();
@@ -716,19 +713,18 @@ hipError_t launch_bounds_io(const BoundsArgs& p, hipStream_t stream) {
   }
 }
 
-constexpr int kMostLds = kFew * kWaves;   // keys of a list in LDS: what its workgroup's waves hold
-
 // One launch where lists are short and few, so that their latency counts, two where they are split over workgroups or
 // fill the device anyway. Measured, one against two, 8 key heads of 128 fp16 (bounds of 512 bytes): a request of 64
 // pages 5.6 and 7.5 us, 64 of them 9.3 and 11.5, 256 of them 27.7 and 22.6; 64 of up to 256 pages 13.6 and 15.0; one
 // of 2,048 37 and 12, 16 of 1,024 28 and 22, 64 of 512 36 and 39.
 constexpr int kShort = 256, kFewLists = 1024;
+static_assert(kShort <= kFew, "a list in LDS is one wave's to pick from");
 
 template <typename IO, int D>
 hipError_t launch_select_d(SelectArgs p, hipStream_t stream) {
   const int64_t lists = (int64_t)p.rows.N * p.cache.Hk;
-  p.lds_entries = p.max_held < kMostLds ? p.max_held : kMostLds;
   if (p.max_held <= kShort && lists <= kFewLists) {
+    p.lds_entries = p.max_held;
     hipLaunchKernelGGL((gdn_attn_select_k<IO, D>), dim3(blocks_of(lists)), dim3(kThreads), p.lds_entries * sizeof(uint64_t),
                        stream, p);
     return hipGetLastError();
