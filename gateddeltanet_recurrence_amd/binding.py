@@ -838,6 +838,9 @@ class KVCache:
     page_table_host an optional host mirror, checked on every call: a contiguous int32
     array or CPU tensor is read in place, so that a program can change it along with
     page_table; anything else is copied once, here.
+
+    format is CACHE_IO, CACHE_E4M3 or CACHE_E2M1 (e4m3: whether it is the second; a 4-bit
+    cache has scales, too), io_dtype the type of q, k, v and outputs.
     """
 
     def __init__(self, k_pages, v_pages, page_table, *, k_scales=None, v_scales=None, page_table_host=None):
