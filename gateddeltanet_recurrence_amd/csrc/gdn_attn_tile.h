@@ -41,12 +41,13 @@
 //
 // 4-bit pages (GDN_CACHE_E2M1) have a scale per 32 elements, applied by the conversion to FP16, exactly: about 200 vector
 // instructions for 32 positions of 128 columns, 64 of them conversions. More waves a SIMD hide more than more tiles in
-// flight a wave do (see kMostAhead). 64 requests of up to 16,384, D = 128, 491 MB, 90 to 93 us (5.3 to 5.4 TB/s; its loop
-// alone 6.4); 16 x up to 4 drafts over up to 8,191 positions, D = 256, 75 MB, 31.5 us, of which about 20 are the loop.
+// flight a wave do (see kMostAhead). 64 requests of up to 16,384, D = 128, 491 MB, 89 to 93 us (5.3 to 5.5 TB/s; its loop
+// alone 6.4); 16 x up to 4 drafts over up to 8,191 positions, D = 256, 75 MB, 31.9 us, of which about 20 are the loop.
+// Their M is the largest q.k itself: scale log2(e) and the lift are applied to a score's distance from it.
 //
 // LISTS: the positions of a token and key head are those of its listed pages, each list a segment of its own: 64 requests
 // x 8 key heads x 32 pages of 64, D = 128 fp16, 530 MB, 86 to 90 us (5.9 to 6.2 TB/s, HBM); 2 drafts x 65 pages, D = 256
-// in 4 bits, 13.7 us (latency, the join's 4 us among it).
+// in 4 bits, 13.6 us (latency, the join's 4 us among it).
 #pragma once
 
 #include <type_traits>
@@ -891,7 +892,9 @@ __global__ void __launch_bounds__(64 * WAVES, 1) gdn_attn_k(Args<LISTS> p, Split
           float m = xs[r][0];
           if constexpr (FMT == kE2M1) {
             // NaN where one is, which takes fewer instructions; M stays then, and l shows the NaN. M is a score as it is
-            // here: its distance to another is exact where they are near, however large they are.
+            // here: its distance to another is exact where they are near, however large they are. (Score times factor less
+            // a rounded M in one instruction is 0.3 % of a decode step and 1 % of drafts faster, but then M's rounding is
+            // not the scores': weights of scores from 2^26 on left fp16's range.)
 #pragma unroll
             for (int i = 1; i < S::kPos; ++i) m = __builtin_elementwise_maximum(m, xs[r][i]);
             m = __builtin_elementwise_maximum(row_maximum(m), M[r]);

@@ -8,8 +8,8 @@
 //
 // Both are bound by the latency of lengths -> table -> keys or bounds, and the selection by its 64-bit sums too.
 // Measured: bounds of 64 new tokens, 8 key heads of 128 fp16, pages of 64, 3.7 us (a launch); of prompts of 28,746 tokens,
-// 4 of 256 in 8 bits, 31 MB, 10.5 us. Selection for 64 requests x 8 key heads, 32 of up to 256 pages, 30 MB, 13.7 us
-// (about 11 the scores, 3 the list); 3 drafts x 4 key heads of 256 fp32, 128 of 4,097 pages, 34 MB, 26 us.
+// 4 of 256 in 8 bits, 31 MB, 10.5 us. Selection for 64 requests x 8 key heads, 32 of up to 256 pages, 30 MB, 13.6 us
+// (about 11 the scores, 3 the list); 3 drafts x 4 key heads of 256 fp32, 128 of 4,097 pages, 34 MB, 25.6 us.
 #include <type_traits>
 
 #include "gdn_attn_kernels.h"
@@ -716,7 +716,10 @@ hipError_t launch_bounds_io(const BoundsArgs& p, hipStream_t stream) {
 // One launch where lists are short and few, so that their latency counts, two where they are split over workgroups or
 // fill the device anyway. Measured, one against two, 8 key heads of 128 fp16 (bounds of 512 bytes): a request of 64
 // pages 5.6 and 7.5 us, 64 of them 9.3 and 11.5, 256 of them 27.7 and 22.6; 64 of up to 256 pages 13.6 and 15.0; one
-// of 2,048 37 and 12, 16 of 1,024 28 and 22, 64 of 512 36 and 39.
+// of 2,048 37 and 12, 16 of 1,024 28 and 22. Between 256 and 512 pages few lists gain by two launches and many lose: of
+// 300 pages one request 10.4 and 9.1, 4 10.6 and 9.5, 16 13.5 and 14.4, 64 20.0 and 23.5, 128 41 and 47; of 512 13.2 and
+// 10.2, 13.3 and 10.6, 16.9 and 18.4, 32.3 and 39.5, 59 and 71. A length alone does not tell these apart; kShort is for
+// the few.
 constexpr int kShort = 256, kFewLists = 1024;
 static_assert(kShort <= kFew, "a list in LDS is one wave's to pick from");
 

@@ -336,7 +336,10 @@ typedef struct gdn_select_tensors {
  * last bits. pages[n, h] is the selected i's in ascending order, -1 behind them, and
  * counts[n] their number, min(K, the entries there are), for every h. Tokens behind the
  * last request's are left as they are. The cache's k_pages, v_pages and scales are not read.
- * The workspace is as in gdn_attn_forward, of gdn_attn_select_workspace_bytes() bytes.
+ * The workspace is as in gdn_attn_forward, of gdn_attn_select_workspace_bytes() bytes: 8
+ * for each of N Hk max_pages entries, so that a long prompt is better taken in several
+ * calls (4,096 tokens x 8 heads x 2,048 pages in one: 512 MiB), each with the tokens'
+ * part of q, pages and counts and seq_lens up to its last token.
  * N Hk max_pages is at most 2^40, else GDN_ERR_SHAPE.
  * Errors: GDN_ERR_NULL, GDN_ERR_SHAPE, GDN_ERR_DTYPE, GDN_ERR_CAPACITY,
  * GDN_ERR_WORKSPACE, GDN_ERR_ALIAS. */
