@@ -112,3 +112,26 @@ def test_the_largest_of_far_scores(lists, size, length, D, G):
         want, A = top.mean(0), np.abs(top).mean(0)
         tol = A * (2.0 ** -18 + 2 * (length + 8) * 2.0 ** -24)
         assert_within(got[0, g], want, tol + half_step("e2m1", np.abs(want) + tol), f"size={size} row {g}")
+
+
+@pytest.mark.parametrize("lists", [False, True])
+@pytest.mark.parametrize("length,new", [(1, 1), (50, 1), (50, 4), (700, 3), (6000, 2)])
+def test_a_row_without_a_finite_score_is_zero_and_alone(lists, length, new):
+    """Scores that are all -inf give zeros, whatever the values; other rows of the same tile are as without it, and a NaN
+    in q is its row's."""
+    _case(f"scores of -inf lists={lists} length={length} new={new}")
+    D, G = 64, 4
+    c = make_cache4([length], Hk=1, D=D, page=16, seed=140)
+    pos = np.arange(length)
+    page, slot = c["table"][0, pos // 16], pos % 16
+    byte = c["k_codes"][page, 0, slot, 1]
+    c["k_codes"][page, 0, slot, 1] = (byte & 15) | 0xf0      # channel 3 below zero, at its block's scale
+    c["k_scales"][page, 0, 0, slot] = np.maximum(c["k_scales"][page, 0, 0, slot], 110)
+    cu, q = cu_of([new]), queries(new, G, D, "f16", 141)
+    clean = _run(c, q, cu, lists)
+    q[:, 1, 3], q[:, 2, 7] = np.inf, np.nan
+    got = _run(c, q, cu, lists)
+    assert (got[:, 1] == 0).all() and np.isnan(got[:, 2]).all()
+    assert np.array_equal(got[:, [0, 3]], clean[:, [0, 3]])
+    c["v_scales"][page[0], 0, 1, slot[0]] = 255
+    assert (_run(c, q, cu, lists)[:, 1] == 0).all()
